@@ -1,0 +1,114 @@
+// Activations as sums of float6 parts, and 1-bit weights as float4 +-1: the
+// operands of v_mfma_scale_f32_*_f8f6f4, which multiplies float4 by float6
+// at twice the rate of float8 (measured here 9.2 against 4.9 PFLOP/s with
+// independent accumulators, 16-bit operands 2.4).
+//
+// Parts.  Per block of 32 positions of one token, with f the biased exponent
+// of its largest |x| and e = max(f - 2, 12), y = x 2^(127 - e) lies below 8
+// in magnitude; p0 = fp6(y), p1 = fp6(16 (y - p0)), p2 = fp6(16 (16 (y - p0)
+// - p1)), ... (E2M3: 4 significant bits up to 7.5, step 1/8 below 2; every
+// remainder is exact in float32), and part p carries the power of two
+// e - 4 p as its hardware scale, which is what the one exponent byte per
+// block holds.  NP = 3 parts keep a value to 2^-14 of its block's largest
+// one (and exactly, when it is a bfloat16 above 2^-6 or a float16 above 2^-3
+// of it): the rounding of a sum of K of them stays 20 times below that of a
+// 16-bit result (measured 1e-5 of the result for Gaussian bfloat16, 3e-5 for
+// float16, 8e-5 with one value in a hundred 20 times the others).  Float32
+// results take NP = 4 (2^-18 of the block's largest; measured 2e-7, 6e-7 and
+// 1.2e-6).  The products with +-1 are exact and are summed in float32.  A
+// block with an infinity or a NaN has e = 255, which the matrix cores read
+// as NaN: its token's results are all NaN.
+//
+// Image.  A token's positions come in groups of 4 H blocks (H = 2 for the
+// 32 x 32 x 64 instruction, H = 4 for the 16 x 16 x 128 one); lane group h
+// holds block 4 h + u of the group at step u < 4, so that its four sign
+// words of the group are one 16-byte load.  Per token and group:
+//   [u][part][h] the first 16 bytes of an operand (24 bytes, 32 x 6 bits),
+//   [u][part][h] its last 8, then [h] the four exponent bytes (u = byte).
+// A group takes 96 H NP + 16 bytes, an odd number of 16-byte chunks, so
+// rows of groups in LDS start in different banks.  Element 8 q + t of a
+// block is its position 4 t + q: the order in which three shifts and four
+// bit selects turn a sign word into float4 +-1 (expand_signs).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace lq {
+namespace f6 {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned u32x6 __attribute__((ext_vector_type(6)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x32 __attribute__((ext_vector_type(32)));
+
+constexpr int kPadPositions = 512;      // images cover whole multiples of this, zero past K
+
+constexpr int group_positions(int H) { return 128 * H; }
+constexpr int group_bytes(int H, int NP) { return 96 * H * NP + 16; }
+// Offsets of a group's three sections.
+constexpr int tail_offset(int H, int NP) { return 64 * H * NP; }
+constexpr int exp_offset(int H, int NP) { return 96 * H * NP; }
+
+inline int64_t padded_positions(int64_t K) {
+  return (K + kPadPositions - 1) / kPadPositions * kPadPositions;
+}
+inline int64_t row_bytes(int64_t K, int H, int NP) {
+  return padded_positions(K) / group_positions(H) * group_bytes(H, NP);
+}
+
+// A per-lane value that the compiler keeps in a vector register.
+__device__ __forceinline__ uint32_t held(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// A word of 32 sign bits as float4: a set bit gives -1.0 (0xA), a clear one
+// +1.0 (0x2), so products hold -sigma and the epilogue multiplies by -s.
+// Three shifts and four bit-field inserts; two = held(0x22222222).
+__device__ __forceinline__ i32x8 expand_signs(uint32_t w, uint32_t two) {
+  const uint32_t m = 0x88888888u;
+  i32x8 a;
+  a[0] = static_cast<int>(((w << 3) & m) | (two & ~m));
+  a[1] = static_cast<int>(((w << 2) & m) | (two & ~m));
+  a[2] = static_cast<int>(((w << 1) & m) | (two & ~m));
+  a[3] = static_cast<int>((w & m) | (two & ~m));
+  a[4] = a[5] = a[6] = a[7] = 0;         // unused with a float4 operand
+  return a;
+}
+
+// Scale byte of a block from the bits of its largest |x|.
+__device__ __forceinline__ uint32_t block_exponent(uint32_t largest) {
+  const int f = static_cast<int>(largest >> 23);
+  return f == 255 ? 255u : static_cast<uint32_t>(max(f - 2, 12));
+}
+
+// The parts of a block of 32 values (x in position order), whose scale byte
+// is e.
+template <int NP>
+__device__ __forceinline__ void split_block(const float (&x)[32], uint32_t e, u32x6 (&part)[NP]) {
+  f32x16 even, odd;                      // elements 0, 2, 4, ... and 1, 3, 5, ...
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    even[i] = x[4 * ((2 * i) & 7) + (2 * i) / 8];
+    odd[i] = x[4 * ((2 * i + 1) & 7) + (2 * i + 1) / 8];
+  }
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const float scale = __uint_as_float((e - 4u * p) << 23);
+    part[p] = __builtin_amdgcn_cvt_scalef32_2xpk16_fp6_f32(even, odd, scale);
+    if (p + 1 < NP) {
+      const f32x32 back = __builtin_amdgcn_cvt_scalef32_pk32_f32_fp6(part[p], scale);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        even[i] -= back[2 * i];
+        odd[i] -= back[2 * i + 1];
+      }
+    }
+  }
+}
+
+}  // namespace f6
+}  // namespace lq

@@ -1,0 +1,87 @@
+// 16-bit lifted activations into the float6-part operand image of the
+// products in k_gemm_f6.hip and k_gemv_f6.hip (layout and arithmetic in
+// f6_parts.h).  One thread per (token, block of 32 positions): four 16-byte
+// loads, the block's exponent, the parts (one conversion instruction each),
+// one 16-byte and one 8-byte store per part.  `zero_row`: one more row of zeros
+// follows the last (what a gathered row with an index out of range reads).
+#include "f6_parts.h"
+#include "lq_internal.h"
+
+namespace lq {
+namespace {
+
+using namespace f6;
+
+template <int DT, int H, int NP>
+__global__ void __launch_bounds__(256) f6_image_kernel(const uint16_t* __restrict__ a, int64_t rows,
+                                                       int64_t zero_row, int K, int64_t lda, int blocks,
+                                                       uint8_t* __restrict__ img) {
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = idx / blocks;
+  if (row >= rows) return;
+  const int b = static_cast<int>(idx - row * blocks);
+  float x[32];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k = 32 * b + 8 * j;               // K % 8 == 0: a chunk is all in or out
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (k < K && row != zero_row) v = *reinterpret_cast<const uint4*>(a + row * lda + k);
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (DT == LQ_BF16) {
+        x[8 * j + 2 * i] = __uint_as_float(q[i] << 16);
+        x[8 * j + 2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+      } else {
+        x[8 * j + 2 * i] = f16_bits_to_float(static_cast<uint16_t>(q[i]));
+        x[8 * j + 2 * i + 1] = f16_bits_to_float(static_cast<uint16_t>(q[i] >> 16));
+      }
+    }
+  }
+  uint32_t largest = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) largest = max(largest, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  const uint32_t e = block_exponent(largest);
+  u32x6 part[NP];
+  split_block<NP>(x, e, part);
+  const int per = 4 * H;                        // blocks per group
+  const int c = b / per, r = b % per, h = r / 4, u = r % 4;
+  uint8_t* g = img + (row * (blocks / per) + c) * group_bytes(H, NP);
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int at = (u * NP + p) * H + h;
+    *reinterpret_cast<uint4*>(g + 16 * at) =
+        make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+    *reinterpret_cast<uint2*>(g + tail_offset(H, NP) + 8 * at) = make_uint2(part[p][4], part[p][5]);
+  }
+  g[exp_offset(H, NP) + 4 * h + u] = static_cast<uint8_t>(e);
+}
+
+template <int H, int NP>
+hipError_t launch(const void* a, lq_dtype dt, int64_t rows, bool zero_row, int64_t K, int64_t lda,
+                  void* img, hipStream_t st) {
+  const int blocks = static_cast<int>(padded_positions(K) / 32);
+  const int64_t all = rows + zero_row;
+  const int64_t grid = (all * blocks + 255) / 256;
+  const auto* p = static_cast<const uint16_t*>(a);
+  if (dt == LQ_BF16)
+    f6_image_kernel<LQ_BF16, H, NP><<<dim3(static_cast<uint32_t>(grid)), 256, 0, st>>>(
+        p, all, zero_row ? rows : -1, static_cast<int>(K), lda, blocks, static_cast<uint8_t*>(img));
+  else
+    f6_image_kernel<LQ_F16, H, NP><<<dim3(static_cast<uint32_t>(grid)), 256, 0, st>>>(
+        p, all, zero_row ? rows : -1, static_cast<int>(K), lda, blocks, static_cast<uint8_t*>(img));
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_f6_image(const void* a, lq_dtype dt, int64_t rows, bool zero_row, int64_t K,
+                           int64_t lda, int H, int NP, void* img, hipStream_t st) {
+  if (H == 2)
+    return NP == 3 ? launch<2, 3>(a, dt, rows, zero_row, K, lda, img, st)
+                   : launch<2, 4>(a, dt, rows, zero_row, K, lda, img, st);
+  return NP == 3 ? launch<4, 3>(a, dt, rows, zero_row, K, lda, img, st)
+                 : launch<4, 4>(a, dt, rows, zero_row, K, lda, img, st);
+}
+
+}  // namespace lq

@@ -1,0 +1,350 @@
+// Product of 1-bit weights with 16-bit lifted activations for many tokens,
+// on the matrix cores in float4 (signs) x float6 (activation parts,
+// f6_parts.h), with the epilogue of lq_gemm_ep and the ragged expert runs of
+// lq_gemm_grouped.
+//
+// Tile.  A workgroup of 8 waves takes 128 WR rows of the weights and 32 TT
+// tokens; the weights cost 1/8 byte per position and the parts 2.3, so the
+// tile is tall.  WK = 8 / WR waves share each 128-row strip and split the
+// positions of a stage; every wave holds 128 rows x 32 TT tokens of sums
+// (4 TT tiles of 32 x 32) and uses each operand it reads from LDS four times.
+// A stage is SG groups of 256 positions (SG = 2 for WR = 1, so that each of
+// the eight waves has a step), copied to LDS by loads that write it directly
+// (buffer_load ... lds, 16 bytes per lane): the tokens' rows of parts, then
+// 32 bytes of signs per row and group.  A ring of S stages; a wave reads an
+// operand of the next step into the registers of the one it has just used,
+// so the only wait in the loop is the stage barrier, which sits behind the
+// first products of a step.
+//
+// The loads to LDS are inline assembly (they have no output register) so
+// that the waits on them can be counted by hand: the compiler would drain
+// them before every read of LDS.  Every wave issues the same number per
+// stage (the last ones repeat a chunk).
+//
+// End.  The tiles go through LDS, 32 tokens at a time, where the WK partial
+// sums are added in a fixed order and rows become consecutive, so stores are
+// whole runs.
+#include "f6_epilogue.h"
+#include "f6_parts.h"
+#include "f6_product.h"
+#include "lq_internal.h"
+
+namespace lq {
+namespace {
+
+using namespace f6;
+
+constexpr uint32_t kRsrcWord3 = 0x00020000u;
+
+__device__ __forceinline__ f32x16 mfma(const i32x8& a, const i32x8& b, const f32x16& c, int scale) {
+  // A: E2M1 (cbsz 4), scale 2^0; B: E2M3 (blgp 2), scale 2^(scale - 127)
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 4, 2, 0, 127, 0, scale);
+}
+
+// 64 lanes x 16 bytes from resource r at voff + soff to LDS at `lds` (bytes).
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t voff, const i32x4& r,
+                                            uint32_t soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+      : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+__device__ __forceinline__ i32x4 resource(const void* p, uint32_t bytes) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  i32x4 r;
+  r[0] = __builtin_amdgcn_readfirstlane(static_cast<int>(u));
+  r[1] = __builtin_amdgcn_readfirstlane(static_cast<int>(u >> 32) & 0xFFFF);
+  r[2] = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes));
+  r[3] = static_cast<int>(kRsrcWord3);
+  return r;
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+template <int NP, int WR, int TT>
+struct Shape {
+  static constexpr int WK = 8 / WR;
+  static constexpr int SG = WR == 1 ? 2 : 1;
+  static constexpr int NU = 4 * SG / WK;               // steps of a wave per stage
+  static constexpr int TOK = 32 * TT;
+  static constexpr int ROWS = 128 * WR;
+  static constexpr int GB = group_bytes(2, NP);
+  static constexpr int CH = GB / 16;
+  static constexpr int IMG_CHUNKS = SG * TOK * CH;
+  static constexpr int IMG_LOADS = (IMG_CHUNKS + 63) / 64;
+  static constexpr int W_LOADS = SG * ROWS * 2 / 64;
+  static constexpr int LOADS = (IMG_LOADS + W_LOADS + 7) / 8;   // per wave and stage
+  static constexpr int STAGE = (IMG_LOADS + W_LOADS) * 1024;
+  static constexpr int RING = 163840 / STAGE;
+  static constexpr int S = RING > 4 ? 4 : RING;
+  static constexpr int PITCH = 132;                    // floats per token in the final exchange
+  static constexpr int EXCHANGE = 8 * 32 * PITCH * 4;
+  static constexpr int LDS = S * STAGE > EXCHANGE ? S * STAGE : EXCHANGE;
+  static_assert(S >= 2 && LDS <= 163840);
+  static_assert((S - 1) * LOADS < 64);
+};
+
+template <int NP, int WR, int TT>
+__global__ void __launch_bounds__(512, 2) gemm_f6_kernel(F6Product a) {
+  using P = Shape<NP, WR, TT>;
+  constexpr int WK = P::WK, SG = P::SG, NU = P::NU, TOK = P::TOK, ROWS = P::ROWS;
+  extern __shared__ __align__(1024) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = uniform(tid >> 6);
+  const int wr = wave % WR, wk = wave / WR;
+
+  // ---- which tile: token tiles in pairs, the rows inside, so that the
+  // workgroups of an XCD (every eighth block) share parts and signs in its L2
+  const int RT = a.row_tiles;
+  int tiles = a.token_tiles;
+  if (a.offsets) {
+    tiles = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 64) tiles += uniform(wave_total(run_tiles(a, e0 + lane, TOK)));
+  }
+  const int total = tiles * RT;
+  const int chunk = (total + 7) / 8;
+  const int at = static_cast<int>(blockIdx.x & 7) * chunk + static_cast<int>(blockIdx.x >> 3);
+  if (static_cast<int>(blockIdx.x >> 3) >= chunk || at >= total) return;
+  const int pair = at / (2 * RT), in = at - pair * 2 * RT;
+  const int wide = min(2, tiles - 2 * pair);
+  int tile = 2 * pair + in % wide;
+  const int rt = in / wide;
+  int expert = 0, row0 = tile * TOK, row_end = a.R;
+  if (a.offsets) find_run(a, tile, TOK, lane, expert, row0, row_end);
+  const int tokens = min(TOK, row_end - row0);
+
+  const uint32_t* w = a.w + static_cast<int64_t>(expert) * a.m * a.ldw;
+  const float* s = a.s + static_cast<int64_t>(expert) * a.m;
+  const float* bias = a.bias ? a.bias + static_cast<int64_t>(expert) * a.m : nullptr;
+  const int half_m = a.m / 2;
+  const int outs = a.gated ? ROWS / 2 : ROWS;          // outputs of the tile
+  const int out0 = rt * outs;
+  const int out_m = a.gated ? half_m : a.m;
+
+  // ---- sources of this wave's loads: loads wave, wave + 8, ... of a stage
+  const i32x4 ires = resource(a.img, a.img_bytes);
+  const i32x4 wres = resource(w, static_cast<uint32_t>(a.m) * a.ldw * 4u);
+  uint32_t src[P::LOADS];
+  i32x4 from[P::LOADS];
+#pragma unroll
+  for (int i = 0; i < P::LOADS; ++i) {
+    const int l = min(wave + 8 * i, P::IMG_LOADS + P::W_LOADS - 1);
+    from[i] = l < P::IMG_LOADS ? ires : wres;
+    if (l < P::IMG_LOADS) {
+      const int c = min(l * 64 + lane, P::IMG_CHUNKS - 1);
+      const int sg = c / (TOK * P::CH), t = c / P::CH % TOK, ch = c % P::CH;
+      int r = row0 + min(t, tokens - 1);
+      if (a.rows) {
+        r = a.rows[r];
+        r = r < 0 || r >= a.src_rows ? a.src_rows : r;   // the image's row of zeros
+      }
+      src[i] = static_cast<uint32_t>(r) * a.img_row_bytes + sg * P::GB + ch * 16;
+    } else {
+      const int c = (l - P::IMG_LOADS) * 64 + lane;
+      const int sg = c / (2 * ROWS), lr = c / 2 % ROWS, h = c & 1;
+      int row;
+      if (a.gated)
+        row = min(out0 + lr / 128 * 64 + (lr & 63), half_m - 1) + ((lr >> 6) & 1) * half_m;
+      else
+        row = min(out0 + lr, a.m - 1);
+      src[i] = static_cast<uint32_t>(row) * a.ldw * 4u + sg * 32 + h * 16;
+    }
+  }
+  const int stages = a.groups / SG;
+  auto issue = [&](int stage, int slot) {
+    stage = min(stage, stages - 1);                    // past the end: a slot nobody reads
+#pragma unroll
+    for (int i = 0; i < P::LOADS; ++i) {
+      const int l = min(wave + 8 * i, P::IMG_LOADS + P::W_LOADS - 1);
+      const uint32_t to = lds_address(lds) + slot * P::STAGE + l * 1024;
+      load_to_lds(to, src[i], from[i], stage * SG * (l < P::IMG_LOADS ? P::GB : 32));
+    }
+  };
+
+  // ---- operands
+  const int i32 = lane & 31, h = lane >> 5;
+  const uint32_t two = held(0x22222222u);
+  f32x16 acc[4][TT] = {};
+  i32x8 b[TT][NP];
+  uint32_t word[4], ex[TT];
+  auto step_group = [&](int u) { return SG == 2 ? wk >> 2 : 0; };
+  auto step_u = [&](int u) { return SG == 2 ? wk & 3 : wk * NU + u; };
+  auto read_part = [&](int slot, int u, int t, int p) {
+    const uint8_t* g = lds + slot * P::STAGE + step_group(u) * TOK * P::GB +
+                       (32 * t + i32) * P::GB;
+    const int at2 = (step_u(u) * NP + p) * 2 + h;
+    const int4 lo = *reinterpret_cast<const int4*>(g + 16 * at2);
+    const int2 hi = *reinterpret_cast<const int2*>(g + tail_offset(2, NP) + 8 * at2);
+    b[t][p][0] = lo.x; b[t][p][1] = lo.y; b[t][p][2] = lo.z; b[t][p][3] = lo.w;
+    b[t][p][4] = hi.x; b[t][p][5] = hi.y; b[t][p][6] = 0; b[t][p][7] = 0;
+  };
+  auto read_exponent = [&](int slot, int u, int t) {
+    const uint8_t* g = lds + slot * P::STAGE + step_group(u) * TOK * P::GB +
+                       (32 * t + i32) * P::GB + exp_offset(2, NP) + 4 * h;
+    ex[t] = *reinterpret_cast<const uint32_t*>(g) >> (8 * step_u(u)) & 255u;
+  };
+  auto read_words = [&](int slot, int u) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      word[q] = *reinterpret_cast<const uint32_t*>(
+          lds + slot * P::STAGE + P::IMG_LOADS * 1024 + step_group(u) * ROWS * 32 +
+          (wr * 128 + 32 * q + i32) * 32 + h * 16 + 4 * step_u(u));
+  };
+
+#pragma unroll
+  for (int i = 0; i < P::S; ++i) issue(i, i);
+  wait_and_barrier<(P::S - 1) * P::LOADS>();
+  read_words(0, 0);
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    read_exponent(0, 0, t);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) read_part(0, 0, t, p);
+  }
+
+  int slot = 0;
+  for (int stage = 0; stage < stages; ++stage) {
+    const int next = slot + 1 == P::S ? 0 : slot + 1;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const bool last = u == NU - 1;
+      const int nslot = last ? next : slot, nu = last ? 0 : u + 1;
+      i32x8 sign[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sign[q] = expand_signs(word[q], two);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const int e = static_cast<int>(ex[t]);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[q][t] = mfma(sign[q], b[t][p], acc[q][t], e - 4 * p);
+          if (t == 0 && p == 0) {
+            if (last) {
+              // the next stage has landed and nobody reads this one any more
+              wait_and_barrier<(P::S - 2) * P::LOADS>();
+              issue(stage + P::S, slot);
+            }
+            read_words(nslot, nu);
+          }
+          read_part(nslot, nu, t, p);
+        }
+        read_exponent(nslot, nu, t);
+      }
+    }
+    slot = next;
+  }
+  wait_and_barrier<0>();
+
+  // ---- the exchange: [wave][token][row], 32 tokens at a time
+  float* ex32 = reinterpret_cast<float*>(lds);
+  const int64_t esz = a.out_dt == LQ_F32 ? 4 : 2;
+  const bool wide_out = (reinterpret_cast<uint64_t>(a.out) | static_cast<uint64_t>(a.ldo * esz)) % (4 * esz) == 0 &&
+                        (!a.residual || (reinterpret_cast<uint64_t>(a.residual) |
+                                         static_cast<uint64_t>(a.ldr * esz)) % (4 * esz) == 0);
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    if (t) __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int r4 = 0; r4 < 4; ++r4)
+        *reinterpret_cast<float4*>(ex32 + (wave * 32 + i32) * P::PITCH + 32 * q + 8 * r4 + 4 * h) =
+            make_float4(acc[q][t][4 * r4], acc[q][t][4 * r4 + 1], acc[q][t][4 * r4 + 2],
+                        acc[q][t][4 * r4 + 3]);
+    __syncthreads();
+    const int quads = outs / 4;
+    for (int j = tid; j < 32 * quads; j += 512) {
+      const int tk = j / quads, o = (j - tk * quads) * 4;
+      const int token = 32 * t + tk;
+      const int n = min(4, out_m - (out0 + o));
+      if (token >= tokens || n <= 0) continue;
+      float y[4];
+      const int strip = a.gated ? o / 64 : o / 128, at0 = a.gated ? o % 64 : o % 128;
+      auto sum = [&](int row_in_strip, int64_t row, float (&z)[4]) {
+        float4 v = *reinterpret_cast<const float4*>(ex32 + (strip * 32 + tk) * P::PITCH + row_in_strip);
+#pragma unroll
+        for (int k = 1; k < WK; ++k) {
+          const float4 x = *reinterpret_cast<const float4*>(
+              ex32 + ((k * WR + strip) * 32 + tk) * P::PITCH + row_in_strip);
+          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+        }
+        const float raw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int64_t rr = row + min(c, n - 1);
+          z[c] = -raw[c] * s[rr] + (bias ? bias[rr] : 0.f);
+        }
+      };
+      sum(at0, out0 + o, y);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] = activate(y[c], a.act);
+      if (a.gated) {
+        float up[4];
+        sum(64 + at0, static_cast<int64_t>(half_m) + out0 + o, up);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] *= up[c];
+      }
+      const int64_t row = row0 + token;
+      finish4(y, n, wide_out, a.residual, row * a.ldr + out0 + o, a.out, row * a.ldo + out0 + o,
+              a.out_dt);
+    }
+  }
+}
+
+template <int NP, int WR, int TT>
+hipError_t launch(const F6Product& p, hipStream_t st) {
+  using P = Shape<NP, WR, TT>;
+  F6Product a = p;
+  const int64_t outs = a.gated ? P::ROWS / 2 : P::ROWS;
+  const int64_t out_m = a.gated ? a.m / 2 : a.m;
+  a.row_tiles = static_cast<int>((out_m + outs - 1) / outs);
+  int64_t tiles = (a.R + P::TOK - 1) / P::TOK;
+  if (a.offsets) tiles = a.R / P::TOK + (a.E < a.R ? a.E : a.R);
+  a.token_tiles = static_cast<int>(tiles);
+  const int64_t grid = (tiles * a.row_tiles + 7) / 8 * 8;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  auto* k = gemm_f6_kernel<NP, WR, TT>;
+  static const hipError_t big = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, P::LDS);
+  if (big != hipSuccess) return big;
+  k<<<dim3(static_cast<uint32_t>(grid)), 512, P::LDS, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int NP>
+hipError_t choose(const F6Product& p, hipStream_t st) {
+  // rows per tile: the tallest that still leaves a workgroup per compute
+  // unit; 64 tokens unless the runs are short
+  const int64_t out_m = p.gated ? p.m / 2 : p.m;
+  const int64_t runs = p.offsets ? (p.E < p.R ? p.E : p.R) : 1;
+  const bool two = p.R > 32 * runs;
+  auto count = [&](int WR, int TT) {
+    const int64_t outs = (p.gated ? 64 : 128) * WR;
+    return (p.R / (32 * TT) + runs) * ((out_m + outs - 1) / outs);
+  };
+  const int64_t cus = num_cus();
+  if constexpr (NP == 3)                               // (4, 2) with four parts spills
+    if (two && count(4, 2) >= 2 * cus) return launch<NP, 4, 2>(p, st);
+  if (two && count(2, 2) >= cus) return launch<NP, 2, 2>(p, st);
+  if (count(4, 1) >= 2 * cus) return launch<NP, 4, 1>(p, st);
+  if (count(2, 1) >= cus) return launch<NP, 2, 1>(p, st);
+  return launch<NP, 1, 1>(p, st);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_f6(const F6Product& p, int NP, hipStream_t st) {
+  return NP == 3 ? choose<3>(p, st) : choose<4>(p, st);
+}
+
+}  // namespace lq

@@ -6,6 +6,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "f6_parts.h"
 #include "lq_internal.h"
 
 namespace {
@@ -121,6 +122,123 @@ hipError_t scratch_pointer(void** ptr) {
   }
   *ptr = g_scratch_ptr[dev];
   return hipSuccess;
+}
+
+// ---- checks and plan shared by lq_gemm_ep, lq_gemm_grouped and lq_gemm_join
+
+lq_status f6_types(lq_dtype lift_dtype, lq_act act, int32_t gated, int64_t m, lq_dtype out_dtype) {
+  if (lift_dtype != LQ_F16 && lift_dtype != LQ_BF16)
+    return fail(LQ_ERR_DTYPE, "a_lift must be LQ_F16 or LQ_BF16");
+  if (!valid_dtype(out_dtype)) return fail(LQ_ERR_DTYPE, "unknown output dtype");
+  if (act < LQ_ACT_NONE || act > LQ_ACT_GELU_TANH)
+    return fail(LQ_ERR_UNSUPPORTED, "activation %d", (int)act);
+  if (gated && m % 2) return fail(LQ_ERR_SHAPE, "gated rows m=%lld must be even", (long long)m);
+  return LQ_OK;
+}
+
+int f6_parts_count(lq_dtype out_dtype) { return out_dtype == LQ_F32 ? 4 : 3; }
+
+// rows: of the activations.  One image of them is addressed with 32-bit offsets.
+lq_status f6_sizes(int64_t E, int64_t m, int64_t K, int64_t rows, lq_dtype out_dtype) {
+  if (E < 1 || E > 1024) return fail(LQ_ERR_SHAPE, "E=%lld outside 1..1024", (long long)E);
+  if (m < 1 || m > INT32_MAX || K < 1 || K > kGemmMaxK || rows < 0 || rows > INT32_MAX)
+    return fail(LQ_ERR_SHAPE, "m=%lld K=%lld (1..2^22) rows=%lld", (long long)m, (long long)K,
+                (long long)rows);
+  if (K % 8) return fail(LQ_ERR_SHAPE, "K=%lld must be a multiple of 8", (long long)K);
+  if ((rows + 1) * lq::f6::row_bytes(K, 2, f6_parts_count(out_dtype)) > INT64_C(0xFFFFFFFF))
+    return fail(LQ_ERR_SHAPE, "%lld rows of %lld positions exceed the 4 GiB operand image of one "
+                "call", (long long)rows, (long long)K);
+  return LQ_OK;
+}
+
+lq_status f6_matrices(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw, const float* s,
+                      const void* a_lift, int64_t lda, const float* bias) {
+  if (ldw < (K + 31) / 32) return fail(LQ_ERR_SHAPE, "ldw=%lld < ceil(K/32)", (long long)ldw);
+  if (ldw % 4) return fail(LQ_ERR_ALIGN, "ldw=%lld must be a multiple of 4", (long long)ldw);
+  if (ldw > (int64_t{1} << 28) || m * ldw * 4 > (int64_t{1} << 30))
+    return fail(LQ_ERR_SHAPE, "weights of one matrix exceed the 1 GiB per-call limit");
+  if (lda < K) return fail(LQ_ERR_SHAPE, "lda=%lld < K=%lld", (long long)lda, (long long)K);
+  if (lda % 8) return fail(LQ_ERR_ALIGN, "lda=%lld must be a multiple of 8", (long long)lda);
+  if (!aligned(w_packed, 16)) return fail(LQ_ERR_ALIGN, "w_packed must be 16-byte aligned");
+  if (!aligned(a_lift, 16)) return fail(LQ_ERR_ALIGN, "a_lift must be 16-byte aligned");
+  if (!aligned(s, 4) || !aligned(bias, 4)) return fail(LQ_ERR_ALIGN, "misaligned s or bias");
+  return LQ_OK;
+}
+
+lq_status f6_rows_out(const void* residual, int64_t ldr, const void* out, lq_dtype out_dtype,
+                      int64_t ldo, int64_t width, int64_t rows) {
+  if (ldo < width && rows > 1)
+    return fail(LQ_ERR_SHAPE, "ldo=%lld < %lld outputs", (long long)ldo, (long long)width);
+  if (residual && ldr < width && rows > 1)
+    return fail(LQ_ERR_SHAPE, "ldr=%lld < %lld outputs", (long long)ldr, (long long)width);
+  if (!aligned(out, dtype_size(out_dtype)) || !aligned(residual, dtype_size(out_dtype)))
+    return fail(LQ_ERR_ALIGN, "misaligned out or residual");
+  return LQ_OK;
+}
+
+lq_status f6_workspace(const void* workspace, size_t have, size_t need) {
+  if (!workspace) return fail(LQ_ERR_WORKSPACE, "workspace of %zu bytes required", need);
+  if (have < need) return fail(LQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", have, need);
+  if (!aligned(workspace, 256)) return fail(LQ_ERR_ALIGN, "workspace must be 256-byte aligned");
+  return LQ_OK;
+}
+
+lq_status join_sizes(int64_t T, int32_t k) {
+  if (T < 0 || k < 1 || k > 32 || T * k > INT32_MAX)
+    return fail(LQ_ERR_SHAPE, "T=%lld k=%d (k in 1..32)", (long long)T, (int)k);
+  return LQ_OK;
+}
+
+lq_status route_sizes(int64_t T, int64_t E, int32_t k) {
+  if (E < 1 || E > 1024) return fail(LQ_ERR_SHAPE, "E=%lld outside 1..1024", (long long)E);
+  if (T < 0 || k < 1 || k > 32 || k > E || T * k > INT32_MAX)
+    return fail(LQ_ERR_SHAPE, "T=%lld k=%d E=%lld (k in 1..min(E, 32))", (long long)T, (int)k,
+                (long long)E);
+  return LQ_OK;
+}
+
+// How one product runs: the image's form and what the workspace holds.
+struct F6Plan {
+  int H, NP;
+  int64_t row_bytes, rows;
+  size_t z_at;                 // float32 rows of lq_gemm_join
+  int64_t ldz;
+  size_t bytes;
+};
+
+F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtype out_dtype,
+               bool grouped, bool join) {
+  F6Plan p{};
+  p.H = 2;
+  p.NP = f6_parts_count(out_dtype);
+  p.row_bytes = lq::f6::row_bytes(K, p.H, p.NP);
+  p.rows = rows + (grouped ? 1 : 0);      // a row of zeros behind the last
+  p.bytes = (static_cast<size_t>(p.rows * p.row_bytes) + 255) / 256 * 256;
+  if (join) {
+    p.z_at = p.bytes;
+    p.ldz = (m + 3) / 4 * 4;
+    p.bytes += static_cast<size_t>(R) * p.ldz * 4;
+  }
+  return p;
+}
+
+lq::F6Product f6_product(const uint32_t* w, int64_t m, int64_t K, int64_t ldw, const float* s,
+                         const float* bias, int act, int gated, const F6Plan& plan,
+                         const void* image) {
+  lq::F6Product p{};
+  p.img = static_cast<const uint8_t*>(image);
+  p.img_row_bytes = static_cast<uint32_t>(plan.row_bytes);
+  p.img_bytes = static_cast<uint32_t>(plan.rows * plan.row_bytes);
+  p.groups = static_cast<int>(lq::f6::padded_positions(K) / 256);
+  p.w = w;
+  p.m = static_cast<int>(m);
+  p.ldw = static_cast<int>(ldw);
+  p.s = s;
+  p.bias = bias;
+  p.act = act;
+  p.gated = gated != 0;
+  p.E = 1;
+  return p;
 }
 
 }  // namespace
@@ -549,6 +667,183 @@ lq_status lq_gemm(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw, c
   return hip_status(lq::launch_gemm(w_packed, m, K, ldw, s, a_lift, lift_dtype, B, out,
                                     as_stream(stream)),
                     "lq_gemm launch");
+}
+
+// ------------------------------------------------ float4 x float6 products and the router
+lq_status lq_gemm_ep_workspace_size(int64_t m, int64_t K, int64_t B, lq_dtype out_dtype,
+                                    size_t* bytes) {
+  if (!bytes) return fail(LQ_ERR_NULL, "bytes is null");
+  if (!valid_dtype(out_dtype)) return fail(LQ_ERR_DTYPE, "unknown dtype");
+  const lq_status st = f6_sizes(1, m, K, B, out_dtype);
+  if (st != LQ_OK) return st;
+  *bytes = f6_plan(1, m, K, B, B, out_dtype, false, false).bytes;
+  return ok();
+}
+
+lq_status lq_gemm_ep(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw, const float* s,
+                     const void* a_lift, lq_dtype lift_dtype, int64_t lda, int64_t B,
+                     const float* bias, lq_act act, int32_t gated, const void* residual,
+                     int64_t ldr, void* out, lq_dtype out_dtype, int64_t ldo, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!w_packed || !s || !a_lift || !out) return fail(LQ_ERR_NULL, "null pointer");
+  lq_status st = f6_types(lift_dtype, act, gated, m, out_dtype);
+  if (st == LQ_OK) st = f6_sizes(1, m, K, B, out_dtype);
+  if (st != LQ_OK) return st;
+  if (B < 1) return fail(LQ_ERR_SHAPE, "B=%lld", (long long)B);
+  const int64_t width = gated ? m / 2 : m;
+  st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
+  if (st == LQ_OK) st = f6_rows_out(residual, ldr, out, out_dtype, ldo, width, B);
+  const auto plan = f6_plan(1, m, K, B, B, out_dtype, false, false);
+  if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
+  if (st != LQ_OK) return st;
+  lq::F6Product p = f6_product(w_packed, m, K, ldw, s, bias, act, gated, plan, workspace);
+  p.residual = residual;
+  p.ldr = ldr;
+  p.out = out;
+  p.ldo = ldo;
+  p.out_dt = out_dtype;
+  p.R = static_cast<int>(B);
+  p.src_rows = static_cast<int>(B);
+  const hipStream_t hs = as_stream(stream);
+  hipError_t e = lq::launch_f6_image(a_lift, lift_dtype, B, false, K, lda, plan.H, plan.NP,
+                                     workspace, hs);
+  if (e == hipSuccess) e = lq::launch_gemm_f6(p, plan.NP, hs);
+  return hip_status(e, "lq_gemm_ep launch");
+}
+
+lq_status lq_gemm_grouped_workspace_size(int64_t E, int64_t m, int64_t K, int64_t a_rows,
+                                         int64_t R, lq_dtype out_dtype, size_t* bytes) {
+  if (!bytes) return fail(LQ_ERR_NULL, "bytes is null");
+  if (!valid_dtype(out_dtype)) return fail(LQ_ERR_DTYPE, "unknown dtype");
+  lq_status st = f6_sizes(E, m, K, a_rows, out_dtype);
+  if (st == LQ_OK && (R < 0 || R > INT32_MAX)) st = fail(LQ_ERR_SHAPE, "R=%lld", (long long)R);
+  if (st != LQ_OK) return st;
+  *bytes = f6_plan(E, m, K, a_rows, R, out_dtype, true, false).bytes;
+  return ok();
+}
+
+lq_status lq_gemm_grouped(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K, int64_t ldw,
+                          const float* s, const void* a_lift, lq_dtype lift_dtype, int64_t lda,
+                          int64_t a_rows, const int32_t* rows, const int32_t* offsets, int64_t R,
+                          const float* bias, lq_act act, int32_t gated, void* out,
+                          lq_dtype out_dtype, int64_t ldo, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  lq_status st = f6_types(lift_dtype, act, gated, m, out_dtype);
+  if (st == LQ_OK) st = f6_sizes(E, m, K, a_rows, out_dtype);
+  if (st != LQ_OK) return st;
+  if (R < 0 || R > INT32_MAX) return fail(LQ_ERR_SHAPE, "R=%lld", (long long)R);
+  if (!rows && a_rows < R)
+    return fail(LQ_ERR_SHAPE, "a_rows=%lld < R=%lld without row indices", (long long)a_rows,
+                (long long)R);
+  if (R == 0) return ok();
+  if (a_rows < 1) return fail(LQ_ERR_SHAPE, "a_rows=%lld", (long long)a_rows);
+  if (!w_packed || !s || !a_lift || !out || !offsets) return fail(LQ_ERR_NULL, "null pointer");
+  if (!aligned(offsets, 4) || (rows && !aligned(rows, 4)))
+    return fail(LQ_ERR_ALIGN, "misaligned rows or offsets");
+  const int64_t width = gated ? m / 2 : m;
+  st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
+  if (st == LQ_OK) st = f6_rows_out(nullptr, 0, out, out_dtype, ldo, width, R);
+  const auto plan = f6_plan(E, m, K, a_rows, R, out_dtype, true, false);
+  if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
+  if (st != LQ_OK) return st;
+  lq::F6Product p = f6_product(w_packed, m, K, ldw, s, bias, act, gated, plan, workspace);
+  p.out = out;
+  p.ldo = ldo;
+  p.out_dt = out_dtype;
+  p.R = static_cast<int>(R);
+  p.offsets = offsets;
+  p.E = static_cast<int>(E);
+  p.rows = rows;
+  p.src_rows = static_cast<int>(a_rows);
+  const hipStream_t hs = as_stream(stream);
+  hipError_t e = lq::launch_f6_image(a_lift, lift_dtype, a_rows, true, K, lda, plan.H, plan.NP,
+                                     workspace, hs);
+  if (e == hipSuccess) e = lq::launch_gemm_f6(p, plan.NP, hs);
+  return hip_status(e, "lq_gemm_grouped launch");
+}
+
+lq_status lq_gemm_join_workspace_size(int64_t E, int64_t m, int64_t K, int64_t R, int64_t T,
+                                      int32_t k, lq_dtype out_dtype, size_t* bytes) {
+  if (!bytes) return fail(LQ_ERR_NULL, "bytes is null");
+  if (!valid_dtype(out_dtype)) return fail(LQ_ERR_DTYPE, "unknown dtype");
+  lq_status st = f6_sizes(E, m, K, R, out_dtype);
+  if (st == LQ_OK) st = join_sizes(T, k);
+  if (st != LQ_OK) return st;
+  *bytes = f6_plan(E, m, K, R, R, out_dtype, true, true).bytes;
+  return ok();
+}
+
+lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K, int64_t ldw,
+                       const float* s, const void* a_lift, lq_dtype lift_dtype, int64_t lda,
+                       const int32_t* offsets, int64_t R, const float* bias, const int32_t* pos,
+                       const float* weight, int64_t T, int32_t k, const void* residual,
+                       int64_t ldr, void* out, lq_dtype out_dtype, int64_t ldo, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  lq_status st = f6_types(lift_dtype, LQ_ACT_NONE, 0, m, out_dtype);
+  if (st == LQ_OK) st = f6_sizes(E, m, K, R, out_dtype);
+  if (st == LQ_OK) st = join_sizes(T, k);
+  if (st != LQ_OK) return st;
+  if (T == 0) return ok();
+  if (!w_packed || !s || !out || !offsets || !pos || !weight || (R > 0 && !a_lift))
+    return fail(LQ_ERR_NULL, "null pointer");
+  if (!aligned(offsets, 4) || !aligned(pos, 4) || !aligned(weight, 4))
+    return fail(LQ_ERR_ALIGN, "misaligned offsets, pos or weight");
+  st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
+  if (st == LQ_OK) st = f6_rows_out(residual, ldr, out, out_dtype, ldo, m, T);
+  const auto plan = f6_plan(E, m, K, R, R, out_dtype, true, true);
+  if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
+  if (st != LQ_OK) return st;
+  const hipStream_t hs = as_stream(stream);
+  float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.z_at);
+  hipError_t e = hipSuccess;
+  if (R > 0) {
+    lq::F6Product p = f6_product(w_packed, m, K, ldw, s, bias, LQ_ACT_NONE, 0, plan, workspace);
+    p.out = z;
+    p.ldo = plan.ldz;
+    p.out_dt = LQ_F32;
+    p.R = static_cast<int>(R);
+    p.offsets = offsets;
+    p.E = static_cast<int>(E);
+    p.src_rows = static_cast<int>(R);
+    e = lq::launch_f6_image(a_lift, lift_dtype, R, true, K, lda, plan.H, plan.NP, workspace, hs);
+    if (e == hipSuccess) e = lq::launch_gemm_f6(p, plan.NP, hs);
+  }
+  if (e == hipSuccess)
+    e = lq::launch_join(z, R, m, plan.ldz, pos, weight, T, k, residual, ldr, out, ldo, out_dtype,
+                        hs);
+  return hip_status(e, "lq_gemm_join launch");
+}
+
+lq_status lq_route_workspace_size(int64_t T, int64_t E, int32_t k, size_t* bytes) {
+  if (!bytes) return fail(LQ_ERR_NULL, "bytes is null");
+  const lq_status st = route_sizes(T, E, k);
+  if (st != LQ_OK) return st;
+  *bytes = lq::route_workspace_bytes(T, static_cast<int>(E));
+  return ok();
+}
+
+lq_status lq_route(const void* logits, lq_dtype dtype, int64_t T, int64_t E, int64_t ld,
+                   const uint8_t* valid, int32_t k, int32_t renorm, int32_t* ids, float* weight,
+                   int32_t* pos, int32_t* rows, int32_t* offsets, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  if (!valid_dtype(dtype)) return fail(LQ_ERR_DTYPE, "unknown dtype");
+  lq_status st = route_sizes(T, E, k);
+  if (st != LQ_OK) return st;
+  if (ld < E) return fail(LQ_ERR_SHAPE, "ld=%lld < E=%lld", (long long)ld, (long long)E);
+  if (!offsets || (T > 0 && (!logits || !ids || !weight || !pos || !rows)))
+    return fail(LQ_ERR_NULL, "null pointer");
+  if (!aligned(logits, dtype_size(dtype)) || !aligned(ids, 4) || !aligned(weight, 4) ||
+      !aligned(pos, 4) || !aligned(rows, 4) || !aligned(offsets, 4))
+    return fail(LQ_ERR_ALIGN, "misaligned pointer");
+  const size_t need = lq::route_workspace_bytes(T, static_cast<int>(E));
+  if (need) {
+    st = f6_workspace(workspace, workspace_bytes, need);
+    if (st != LQ_OK) return st;
+  }
+  return hip_status(lq::launch_route(logits, dtype, T, static_cast<int>(E), ld, valid, k, renorm,
+                                     ids, weight, pos, rows, offsets, workspace,
+                                     as_stream(stream)),
+                    "lq_route launch");
 }
 
 }  // extern "C"

@@ -162,4 +162,46 @@ hipError_t launch_gemv_f4r(const uint32_t* w, int64_t m, int64_t K, int64_t ldw,
 hipError_t launch_gemm(const uint32_t* w, int64_t m, int64_t K, int64_t ldw, const float* s,
                        const void* a_lift, lq_dtype dt, int64_t B, float* out, hipStream_t st);
 
+// ---------------------------------------------------------------- float4 x float6 products
+// Arguments of the products on float6 parts (f6_parts.h): lq_gemm_ep (one
+// matrix, R tokens) and lq_gemm_grouped (E matrices, ragged runs of R rows).
+struct F6Product {
+  const uint8_t* img;          // parts of the activations
+  uint32_t img_row_bytes;
+  uint32_t img_bytes;
+  int groups;                  // groups of 256 positions, even
+  const uint32_t* w;           // [E][m][ldw]
+  int m, ldw;
+  const float* s;              // [E][m]
+  const float* bias;           // [E][m] or null
+  int act, gated;
+  const void* residual;        // [R][ldr] or null
+  int64_t ldr;
+  void* out;                   // [R][ldo]
+  int64_t ldo;
+  int out_dt;
+  int R;
+  const int* offsets;          // [E + 1], or null: one matrix
+  int E;
+  const int* rows;             // image row of each row, or null: its own
+  int src_rows;                // rows of the image (with `rows`, one more of zeros follows)
+  int row_tiles, token_tiles;  // set by the launcher
+};
+
+// 16-bit activations -> parts image (k_f6_image.hip); H = 2 or 4, NP = 3 or 4.
+hipError_t launch_f6_image(const void* a, lq_dtype dt, int64_t rows, bool zero_row, int64_t K,
+                           int64_t lda, int H, int NP, void* img, hipStream_t st);
+hipError_t launch_gemm_f6(const F6Product& p, int NP, hipStream_t st);
+
+// out = residual + sum_j weight z[pos] (k_join.hip); ldz a multiple of 4.
+hipError_t launch_join(const float* z, int64_t R, int64_t m, int64_t ldz, const int* pos,
+                       const float* weight, int64_t T, int k, const void* residual, int64_t ldr,
+                       void* out, int64_t ldo, int dt, hipStream_t st);
+
+// Router (k_route.hip), E <= 1024, k <= 32.
+size_t route_workspace_bytes(int64_t T, int E);
+hipError_t launch_route(const void* logits, lq_dtype dt, int64_t T, int E, int64_t ld,
+                        const uint8_t* valid, int k, int renorm, int* ids, float* weight, int* pos,
+                        int* rows, int* offsets, void* ws, hipStream_t st);
+
 }  // namespace lq

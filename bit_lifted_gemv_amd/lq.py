@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -30,7 +30,13 @@ EXPORTS = ("lq_status_string", "lq_last_error", "lq_version", "lq_pack_signs", "
            "lq_softmin_grad", "lq_adam_update", "lq_gemm_decoded_workspace_size",
            "lq_gemm_decoded", "lq_layer_b1_workspace_size", "lq_layer_b1",
            "lq_gemv_noalloc", "lq_stream_read", "lq_lift_parts_size", "lq_lift_parts",
-           "lq_gemv_parts_workspace_size", "lq_gemv_parts")
+           "lq_gemv_parts_workspace_size", "lq_gemv_parts",
+           "lq_gemm_ep_workspace_size", "lq_gemm_ep", "lq_route_workspace_size", "lq_route",
+           "lq_gemm_grouped_workspace_size", "lq_gemm_grouped", "lq_gemm_join_workspace_size",
+           "lq_gemm_join")
+
+# Activations of gemm_ep and gemm_grouped.
+ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
@@ -81,6 +87,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                    _vp, _vp, _sz, _vp]),
         "lq_softmin_grad": (_i32, [_vp, _i64, _vp, _i32, _i32, ctypes.c_float, _vp, _vp, _vp,
                                    _sz, _vp]),
+        "lq_gemm_ep_workspace_size": (_i32, [_i64, _i64, _i64, _i32, ctypes.POINTER(_sz)]),
+        "lq_gemm_ep": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _i64, _vp, _i32, _i32,
+                              _vp, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
+        "lq_route_workspace_size": (_i32, [_i64, _i64, _i32, ctypes.POINTER(_sz)]),
+        "lq_route": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                            _vp, _sz, _vp]),
+        "lq_gemm_grouped_workspace_size": (_i32, [_i64, _i64, _i64, _i64, _i64, _i32,
+                                                  ctypes.POINTER(_sz)]),
+        "lq_gemm_grouped": (_i32, [_vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _i64, _vp,
+                                   _vp, _i64, _vp, _i32, _i32, _vp, _i32, _i64, _vp, _sz, _vp]),
+        "lq_gemm_join_workspace_size": (_i32, [_i64, _i64, _i64, _i64, _i64, _i32, _i32,
+                                               ctypes.POINTER(_sz)]),
+        "lq_gemm_join": (_i32, [_vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp,
+                                _vp, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
         "lq_adam_update": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, ctypes.c_float,
                                   ctypes.c_float, ctypes.c_float, ctypes.c_float, _vp]),
     }
@@ -420,6 +440,242 @@ def gemm(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor, K: Optio
     return out
 
 
+# ------------------------------------- products with an epilogue, experts, router
+class _On:
+    """The device and stream that one of the calls below runs on: the
+    tensors' device (current or not) and its current stream, or `stream`.
+    Temporary workspaces come from torch's allocator on that stream, a new
+    one for every call, so that calls on two streams or captured graphs never
+    share one."""
+
+    __slots__ = ("device", "stream", "handle", "guard")
+
+    def __init__(self, device: torch.device, stream):
+        self.device = device
+        self.stream = stream
+        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        self.guard = None
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def workspace(self, nbytes: int) -> Optional[torch.Tensor]:
+        if not nbytes:
+            return None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        if self.stream is not None:
+            ws.record_stream(self.stream)
+        return ws
+
+
+def _same_device(device: torch.device, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _plain(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple) -> None:
+    """A contiguous tensor of this type and shape (or None)."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _pitch(name: str, t: torch.Tensor, shape: tuple, dtype: Optional[torch.dtype] = None) -> int:
+    """Row pitch of a matrix whose rows are dense and may lie apart."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be dense")
+    # the stride of a single row says nothing
+    return t.stride(0) if shape[0] > 1 else shape[1] + -shape[1] % 8
+
+
+def _experts(w_packed: torch.Tensor, s: torch.Tensor, bias: Optional[torch.Tensor],
+             lead: tuple) -> None:
+    if not w_packed.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    _plain("w_packed", w_packed, torch.int32, lead + (w_packed.shape[-1],))
+    _plain("s", s, torch.float32, lead)
+    _plain("bias", bias, torch.float32, lead)
+
+
+def _lifted(a_lift: torch.Tensor) -> int:
+    if a_lift.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"a_lift must be float16 or bfloat16, not {a_lift.dtype}")
+    return _pitch("a_lift", a_lift, tuple(a_lift.shape))
+
+
+def _target(out: Optional[torch.Tensor], rows: int, width: int, out_dtype: Optional[torch.dtype],
+            a_lift: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    if out is None:
+        dt = a_lift.dtype if out_dtype is None else out_dtype
+        out = torch.empty((rows, width), dtype=dt, device=a_lift.device)
+        return out, width
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, not {out_dtype}")
+    return out, _pitch("out", out, (rows, width))
+
+
+def _act(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"unknown activation {act!r} (one of {', '.join(ACTS)})")
+    return ACTS[act]
+
+
+def gemm_ep(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
+            bias: Optional[torch.Tensor] = None, act: str = "none", gated: bool = False,
+            residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """act(s * (sigma @ a_lift^T) + bias) + residual for any number of tokens
+    (lq_gemm_ep).  a_lift float16 or bfloat16 [B][K] (rows may lie apart);
+    `act` one of ACTS; `gated`: rows of w_packed are the gate's m/2, then the up
+    projection's, and out [B][m/2] = act(gate) * up + residual.  out_dtype
+    (default a_lift's): float32, float16 or bfloat16, also the residual's;
+    `residual` may be `out`."""
+    m, ldw = w_packed.shape
+    B, K = a_lift.shape
+    dev = a_lift.device
+    _experts(w_packed, s, bias, (m,))
+    _same_device(dev, w_packed=w_packed, s=s, bias=bias, residual=residual, out=out)
+    lda = _lifted(a_lift)
+    width = m // 2 if gated else m
+    code = _act(act)
+    with _On(dev, stream) as on:
+        out, ldo = _target(out, B, width, out_dtype, a_lift)
+        ldr = 0 if residual is None else _pitch("residual", residual, (B, width), out.dtype)
+        n = _sz(0)
+        L = lib()
+        check(L.lq_gemm_ep_workspace_size(m, K, B, _dt(out), ctypes.byref(n)))
+        ws = on.workspace(n.value)
+        check(L.lq_gemm_ep(_ptr(w_packed), m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift), lda, B,
+                           _ptr(bias), code, int(gated), _ptr(residual), ldr, _ptr(out), _dt(out),
+                           ldo, _ptr(ws), n.value, on.handle))
+    return out
+
+
+def gemm_grouped(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
+                 offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                 bias: Optional[torch.Tensor] = None, act: str = "none", gated: bool = False,
+                 out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """The experts' products on ragged runs of rows (lq_gemm_grouped):
+    w_packed [E][m][ldw], s and bias [E][m], offsets int32 [E + 1], rows int32
+    [R] (which row of a_lift each sorted row is; None: its own).  Returns out
+    [R][m], or [R][m/2] when gated; rows outside every run are not written."""
+    E, m, ldw = w_packed.shape
+    n_rows, K = a_lift.shape
+    dev = a_lift.device
+    R = n_rows if rows is None else rows.shape[0]
+    _experts(w_packed, s, bias, (E, m))
+    _plain("offsets", offsets, torch.int32, (E + 1,))
+    _plain("rows", rows, torch.int32, (R,))
+    _same_device(dev, w_packed=w_packed, s=s, bias=bias, offsets=offsets, rows=rows, out=out)
+    lda = _lifted(a_lift)
+    width = m // 2 if gated else m
+    code = _act(act)
+    with _On(dev, stream) as on:
+        out, ldo = _target(out, R, width, out_dtype, a_lift)
+        n = _sz(0)
+        L = lib()
+        check(L.lq_gemm_grouped_workspace_size(E, m, K, n_rows, R, _dt(out), ctypes.byref(n)))
+        ws = on.workspace(n.value)
+        check(L.lq_gemm_grouped(_ptr(w_packed), E, m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift),
+                                lda, n_rows, _ptr(rows), _ptr(offsets), R, _ptr(bias), code,
+                                int(gated), _ptr(out), _dt(out), ldo, _ptr(ws), n.value,
+                                on.handle))
+    return out
+
+
+def gemm_join(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
+              offsets: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor,
+              bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+              out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """The experts' products on the sorted rows a_lift [R][K] and their weighted
+    sum per token (lq_gemm_join): out [T][m] = residual + sum_j weight[t][j]
+    z[pos[t][j]], pos int32 and weight float32 [T][k].  `residual` may be `out`."""
+    E, m, ldw = w_packed.shape
+    R, K = a_lift.shape
+    T, k = pos.shape
+    dev = a_lift.device
+    _experts(w_packed, s, bias, (E, m))
+    _plain("offsets", offsets, torch.int32, (E + 1,))
+    _plain("pos", pos, torch.int32, (T, k))
+    _plain("weight", weight, torch.float32, (T, k))
+    _same_device(dev, w_packed=w_packed, s=s, bias=bias, offsets=offsets, pos=pos, weight=weight,
+                 residual=residual, out=out)
+    lda = _lifted(a_lift)
+    with _On(dev, stream) as on:
+        out, ldo = _target(out, T, m, out_dtype, a_lift)
+        ldr = 0 if residual is None else _pitch("residual", residual, (T, m), out.dtype)
+        n = _sz(0)
+        L = lib()
+        check(L.lq_gemm_join_workspace_size(E, m, K, R, T, k, _dt(out), ctypes.byref(n)))
+        ws = on.workspace(n.value)
+        check(L.lq_gemm_join(_ptr(w_packed), E, m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift),
+                             lda, _ptr(offsets), R, _ptr(bias), _ptr(pos), _ptr(weight), T, k,
+                             _ptr(residual), ldr, _ptr(out), _dt(out), ldo, _ptr(ws), n.value,
+                             on.handle))
+    return out
+
+
+class Routing(NamedTuple):
+    """What lq_route gives: ids int32 and weight float32 [T][k] (largest logit
+    first; -1 and 0 where a token has no further expert), pos int32 [T][k]
+    (sorted position of each pair, or -1), rows int32 [T * k] (token of each
+    sorted position, -1 behind the last), offsets int32 [E + 1]."""
+    ids: torch.Tensor
+    weight: torch.Tensor
+    pos: torch.Tensor
+    rows: torch.Tensor
+    offsets: torch.Tensor
+
+
+def route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None, renorm: bool = True,
+          stream=None) -> Routing:
+    """Each token's k experts, their weights and the pairs sorted by expert
+    (lq_route).  logits [T][E] float32, float16 or bfloat16 (rows may lie
+    apart); valid: uint8 or bool [T], 0 for tokens that go to no expert."""
+    T, E = logits.shape
+    dev = logits.device
+    if not logits.is_cuda:
+        raise ValueError("tensors must live on the GPU")
+    if valid is not None and valid.dtype == torch.bool:
+        valid = valid.view(torch.uint8)
+    _plain("valid", valid, torch.uint8, (T,))
+    _same_device(dev, valid=valid)
+    ld = _pitch("logits", logits, (T, E))
+    code = _dt(logits)
+    with _On(dev, stream) as on:
+        n = _sz(0)
+        L = lib()
+        check(L.lq_route_workspace_size(T, E, k, ctypes.byref(n)))
+        ws = on.workspace(n.value)
+        pairs = torch.empty((3, T, k), dtype=torch.int32, device=dev)
+        weight = torch.empty((T, k), dtype=torch.float32, device=dev)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        ids, pos, rows = pairs[0], pairs[1], pairs[2].view(-1)
+        check(L.lq_route(_ptr(logits), code, T, E, ld, _ptr(valid), k, int(renorm), _ptr(ids),
+                         _ptr(weight), _ptr(pos), _ptr(rows), _ptr(offsets), _ptr(ws), n.value,
+                         on.handle))
+    return Routing(ids, weight, pos, rows, offsets)
+
+
 # ----------------------------------------------------------------- layer
 class DeviceLayer:
     """A layer's stored arrays resident on the GPU (uploaded once)."""
@@ -473,6 +729,32 @@ class DeviceLayer:
             return gemm(self.w, self.s, al, self.K)
         al = lift(a, self.t_inv, self.M, self.d, self.D, out_dtype=torch.float32)
         return gemv(self.w, self.s, al, self.K)
+
+
+class DeviceExperts:
+    """A mixture-of-experts MLP resident on the GPU: E experts of 1-bit lifted
+    layers, w1 [E][2 f][ldw] (gate rows, then up rows) on n inputs, w2 [E][n][ldw]
+    on f, their row scales s1 [E][2 f] and s2 [E][n], and the transforms that all
+    experts share, t1 [n/128][128][128], t2 [f/128][128][128], M1 and M2 [d][D]."""
+
+    def __init__(self, w1, s1, t1, M1, w2, s2, t2, M2, d: int, D: int, k: int, act: str = "silu",
+                 bias1=None, bias2=None):
+        self.w1, self.s1, self.t1, self.M1, self.bias1 = w1, s1, t1, M1, bias1
+        self.w2, self.s2, self.t2, self.M2, self.bias2 = w2, s2, t2, M2, bias2
+        self.d, self.D, self.k, self.act = d, D, k, act
+
+    def forward(self, x: torch.Tensor, logits: torch.Tensor,
+                residual: Optional[torch.Tensor] = None, valid: Optional[torch.Tensor] = None,
+                renorm: bool = True) -> torch.Tensor:
+        """x [T][n] (float16 or bfloat16), router logits [T][E] -> [T][n]: each token
+        through its k experts, weighted, plus the residual.  valid[t] == 0: none."""
+        r = route(logits, self.k, valid=valid, renorm=renorm)
+        a = lift(x, self.t1, self.M1, self.d, self.D, out_dtype=x.dtype)
+        h = gemm_grouped(self.w1, self.s1, a, r.offsets, rows=r.rows, bias=self.bias1,
+                         act=self.act, gated=True)
+        hl = lift(h, self.t2, self.M2, self.d, self.D, out_dtype=x.dtype)
+        return gemm_join(self.w2, self.s2, hl, r.offsets, r.pos, r.weight, bias=self.bias2,
+                         residual=residual)
 
 
 def to_torch_16(x, dtype: str) -> torch.Tensor:

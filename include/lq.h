@@ -56,6 +56,14 @@ typedef int32_t lq_dtype;
 #define LQ_F16  1
 #define LQ_BF16 2
 
+/* Activations of the products with an epilogue (lq_gemm_ep, lq_gemm_grouped). */
+typedef int32_t lq_act;
+#define LQ_ACT_NONE      0  /* z                                                   */
+#define LQ_ACT_RELU      1  /* max(z, 0)                                           */
+#define LQ_ACT_SILU      2  /* z / (1 + exp(-z))                                   */
+#define LQ_ACT_GELU      3  /* z (1 + erf(z / sqrt 2)) / 2                         */
+#define LQ_ACT_GELU_TANH 4  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2   */
+
 /* Human-readable name of a status code (static string). */
 const char* lq_status_string(lq_status st);
 /* Message of the last failed call on this thread ("" if none). */
@@ -406,6 +414,123 @@ lq_status lq_layer_b1(const void* a, lq_dtype a_dtype, int64_t n, const void* t_
 lq_status lq_gemm(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw,
                   const float* s, const void* a_lift, lq_dtype lift_dtype, int64_t B,
                   float* out, void* stream);
+
+/*
+ * lq_gemm_ep -- the product of the 1-bit weights with 16-bit lifted
+ * activations (关键设计 4), followed in the same pass by what a transformer
+ * layer does with it: bias, activation or gate, residual, and the store in
+ * the layer's own type.  For any number of tokens, from one:
+ *   z[b][i]   = s[i] * sum_{k<K} sigma_ik * a_lift[b][k] + bias[i]
+ *   out[b][i] = act(z[b][i]) + residual[b][i]                        (gated == 0)
+ *   out[b][i] = act(z[b][i]) * z[b][m/2 + i] + residual[b][i], i < m/2  (gated != 0:
+ *               the first m/2 rows of W_q are the gate's, the others the up rows)
+ * w_packed: uint32 [m][ldw] (layout of lq_pack_signs), 16-byte aligned,
+ *           ldw >= ceil(K/32), a multiple of 4, m*ldw*4 <= 2^30; bits at
+ *           positions >= K may hold anything.
+ * s:        float [m];  bias: float [m] or NULL.
+ * a_lift:   [B] rows of K values of lift_dtype (LQ_F16 or LQ_BF16;
+ *           lq_lift_activations writes them), lda apart; K and lda multiples
+ *           of 8, 16-byte aligned, K <= 2^22.
+ * residual: [B] rows, ldr apart, of out_dtype, or NULL; it may be `out`
+ *           itself (with ldr == ldo), otherwise it must not overlap it.
+ * out:      [B] rows of m (gated: m/2) values of out_dtype (LQ_F32, LQ_F16 or
+ *           LQ_BF16, rounded once to nearest even), ldo apart.
+ * workspace: >= lq_gemm_ep_workspace_size bytes, 256-byte aligned,
+ *           caller-owned, no initialisation needed.
+ * Requires B >= 1; B rows of operand image (2.3 bytes per position, 3.1 for
+ * float32 outputs) below 4 GiB: split more tokens over several calls.
+ * Arithmetic: every value is carried by float6 (E2M3) parts of 4 significant
+ * bits with one power of two per 32 positions of a token, three parts for
+ * 16-bit outputs (within 2^-14 of the 32 positions' largest value), four for
+ * float32 (2^-18); exact products with the signs, float32 sums in a fixed
+ * order (deterministic); epilogue in float32.  A token that holds an
+ * infinity or a NaN gives NaN in all of its outputs.
+ */
+lq_status lq_gemm_ep_workspace_size(int64_t m, int64_t K, int64_t B, lq_dtype out_dtype,
+                                    size_t* bytes);
+lq_status lq_gemm_ep(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw, const float* s,
+                     const void* a_lift, lq_dtype lift_dtype, int64_t lda, int64_t B,
+                     const float* bias, lq_act act, int32_t gated, const void* residual,
+                     int64_t ldr, void* out, lq_dtype out_dtype, int64_t ldo, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * lq_route -- the router of a mixture-of-experts layer: each token's k
+ * experts of E, their weights, and the (token, choice) pairs sorted by expert
+ * (within an expert by token), which is what lq_gemm_grouped and
+ * lq_gemm_join run over.
+ *   ids[t][j]: the experts of the k largest logits, largest first, equal ones
+ *     lowest expert first (-0 equals +0).  A NaN or -inf is never chosen; a
+ *     token with fewer than k others, or with valid[t] == 0, fills up with -1.
+ *   weight[t][j] = exp(l_j) / sum exp(l) over the token's chosen experts
+ *     (renorm != 0) or over all of its logits (renorm == 0); 0 where ids is -1.
+ *     +inf logits share the whole weight.
+ *   offsets[e] .. offsets[e + 1]: the sorted positions of expert e's pairs;
+ *   rows[p]: the token of sorted position p, -1 from offsets[E] on;
+ *   pos[t][j]: the sorted position of the pair, -1 where ids is -1.
+ * logits: [T] rows of E values of dtype, ld apart.  valid: uint8 [T] or NULL.
+ * ids, pos: int32 [T][k];  weight: float [T][k];  rows: int32 [T*k];
+ * offsets: int32 [E + 1].
+ * workspace: >= lq_route_workspace_size bytes (0 up to 64 tokens, then it may
+ *     be NULL), 256-byte aligned, caller-owned, no initialisation needed.
+ * Requires 1 <= E <= 1024, 1 <= k <= min(E, 32), T >= 0, T*k < 2^31.  T == 0
+ * writes zero offsets.  Float32 arithmetic; deterministic.
+ */
+lq_status lq_route_workspace_size(int64_t T, int64_t E, int32_t k, size_t* bytes);
+lq_status lq_route(const void* logits, lq_dtype dtype, int64_t T, int64_t E, int64_t ld,
+                   const uint8_t* valid, int32_t k, int32_t renorm, int32_t* ids, float* weight,
+                   int32_t* pos, int32_t* rows, int32_t* offsets, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/*
+ * lq_gemm_grouped -- one 1-bit matrix per expert and a ragged run of rows
+ * each, the way into a mixture-of-experts layer: row r of the sorted order,
+ * offsets[e] <= r < offsets[e + 1], is
+ *   z[r][i] = s[e][i] * sum_k sigma^e_ik * a_lift[rows[r]][k] + bias[e][i]
+ *   out[r] = act(z[r]) or the gated form, as lq_gemm_ep.
+ * w_packed: uint32 [E][m][ldw];  s: float [E][m];  bias: float [E][m] or NULL.
+ * a_lift:   [a_rows] rows as in lq_gemm_ep.  rows: int32 [R] on the device
+ *           (lq_route's), or NULL for row r itself (then a_rows >= R).  An
+ *           index outside [0, a_rows) reads a row of zeros.
+ * offsets:  int32 [E + 1] on the device, ascending; runs are cut to [0, R].
+ * out:      [R] rows of out_dtype, ldo apart.  Rows outside every run are
+ *           left as they were.
+ * Everything else (limits with a_rows for B, arithmetic, workspace of
+ * lq_gemm_grouped_workspace_size bytes) as lq_gemm_ep; 1 <= E <= 1024,
+ * 0 <= R < 2^31 (R == 0 is a no-op).  No host synchronisation: the runs are
+ * read on the device.
+ */
+lq_status lq_gemm_grouped_workspace_size(int64_t E, int64_t m, int64_t K, int64_t a_rows,
+                                         int64_t R, lq_dtype out_dtype, size_t* bytes);
+lq_status lq_gemm_grouped(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K, int64_t ldw,
+                          const float* s, const void* a_lift, lq_dtype lift_dtype, int64_t lda,
+                          int64_t a_rows, const int32_t* rows, const int32_t* offsets, int64_t R,
+                          const float* bias, lq_act act, int32_t gated, void* out,
+                          lq_dtype out_dtype, int64_t ldo, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * lq_gemm_join -- the way out: the experts' products on the sorted rows and
+ * their weighted sum per token,
+ *   z[r][i]   = s[e][i] * sum_k sigma^e_ik * a_lift[r][k] + bias[e][i]
+ *   out[t][i] = residual[t][i] + sum_j weight[t][j] * z[pos[t][j]][i].
+ * a_lift:   [R] rows in the sorted order (the lifted rows of lq_gemm_grouped).
+ * pos, weight: int32 and float [T][k] (lq_route's).  A position outside
+ *           [0, R) adds nothing (one inside, but outside every run, adds an
+ *           unspecified value: lq_route gives none).
+ * residual: [T] rows of out_dtype, ldr apart, or NULL; it may be `out`.
+ * out:      [T] rows of m values of out_dtype, ldo apart.
+ * Sums over j in float32, in order.  1 <= k <= 32, T*k < 2^31, T == 0 is a
+ * no-op; everything else as lq_gemm_grouped.
+ */
+lq_status lq_gemm_join_workspace_size(int64_t E, int64_t m, int64_t K, int64_t R, int64_t T,
+                                      int32_t k, lq_dtype out_dtype, size_t* bytes);
+lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K, int64_t ldw,
+                       const float* s, const void* a_lift, lq_dtype lift_dtype, int64_t lda,
+                       const int32_t* offsets, int64_t R, const float* bias, const int32_t* pos,
+                       const float* weight, int64_t T, int32_t k, const void* residual,
+                       int64_t ldr, void* out, lq_dtype out_dtype, int64_t ldo, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
