@@ -7,15 +7,54 @@
 namespace lq {
 namespace f6 {
 
-__device__ __forceinline__ float activate(float z, int act) {
+// 1 / (1 + exp(-x)) to a few 2^-24 of itself (hardware exponential and
+// reciprocal, 1 unit in the last place each); 0 and 1 far out.
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
+}
+
+__device__ __forceinline__ void activate4(float (&z)[4], int act) {
   switch (act) {
-    case LQ_ACT_RELU: return z < 0.f ? 0.f : z;           // a NaN stays one
-    case LQ_ACT_SILU: return z / (1.f + expf(-z));
-    case LQ_ACT_GELU: return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    case LQ_ACT_GELU_TANH:
-      return 0.5f * z * (1.f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-    default: return z;
+    case LQ_ACT_RELU:
+#pragma unroll
+      for (int c = 0; c < 4; ++c) z[c] = z[c] < 0.f ? 0.f : z[c];     // a NaN stays one
+      break;
+    case LQ_ACT_SILU:
+#pragma unroll
+      for (int c = 0; c < 4; ++c) z[c] *= sigmoid(z[c]);
+      break;
+    case LQ_ACT_GELU:
+#pragma unroll
+      for (int c = 0; c < 4; ++c) z[c] = 0.5f * z[c] * (1.f + erff(z[c] * 0.70710678118654752f));
+      break;
+    case LQ_ACT_GELU_TANH:                                            // (1 + tanh u) / 2 = sigmoid(2 u)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        z[c] *= sigmoid(1.59576912160573071f * (z[c] + 0.044715f * z[c] * z[c] * z[c]));
+      break;
+    default: break;
   }
+}
+
+// -s and bias of four rows (the tiles hold -sum); rows past the last repeat it.
+struct RowScales {
+  float s[4], b[4];
+};
+__device__ __forceinline__ RowScales row_scales(const float* s, const float* bias, int row, int n) {
+  RowScales r;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int at = row + max(min(c, n - 1), 0);
+    r.s[c] = n > 0 ? -s[at] : 0.f;
+    r.b[c] = n > 0 && bias ? bias[at] : 0.f;
+  }
+  return r;
+}
+__device__ __forceinline__ void scaled(const float4& v, const RowScales& r, float (&z)[4]) {
+  z[0] = v.x * r.s[0] + r.b[0];
+  z[1] = v.y * r.s[1] + r.b[1];
+  z[2] = v.z * r.s[2] + r.b[2];
+  z[3] = v.w * r.s[3] + r.b[3];
 }
 
 __device__ __forceinline__ float load_typed(const void* p, int dt, int64_t i) {
@@ -30,12 +69,27 @@ __device__ __forceinline__ uint16_t round16(float v, int dt) {
   return v != v ? uint16_t{0x7FC0} : float_to_bf16_bits_rne(v);
 }
 
-// y[0 .. 3]: the outputs of columns o .. o + 3 of one token, `n` of them
-// inside; adds the residual and stores.  `wide`: 4 outputs at o can go in
-// one store (and load) of 8 or 16 bytes.
-__device__ __forceinline__ void finish4(float (&y)[4], int n, bool wide, const void* residual,
-                                        int64_t at_residual, void* out, int64_t at, int dt) {
-  if (wide && n == 4) {
+// `wide`: four consecutive outputs go in one access of 8 or 16 bytes.
+struct OutputTypes {
+  int dt;
+  bool wide;
+};
+__host__ __device__ __forceinline__ OutputTypes output_types(const void* out, int64_t ldo,
+                                                             const void* residual, int64_t ldr,
+                                                             int dt) {
+  const uint64_t esz = dt == LQ_F32 ? 4 : 2;
+  uint64_t bits = reinterpret_cast<uint64_t>(out) | static_cast<uint64_t>(ldo) * esz;
+  if (residual) bits |= reinterpret_cast<uint64_t>(residual) | static_cast<uint64_t>(ldr) * esz;
+  return {dt, bits % (4 * esz) == 0};
+}
+
+// y[0 .. 3]: outputs of four columns of one token, the first n of them
+// inside; adds the residual and stores.
+__device__ __forceinline__ void finish4(float (&y)[4], int n, const OutputTypes& types,
+                                        const void* residual, int64_t at_residual, void* out,
+                                        int64_t at) {
+  const int dt = types.dt;
+  if (types.wide && n == 4) {
     if (dt == LQ_F32) {
       if (residual) {
         const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(residual) + at_residual);

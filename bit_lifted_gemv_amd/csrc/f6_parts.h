@@ -19,20 +19,24 @@
 // block with an infinity or a NaN has e = 255, which the matrix cores read
 // as NaN: its token's results are all NaN.
 //
-// Image.  A token's positions come in groups of 4 H blocks (H = 2 for the
-// 32 x 32 x 64 instruction, H = 4 for the 16 x 16 x 128 one); lane group h
-// holds block 4 h + u of the group at step u < 4, so that its four sign
-// words of the group are one 16-byte load.  Per token and group:
+// Image.  A token's positions come in groups of H U blocks: H = 2, U = 2 for
+// the 32 x 32 x 64 instruction, H = 4, U = 4 for the 16 x 16 x 128 one.  Per
+// token and group:
 //   [u][part][h] the first 16 bytes of an operand (24 bytes, 32 x 6 bits),
-//   [u][part][h] its last 8, then [h] the four exponent bytes (u = byte).
-// A group takes 96 H NP + 16 bytes, an odd number of 16-byte chunks, so
-// rows of groups in LDS start in different banks.  Element 8 q + t of a
+//   [u][part][h] its last 8, then 16 bytes with the exponents, [h][u].
+// A group takes an odd number of 16-byte chunks, so rows of groups in LDS
+// start in different banks.  With H = 4, lane group h holds block 4 h + u of
+// the group at step u, so that its four sign words are one 16-byte load.
+// With H = 2 the same holds over a pair of groups (256 positions): block
+// 4 h + 2 j + u of the pair is (h, u) of its group j.  Element 8 q + t of a
 // block is its position 4 t + q: the order in which three shifts and four
 // bit selects turn a sign word into float4 +-1 (expand_signs).
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "lq_internal.h"
 
 namespace lq {
 namespace f6 {
@@ -46,11 +50,12 @@ typedef float f32x32 __attribute__((ext_vector_type(32)));
 
 constexpr int kPadPositions = 512;      // images cover whole multiples of this, zero past K
 
-constexpr int group_positions(int H) { return 128 * H; }
-constexpr int group_bytes(int H, int NP) { return 96 * H * NP + 16; }
-// Offsets of a group's three sections.
-constexpr int tail_offset(int H, int NP) { return 64 * H * NP; }
-constexpr int exp_offset(int H, int NP) { return 96 * H * NP; }
+constexpr int group_steps(int H) { return H == 2 ? 2 : 4; }
+constexpr int group_positions(int H) { return 32 * H * group_steps(H); }
+// Offsets of a group's sections, and its length.
+constexpr int tail_offset(int H, int NP) { return 16 * H * group_steps(H) * NP; }
+constexpr int exp_offset(int H, int NP) { return 24 * H * group_steps(H) * NP; }
+constexpr int group_bytes(int H, int NP) { return exp_offset(H, NP) + 16; }
 
 inline int64_t padded_positions(int64_t K) {
   return (K + kPadPositions - 1) / kPadPositions * kPadPositions;
@@ -83,6 +88,28 @@ __device__ __forceinline__ i32x8 expand_signs(uint32_t w, uint32_t two) {
 __device__ __forceinline__ uint32_t block_exponent(uint32_t largest) {
   const int f = static_cast<int>(largest >> 23);
   return f == 255 ? 255u : static_cast<uint32_t>(max(f - 2, 12));
+}
+
+// Eight 16-bit values of a 16-byte load.
+__device__ __forceinline__ void unpack8(const uint4& v, bool bf16, float* x) {
+  const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (bf16) {
+      x[2 * i] = __uint_as_float(q[i] << 16);
+      x[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+    } else {
+      x[2 * i] = f16_bits_to_float(static_cast<uint16_t>(q[i]));
+      x[2 * i + 1] = f16_bits_to_float(static_cast<uint16_t>(q[i] >> 16));
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t largest_bits(const float (&x)[32]) {
+  uint32_t largest = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) largest = max(largest, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  return largest;
 }
 
 // The parts of a block of 32 values (x in position order), whose scale byte

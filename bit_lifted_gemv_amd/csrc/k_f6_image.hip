@@ -26,26 +26,22 @@ __global__ void __launch_bounds__(256) f6_image_kernel(const uint16_t* __restric
     const int k = 32 * b + 8 * j;               // K % 8 == 0: a chunk is all in or out
     uint4 v = make_uint4(0, 0, 0, 0);
     if (k < K && row != zero_row) v = *reinterpret_cast<const uint4*>(a + row * lda + k);
-    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (DT == LQ_BF16) {
-        x[8 * j + 2 * i] = __uint_as_float(q[i] << 16);
-        x[8 * j + 2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
-      } else {
-        x[8 * j + 2 * i] = f16_bits_to_float(static_cast<uint16_t>(q[i]));
-        x[8 * j + 2 * i + 1] = f16_bits_to_float(static_cast<uint16_t>(q[i] >> 16));
-      }
-    }
+    unpack8(v, DT == LQ_BF16, x + 8 * j);
   }
-  uint32_t largest = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j) largest = max(largest, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-  const uint32_t e = block_exponent(largest);
+  const uint32_t e = block_exponent(largest_bits(x));
   u32x6 part[NP];
   split_block<NP>(x, e, part);
-  const int per = 4 * H;                        // blocks per group
-  const int c = b / per, r = b % per, h = r / 4, u = r % 4;
+  constexpr int U = group_steps(H), per = H * U;  // blocks per group
+  int c, h, u;                                    // this block's group and place
+  if (H == 2) {
+    c = b / 8 * 2 + (b >> 1 & 1);
+    h = b >> 2 & 1;
+    u = b & 1;
+  } else {
+    c = b / per;
+    h = b / U % H;
+    u = b % U;
+  }
   uint8_t* g = img + (row * (blocks / per) + c) * group_bytes(H, NP);
 #pragma unroll
   for (int p = 0; p < NP; ++p) {
@@ -54,7 +50,7 @@ __global__ void __launch_bounds__(256) f6_image_kernel(const uint16_t* __restric
         make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
     *reinterpret_cast<uint2*>(g + tail_offset(H, NP) + 8 * at) = make_uint2(part[p][4], part[p][5]);
   }
-  g[exp_offset(H, NP) + 4 * h + u] = static_cast<uint8_t>(e);
+  g[exp_offset(H, NP) + U * h + u] = static_cast<uint8_t>(e);
 }
 
 template <int H, int NP>

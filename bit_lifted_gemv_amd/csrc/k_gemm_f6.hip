@@ -3,18 +3,20 @@
 // f6_parts.h), with the epilogue of lq_gemm_ep and the ragged expert runs of
 // lq_gemm_grouped.
 //
-// Tile.  A workgroup of 8 waves takes 128 WR rows of the weights and 32 TT
-// tokens; the weights cost 1/8 byte per position and the parts 2.3, so the
-// tile is tall.  WK = 8 / WR waves share each 128-row strip and split the
-// positions of a stage; every wave holds 128 rows x 32 TT tokens of sums
-// (4 TT tiles of 32 x 32) and uses each operand it reads from LDS four times.
-// A stage is SG groups of 256 positions (SG = 2 for WR = 1, so that each of
-// the eight waves has a step), copied to LDS by loads that write it directly
-// (buffer_load ... lds, 16 bytes per lane): the tokens' rows of parts, then
-// 32 bytes of signs per row and group.  A ring of S stages; a wave reads an
-// operand of the next step into the registers of the one it has just used,
-// so the only wait in the loop is the stage barrier, which sits behind the
-// first products of a step.
+// Tile.  A workgroup of WR WK waves takes 128 WR rows of the weights and 32 TT
+// tokens; the weights cost 1/8 byte per position and the parts 2.4, so the
+// tile is tall.  WK waves share each 128-row strip and split the positions of
+// a stage; every wave holds 128 rows x 32 TT tokens of sums (4 TT tiles of
+// 32 x 32) and uses each operand it reads from LDS four times.  Operands come
+// to LDS by loads that write it directly (buffer_load ... lds, 16 bytes per
+// lane): the tokens' parts in stages of SEC groups of 128 positions (a ring
+// of S), the signs in units of 256 positions, 32 bytes per row (two units; a
+// 16-byte piece per row and stage would ask L2 for the same lines twice as
+// often).  A wave reads an operand of the next step into the registers of the
+// one it has just used, so the only wait in the loop is the stage barrier,
+// which sits behind the first products of a step.  Workgroups of four waves
+// use half a compute unit's LDS, so that two of them share it and one's
+// barriers, first loads and epilogue are covered by the other's products.
 //
 // The loads to LDS are inline assembly (they have no output register) so
 // that the waits on them can be counted by hand: the compiler would drain
@@ -70,33 +72,39 @@ __device__ __forceinline__ i32x4 resource(const void* p, uint32_t bytes) {
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <int NP, int WR, int TT>
+template <int NP, int WR, int WK, int TT>
 struct Shape {
-  static constexpr int WK = 8 / WR;
-  static constexpr int SG = WR == 1 ? 2 : 1;
-  static constexpr int NU = 4 * SG / WK;               // steps of a wave per stage
+  static constexpr int NW = WR * WK;                   // waves
+  static constexpr int SEC = WK == 4 ? 2 : 1;          // groups per stage
+  static constexpr int NU = 2 * SEC / WK;              // steps of a wave per stage
+  static constexpr int UNIT = 2 / SEC;                 // stages per unit of signs
   static constexpr int TOK = 32 * TT;
   static constexpr int ROWS = 128 * WR;
   static constexpr int GB = group_bytes(2, NP);
   static constexpr int CH = GB / 16;
-  static constexpr int IMG_CHUNKS = SG * TOK * CH;
+  static constexpr int IMG_CHUNKS = SEC * TOK * CH;
   static constexpr int IMG_LOADS = (IMG_CHUNKS + 63) / 64;
-  static constexpr int W_LOADS = SG * ROWS * 2 / 64;
-  static constexpr int LOADS = (IMG_LOADS + W_LOADS + 7) / 8;   // per wave and stage
-  static constexpr int STAGE = (IMG_LOADS + W_LOADS) * 1024;
-  static constexpr int RING = 163840 / STAGE;
+  static constexpr int IL = (IMG_LOADS + NW - 1) / NW;  // loads of parts per wave and stage
+  static constexpr int WL = ROWS / 32 / NW;             // loads of signs per wave and unit
+  static constexpr int STAGE = IMG_LOADS * 1024;
+  static constexpr int SIGNS = ROWS * 32;               // a unit of signs
+  static constexpr int MAX_LDS = NW == 4 ? 81920 : 163840;  // two workgroups per unit, or one
+  static constexpr int RING = (MAX_LDS - 2 * SIGNS) / STAGE;
   static constexpr int S = RING > 4 ? 4 : RING;
+  // loads that may still be on their way when the next stage must have
+  // landed: those of the stages behind it, less those behind its signs
+  static constexpr int WAIT = (UNIT == 1 && S > 3 ? 1 : S - 2) * IL;
   static constexpr int PITCH = 132;                    // floats per token in the final exchange
-  static constexpr int EXCHANGE = 8 * 32 * PITCH * 4;
-  static constexpr int LDS = S * STAGE > EXCHANGE ? S * STAGE : EXCHANGE;
-  static_assert(S >= 2 && LDS <= 163840);
-  static_assert((S - 1) * LOADS < 64);
+  static constexpr int EXCHANGE = NW * 32 * PITCH * 4;
+  static constexpr int LDS = S * STAGE + 2 * SIGNS > EXCHANGE ? S * STAGE + 2 * SIGNS : EXCHANGE;
+  static_assert(S >= 2 && LDS <= MAX_LDS && NU >= 1 && WL >= 1);
+  static_assert((S - 1) * IL + WL < 64);
 };
 
-template <int NP, int WR, int TT>
-__global__ void __launch_bounds__(512, 2) gemm_f6_kernel(F6Product a) {
-  using P = Shape<NP, WR, TT>;
-  constexpr int WK = P::WK, SG = P::SG, NU = P::NU, TOK = P::TOK, ROWS = P::ROWS;
+template <int NP, int WR, int WK, int TT>
+__global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
+  using P = Shape<NP, WR, WK, TT>;
+  constexpr int SEC = P::SEC, NU = P::NU, TOK = P::TOK, ROWS = P::ROWS, NW = P::NW;
   extern __shared__ __align__(1024) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = uniform(tid >> 6);
@@ -130,54 +138,60 @@ __global__ void __launch_bounds__(512, 2) gemm_f6_kernel(F6Product a) {
   const int out0 = rt * outs;
   const int out_m = a.gated ? half_m : a.m;
 
-  // ---- sources of this wave's loads: loads wave, wave + 8, ... of a stage
+  // ---- sources of this wave's loads: loads wave, wave + NW, ... of a stage
+  // (past the last one: the last again) and of a unit of signs
   const i32x4 ires = resource(a.img, a.img_bytes);
   const i32x4 wres = resource(w, static_cast<uint32_t>(a.m) * a.ldw * 4u);
-  uint32_t src[P::LOADS];
-  i32x4 from[P::LOADS];
+  uint32_t part_src[P::IL], sign_src[P::WL];
 #pragma unroll
-  for (int i = 0; i < P::LOADS; ++i) {
-    const int l = min(wave + 8 * i, P::IMG_LOADS + P::W_LOADS - 1);
-    from[i] = l < P::IMG_LOADS ? ires : wres;
-    if (l < P::IMG_LOADS) {
-      const int c = min(l * 64 + lane, P::IMG_CHUNKS - 1);
-      const int sg = c / (TOK * P::CH), t = c / P::CH % TOK, ch = c % P::CH;
-      int r = row0 + min(t, tokens - 1);
-      if (a.rows) {
-        r = a.rows[r];
-        r = r < 0 || r >= a.src_rows ? a.src_rows : r;   // the image's row of zeros
-      }
-      src[i] = static_cast<uint32_t>(r) * a.img_row_bytes + sg * P::GB + ch * 16;
-    } else {
-      const int c = (l - P::IMG_LOADS) * 64 + lane;
-      const int sg = c / (2 * ROWS), lr = c / 2 % ROWS, h = c & 1;
-      int row;
-      if (a.gated)
-        row = min(out0 + lr / 128 * 64 + (lr & 63), half_m - 1) + ((lr >> 6) & 1) * half_m;
-      else
-        row = min(out0 + lr, a.m - 1);
-      src[i] = static_cast<uint32_t>(row) * a.ldw * 4u + sg * 32 + h * 16;
+  for (int i = 0; i < P::IL; ++i) {
+    const int c = min(min(wave + NW * i, P::IMG_LOADS - 1) * 64 + lane, P::IMG_CHUNKS - 1);
+    const int sec = c / (TOK * P::CH), t = c / P::CH % TOK, ch = c % P::CH;
+    int r = row0 + min(t, tokens - 1);
+    if (a.rows) {
+      r = a.rows[r];
+      r = r < 0 || r >= a.src_rows ? a.src_rows : r;   // the image's row of zeros
     }
+    part_src[i] = static_cast<uint32_t>(r) * a.img_row_bytes + sec * P::GB + ch * 16;
   }
-  const int stages = a.groups / SG;
-  auto issue = [&](int stage, int slot) {
-    stage = min(stage, stages - 1);                    // past the end: a slot nobody reads
 #pragma unroll
-    for (int i = 0; i < P::LOADS; ++i) {
-      const int l = min(wave + 8 * i, P::IMG_LOADS + P::W_LOADS - 1);
-      const uint32_t to = lds_address(lds) + slot * P::STAGE + l * 1024;
-      load_to_lds(to, src[i], from[i], stage * SG * (l < P::IMG_LOADS ? P::GB : 32));
-    }
+  for (int i = 0; i < P::WL; ++i) {
+    const int c = (wave + NW * i) * 64 + lane, lr = c / 2;
+    int row;
+    if (a.gated)
+      row = min(out0 + lr / 128 * 64 + (lr & 63), half_m - 1) + ((lr >> 6) & 1) * half_m;
+    else
+      row = min(out0 + lr, a.m - 1);
+    sign_src[i] = static_cast<uint32_t>(row) * a.ldw * 4u + (c & 1) * 16;
+  }
+  const int stages = a.groups / SEC, units = a.groups / 2;
+  const uint32_t lds0 = lds_address(lds);
+  constexpr int SIGNS_AT = P::S * P::STAGE;
+  // past the end: the last one again, into a slot nobody reads
+  auto issue_parts = [&](int stage, int slot) {
+    const uint32_t off = min(stage, stages - 1) * SEC * P::GB;
+#pragma unroll
+    for (int i = 0; i < P::IL; ++i)
+      load_to_lds(lds0 + slot * P::STAGE + min(wave + NW * i, P::IMG_LOADS - 1) * 1024,
+                  part_src[i], ires, off);
+  };
+  auto issue_signs = [&](int unit) {
+    const uint32_t off = min(unit, units - 1) * 32;
+#pragma unroll
+    for (int i = 0; i < P::WL; ++i)
+      load_to_lds(lds0 + SIGNS_AT + (unit & 1) * P::SIGNS + (wave + NW * i) * 1024, sign_src[i],
+                  wres, off);
   };
 
   // ---- operands
   const int i32 = lane & 31, h = lane >> 5;
   const uint32_t two = held(0x22222222u);
   f32x16 acc[4][TT] = {};
-  i32x8 b[TT][NP];
+  i32x8 b[TT][NP], sign[4];
   uint32_t word[4], ex[TT];
-  auto step_group = [&](int u) { return SG == 2 ? wk >> 2 : 0; };
-  auto step_u = [&](int u) { return SG == 2 ? wk & 3 : wk * NU + u; };
+  int scale[TT][NP];
+  auto step_group = [&](int) { return SEC == 2 ? wk >> 1 : 0; };
+  auto step_u = [&](int u) { return SEC == 2 ? wk & 1 : wk * NU + u; };
   auto read_part = [&](int slot, int u, int t, int p) {
     const uint8_t* g = lds + slot * P::STAGE + step_group(u) * TOK * P::GB +
                        (32 * t + i32) * P::GB;
@@ -187,70 +201,106 @@ __global__ void __launch_bounds__(512, 2) gemm_f6_kernel(F6Product a) {
     b[t][p][0] = lo.x; b[t][p][1] = lo.y; b[t][p][2] = lo.z; b[t][p][3] = lo.w;
     b[t][p][4] = hi.x; b[t][p][5] = hi.y; b[t][p][6] = 0; b[t][p][7] = 0;
   };
-  auto read_exponent = [&](int slot, int u, int t) {
-    const uint8_t* g = lds + slot * P::STAGE + step_group(u) * TOK * P::GB +
-                       (32 * t + i32) * P::GB + exp_offset(2, NP) + 4 * h;
-    ex[t] = *reinterpret_cast<const uint32_t*>(g) >> (8 * step_u(u)) & 255u;
+  auto read_exponents = [&](int slot, int u) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      ex[t] = *reinterpret_cast<const uint32_t*>(
+          lds + slot * P::STAGE + step_group(u) * TOK * P::GB + (32 * t + i32) * P::GB +
+          exp_offset(2, NP));
   };
-  auto read_words = [&](int slot, int u) {
+  auto set_scales = [&](int u) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int p = 0; p < NP; ++p)
+        scale[t][p] = static_cast<int>(ex[t] >> (16 * h + 8 * step_u(u)) & 255u) - 4 * p;
+  };
+  // j: group of the pair that the unit covers
+  auto read_words = [&](int unit, int j, int u) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       word[q] = *reinterpret_cast<const uint32_t*>(
-          lds + slot * P::STAGE + P::IMG_LOADS * 1024 + step_group(u) * ROWS * 32 +
-          (wr * 128 + 32 * q + i32) * 32 + h * 16 + 4 * step_u(u));
+          lds + SIGNS_AT + (unit & 1) * P::SIGNS + (wr * 128 + 32 * q + i32) * 32 + h * 16 +
+          8 * (j + step_group(u)) + 4 * step_u(u));
   };
 
+  issue_signs(0);
+  issue_parts(0, 0);
+  issue_signs(1);
 #pragma unroll
-  for (int i = 0; i < P::S; ++i) issue(i, i);
-  wait_and_barrier<(P::S - 1) * P::LOADS>();
-  read_words(0, 0);
+  for (int i = 1; i < P::S; ++i) issue_parts(i, i);
+  wait_and_barrier<P::WL + (P::S - 1) * P::IL>();
+  read_words(0, 0, 0);
+  read_exponents(0, 0);
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    read_exponent(0, 0, t);
+  for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int p = 0; p < NP; ++p) read_part(0, 0, t, p);
-  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) sign[q] = expand_signs(word[q], two);
+  set_scales(0);
 
+  // The order below is kept by the scheduling barriers: four products, then
+  // the reads that refill their operand; the next step's signs are expanded
+  // between the step's last products, each as its operand is free.
   int slot = 0;
-  for (int stage = 0; stage < stages; ++stage) {
-    const int next = slot + 1 == P::S ? 0 : slot + 1;
+  for (int unit = 0; unit < units; ++unit) {
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const bool last = u == NU - 1;
-      const int nslot = last ? next : slot, nu = last ? 0 : u + 1;
-      i32x8 sign[4];
+    for (int j = 0; j < P::UNIT; ++j) {
+      const int next = slot + 1 == P::S ? 0 : slot + 1;
+      const bool unit_ends = j == P::UNIT - 1;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) sign[q] = expand_signs(word[q], two);
+      for (int u = 0; u < NU; ++u) {
+        const bool last = u == NU - 1;
+        const int nslot = last ? next : slot, nu = last ? 0 : u + 1;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int e = static_cast<int>(ex[t]);
+        for (int t = 0; t < TT; ++t) {
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
+          for (int p = 0; p < NP; ++p) {
+            const bool refill = t == TT - 1 && p == NP - 1;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) acc[q][t] = mfma(sign[q], b[t][p], acc[q][t], e - 4 * p);
-          if (t == 0 && p == 0) {
-            if (last) {
-              // the next stage has landed and nobody reads this one any more
-              wait_and_barrier<(P::S - 2) * P::LOADS>();
-              issue(stage + P::S, slot);
+            for (int q = 0; q < 4; ++q) {
+              acc[q][t] = mfma(sign[q], b[t][p], acc[q][t], scale[t][p]);
+              if (refill) {
+                __builtin_amdgcn_sched_barrier(0);
+                sign[q] = expand_signs(word[q], two);
+              }
             }
-            read_words(nslot, nu);
+            __builtin_amdgcn_sched_barrier(0);
+            if (t == 0 && p == 0) {
+              if (last) {
+                // the next stage has landed and nobody reads this one any more
+                wait_and_barrier<P::WAIT>();
+                if (unit_ends) issue_signs(unit + 2);
+                issue_parts(unit * P::UNIT + j + P::S, slot);
+              }
+              if (last && unit_ends) read_words(unit + 1, 0, nu);
+              else read_words(unit, last ? j + 1 : j, nu);
+              read_exponents(nslot, nu);
+            }
+            read_part(nslot, nu, t, p);
+            if (refill) set_scales(nu);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          read_part(nslot, nu, t, p);
         }
-        read_exponent(nslot, nu, t);
       }
+      slot = next;
     }
-    slot = next;
   }
   wait_and_barrier<0>();
 
-  // ---- the exchange: [wave][token][row], 32 tokens at a time
+  // ---- the exchange: [wave][token][row], 32 tokens at a time.  A thread
+  // keeps its four output columns and takes every (512 / quads)-th token, so
+  // scales, bias and column offsets are its own for the whole tile.
   float* ex32 = reinterpret_cast<float*>(lds);
-  const int64_t esz = a.out_dt == LQ_F32 ? 4 : 2;
-  const bool wide_out = (reinterpret_cast<uint64_t>(a.out) | static_cast<uint64_t>(a.ldo * esz)) % (4 * esz) == 0 &&
-                        (!a.residual || (reinterpret_cast<uint64_t>(a.residual) |
-                                         static_cast<uint64_t>(a.ldr * esz)) % (4 * esz) == 0);
+  const int shift = __builtin_ctz(ROWS / 4) - (a.gated ? 1 : 0);   // log2 of the quads of a row
+  const int o = (tid & ((1 << shift) - 1)) * 4, tk0 = tid >> shift, tk_step = 64 * NW >> shift;
+  const int n = min(4, out_m - (out0 + o));
+  const int strip = a.gated ? o / 64 : o / 128;
+  const float* z0 = ex32 + strip * 32 * P::PITCH + (a.gated ? o % 64 : o % 128);
+  const OutputTypes types = output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt);
+  RowScales rs = row_scales(s, bias, out0 + o, n), up = rs;
+  if (a.gated) up = row_scales(s, bias, half_m + out0 + o, n);
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     if (t) __syncthreads();
@@ -262,48 +312,36 @@ __global__ void __launch_bounds__(512, 2) gemm_f6_kernel(F6Product a) {
             make_float4(acc[q][t][4 * r4], acc[q][t][4 * r4 + 1], acc[q][t][4 * r4 + 2],
                         acc[q][t][4 * r4 + 3]);
     __syncthreads();
-    const int quads = outs / 4;
-    for (int j = tid; j < 32 * quads; j += 512) {
-      const int tk = j / quads, o = (j - tk * quads) * 4;
-      const int token = 32 * t + tk;
-      const int n = min(4, out_m - (out0 + o));
-      if (token >= tokens || n <= 0) continue;
-      float y[4];
-      const int strip = a.gated ? o / 64 : o / 128, at0 = a.gated ? o % 64 : o % 128;
-      auto sum = [&](int row_in_strip, int64_t row, float (&z)[4]) {
-        float4 v = *reinterpret_cast<const float4*>(ex32 + (strip * 32 + tk) * P::PITCH + row_in_strip);
+    const int stop = n > 0 ? min(32, tokens - 32 * t) : 0;
+    for (int tk = tk0; tk < stop; tk += tk_step) {
+      const float* z = z0 + tk * P::PITCH;
+      auto sum = [&](const float* from) {              // the WK partial sums, in order
+        float4 v = *reinterpret_cast<const float4*>(from);
 #pragma unroll
         for (int k = 1; k < WK; ++k) {
-          const float4 x = *reinterpret_cast<const float4*>(
-              ex32 + ((k * WR + strip) * 32 + tk) * P::PITCH + row_in_strip);
+          const float4 x = *reinterpret_cast<const float4*>(from + k * WR * 32 * P::PITCH);
           v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
         }
-        const float raw[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int64_t rr = row + min(c, n - 1);
-          z[c] = -raw[c] * s[rr] + (bias ? bias[rr] : 0.f);
-        }
+        return v;
       };
-      sum(at0, out0 + o, y);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] = activate(y[c], a.act);
+      float y[4];
+      scaled(sum(z), rs, y);
+      activate4(y, a.act);
       if (a.gated) {
-        float up[4];
-        sum(64 + at0, static_cast<int64_t>(half_m) + out0 + o, up);
+        float g[4];
+        scaled(sum(z + 64), up, g);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] *= up[c];
+        for (int c = 0; c < 4; ++c) y[c] *= g[c];
       }
-      const int64_t row = row0 + token;
-      finish4(y, n, wide_out, a.residual, row * a.ldr + out0 + o, a.out, row * a.ldo + out0 + o,
-              a.out_dt);
+      const int64_t row = row0 + 32 * t + tk;
+      finish4(y, n, types, a.residual, row * a.ldr + out0 + o, a.out, row * a.ldo + out0 + o);
     }
   }
 }
 
-template <int NP, int WR, int TT>
+template <int NP, int WR, int WK, int TT>
 hipError_t launch(const F6Product& p, hipStream_t st) {
-  using P = Shape<NP, WR, TT>;
+  using P = Shape<NP, WR, WK, TT>;
   F6Product a = p;
   const int64_t outs = a.gated ? P::ROWS / 2 : P::ROWS;
   const int64_t out_m = a.gated ? a.m / 2 : a.m;
@@ -313,11 +351,11 @@ hipError_t launch(const F6Product& p, hipStream_t st) {
   a.token_tiles = static_cast<int>(tiles);
   const int64_t grid = (tiles * a.row_tiles + 7) / 8 * 8;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  auto* k = gemm_f6_kernel<NP, WR, TT>;
+  auto* k = gemm_f6_kernel<NP, WR, WK, TT>;
   static const hipError_t big = hipFuncSetAttribute(
       reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, P::LDS);
   if (big != hipSuccess) return big;
-  k<<<dim3(static_cast<uint32_t>(grid)), 512, P::LDS, st>>>(a);
+  k<<<dim3(static_cast<uint32_t>(grid)), 64 * P::NW, P::LDS, st>>>(a);
   return hipGetLastError();
 }
 
@@ -333,12 +371,12 @@ hipError_t choose(const F6Product& p, hipStream_t st) {
     return (p.R / (32 * TT) + runs) * ((out_m + outs - 1) / outs);
   };
   const int64_t cus = num_cus();
-  if constexpr (NP == 3)                               // (4, 2) with four parts spills
-    if (two && count(4, 2) >= 2 * cus) return launch<NP, 4, 2>(p, st);
-  if (two && count(2, 2) >= cus) return launch<NP, 2, 2>(p, st);
-  if (count(4, 1) >= 2 * cus) return launch<NP, 4, 1>(p, st);
-  if (count(2, 1) >= cus) return launch<NP, 2, 1>(p, st);
-  return launch<NP, 1, 1>(p, st);
+  if constexpr (NP == 3)
+    if (two && count(4, 2) >= cus) return launch<NP, 4, 1, 2>(p, st);
+  if (two && count(2, 2) >= cus) return launch<NP, 2, 4, 2>(p, st);
+  if (count(4, 1) >= 2 * cus) return launch<NP, 4, 1, 1>(p, st);
+  if (count(2, 1) >= cus) return launch<NP, 2, 2, 1>(p, st);
+  return launch<NP, 1, 4, 1>(p, st);
 }
 
 }  // namespace

@@ -12,7 +12,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ z, 
                                                    const int* __restrict__ pos,
                                                    const float* __restrict__ weight, int T, int k,
                                                    const void* residual, int64_t ldr, void* out,
-                                                   int64_t ldo, int dt, int ldz, bool wide) {
+                                                   int64_t ldo, int ldz, f6::OutputTypes types) {
   const int o = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (o >= m) return;
   for (int t = blockIdx.y; t < T; t += gridDim.y) {
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ z, 
       y[2] += w * v.z;
       y[3] += w * v.w;
     }
-    f6::finish4(y, min(4, m - o), wide, residual, t * ldr + o, out, t * ldo + o, dt);
+    f6::finish4(y, min(4, m - o), types, residual, t * ldr + o, out, t * ldo + o);
   }
 }
 
@@ -37,15 +37,12 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ z, 
 hipError_t launch_join(const float* z, int64_t R, int64_t m, int64_t ldz, const int* pos,
                        const float* weight, int64_t T, int k, const void* residual, int64_t ldr,
                        void* out, int64_t ldo, int dt, hipStream_t st) {
-  const int64_t esz = dt == LQ_F32 ? 4 : 2;
-  const auto bits = [](const void* p) { return reinterpret_cast<uint64_t>(p); };
-  const bool wide = (bits(out) | static_cast<uint64_t>(ldo * esz)) % (4 * esz) == 0 &&
-                    (!residual || (bits(residual) | static_cast<uint64_t>(ldr * esz)) % (4 * esz) == 0);
   const dim3 grid(static_cast<uint32_t>((m + 1023) / 1024),
                   static_cast<uint32_t>(T < 65535 ? T : 65535));
   join_kernel<<<grid, 256, 0, st>>>(z, static_cast<int>(R), static_cast<int>(m), pos, weight,
-                                    static_cast<int>(T), k, residual, ldr, out, ldo, dt,
-                                    static_cast<int>(ldz), wide);
+                                    static_cast<int>(T), k, residual, ldr, out, ldo,
+                                    static_cast<int>(ldz),
+                                    f6::output_types(out, ldo, residual, ldr, dt));
   return hipGetLastError();
 }
 

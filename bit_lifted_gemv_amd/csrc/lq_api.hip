@@ -177,6 +177,7 @@ lq_status f6_rows_out(const void* residual, int64_t ldr, const void* out, lq_dty
 }
 
 lq_status f6_workspace(const void* workspace, size_t have, size_t need) {
+  if (need == 0) return LQ_OK;
   if (!workspace) return fail(LQ_ERR_WORKSPACE, "workspace of %zu bytes required", need);
   if (have < need) return fail(LQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", have, need);
   if (!aligned(workspace, 256)) return fail(LQ_ERR_ALIGN, "workspace must be 256-byte aligned");
@@ -197,23 +198,37 @@ lq_status route_sizes(int64_t T, int64_t E, int32_t k) {
   return LQ_OK;
 }
 
-// How one product runs: the image's form and what the workspace holds.
+// How one product runs: on the few-row kernel (which splits its activations
+// itself) or on an operand image, and what the workspace holds.
 struct F6Plan {
-  int H, NP;
-  int64_t row_bytes, rows;
-  size_t z_at;                 // float32 rows of lq_gemm_join
+  bool few;
+  lq::F6FewPlan fp;
+  int NP;
+  int64_t row_bytes, image_rows;
+  size_t sums_at, z_at;        // slices' sums of the few-row kernel; float32 rows of lq_gemm_join
   int64_t ldz;
   size_t bytes;
 };
 
+constexpr int64_t kFewRows = 16, kFewRowsPerRun = 8;
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// rows: of the activations, R: of the product (grouped: in the sorted order).
 F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtype out_dtype,
-               bool grouped, bool join) {
+               bool gated, bool grouped, bool join) {
   F6Plan p{};
-  p.H = 2;
   p.NP = f6_parts_count(out_dtype);
-  p.row_bytes = lq::f6::row_bytes(K, p.H, p.NP);
-  p.rows = rows + (grouped ? 1 : 0);      // a row of zeros behind the last
-  p.bytes = (static_cast<size_t>(p.rows * p.row_bytes) + 255) / 256 * 256;
+  // few rows: up to 16 in all, or about 8 a run on average
+  p.few = R <= kFewRows || (grouped && R <= kFewRowsPerRun * (E < R ? E : R));
+  if (p.few) {
+    p.fp = lq::few_f6_plan(E, m, K, R < 1 ? 1 : R, gated, p.NP, grouped);
+    p.bytes = round256(p.fp.sums_bytes);
+  } else {
+    p.row_bytes = lq::f6::row_bytes(K, 2, p.NP);
+    p.image_rows = rows + (grouped ? 1 : 0);      // a row of zeros behind the last
+    p.bytes = round256(static_cast<size_t>(p.image_rows * p.row_bytes));
+  }
   if (join) {
     p.z_at = p.bytes;
     p.ldz = (m + 3) / 4 * 4;
@@ -222,14 +237,41 @@ F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtyp
   return p;
 }
 
-lq::F6Product f6_product(const uint32_t* w, int64_t m, int64_t K, int64_t ldw, const float* s,
-                         const float* bias, int act, int gated, const F6Plan& plan,
-                         const void* image) {
-  lq::F6Product p{};
-  p.img = static_cast<const uint8_t*>(image);
+// The product of a checked call: conversion where it is a launch of its own,
+// then the kernel.  p lacks only what the plan decides.
+hipError_t f6_run(lq::F6Product& p, const F6Plan& plan, int64_t K, const void* a, lq_dtype a_dt,
+                  int64_t lda, int64_t a_rows, void* workspace, hipStream_t st) {
+  if (plan.few) {
+    lq::F6Few f{};
+    p.groups = plan.fp.groups;
+    f.p = p;
+    f.a = a;
+    f.a_dt = a_dt;
+    f.lda = lda;
+    f.K = static_cast<int>(K);
+    f.kv = plan.fp.kv;
+    f.slices = plan.fp.slices;
+    f.slice_groups = plan.fp.slice_groups;
+    f.row_blocks = plan.fp.row_blocks;
+    f.blocks_per = plan.fp.blocks_per;
+    f.exchange_at = plan.fp.exchange_at;
+    f.sums = static_cast<float*>(workspace);
+    f.ldz = plan.fp.ldz;
+    return lq::launch_gemv_f6(f, plan.fp, plan.NP, st);
+  }
+  p.img = static_cast<const uint8_t*>(workspace);
   p.img_row_bytes = static_cast<uint32_t>(plan.row_bytes);
-  p.img_bytes = static_cast<uint32_t>(plan.rows * plan.row_bytes);
-  p.groups = static_cast<int>(lq::f6::padded_positions(K) / 256);
+  p.img_bytes = static_cast<uint32_t>(plan.image_rows * plan.row_bytes);
+  p.groups = static_cast<int>(lq::f6::padded_positions(K) / lq::f6::group_positions(2));
+  hipError_t e = lq::launch_f6_image(a, a_dt, a_rows, plan.image_rows > a_rows, K, lda, 2, plan.NP,
+                                     workspace, st);
+  if (e == hipSuccess) e = lq::launch_gemm_f6(p, plan.NP, st);
+  return e;
+}
+
+lq::F6Product f6_product(const uint32_t* w, int64_t m, int64_t ldw, const float* s,
+                         const float* bias, int act, int gated) {
+  lq::F6Product p{};
   p.w = w;
   p.m = static_cast<int>(m);
   p.ldw = static_cast<int>(ldw);
@@ -676,7 +718,9 @@ lq_status lq_gemm_ep_workspace_size(int64_t m, int64_t K, int64_t B, lq_dtype ou
   if (!valid_dtype(out_dtype)) return fail(LQ_ERR_DTYPE, "unknown dtype");
   const lq_status st = f6_sizes(1, m, K, B, out_dtype);
   if (st != LQ_OK) return st;
-  *bytes = f6_plan(1, m, K, B, B, out_dtype, false, false).bytes;
+  const size_t plain = f6_plan(1, m, K, B, B, out_dtype, false, false, false).bytes;
+  const size_t gated = f6_plan(1, m, K, B, B, out_dtype, true, false, false).bytes;
+  *bytes = plain > gated ? plain : gated;
   return ok();
 }
 
@@ -693,10 +737,10 @@ lq_status lq_gemm_ep(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw
   const int64_t width = gated ? m / 2 : m;
   st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
   if (st == LQ_OK) st = f6_rows_out(residual, ldr, out, out_dtype, ldo, width, B);
-  const auto plan = f6_plan(1, m, K, B, B, out_dtype, false, false);
+  const auto plan = f6_plan(1, m, K, B, B, out_dtype, gated != 0, false, false);
   if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
   if (st != LQ_OK) return st;
-  lq::F6Product p = f6_product(w_packed, m, K, ldw, s, bias, act, gated, plan, workspace);
+  lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, act, gated);
   p.residual = residual;
   p.ldr = ldr;
   p.out = out;
@@ -705,9 +749,7 @@ lq_status lq_gemm_ep(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw
   p.R = static_cast<int>(B);
   p.src_rows = static_cast<int>(B);
   const hipStream_t hs = as_stream(stream);
-  hipError_t e = lq::launch_f6_image(a_lift, lift_dtype, B, false, K, lda, plan.H, plan.NP,
-                                     workspace, hs);
-  if (e == hipSuccess) e = lq::launch_gemm_f6(p, plan.NP, hs);
+  const hipError_t e = f6_run(p, plan, K, a_lift, lift_dtype, lda, B, workspace, hs);
   return hip_status(e, "lq_gemm_ep launch");
 }
 
@@ -718,7 +760,9 @@ lq_status lq_gemm_grouped_workspace_size(int64_t E, int64_t m, int64_t K, int64_
   lq_status st = f6_sizes(E, m, K, a_rows, out_dtype);
   if (st == LQ_OK && (R < 0 || R > INT32_MAX)) st = fail(LQ_ERR_SHAPE, "R=%lld", (long long)R);
   if (st != LQ_OK) return st;
-  *bytes = f6_plan(E, m, K, a_rows, R, out_dtype, true, false).bytes;
+  const size_t plain = f6_plan(E, m, K, a_rows, R, out_dtype, false, true, false).bytes;
+  const size_t gated = f6_plan(E, m, K, a_rows, R, out_dtype, true, true, false).bytes;
+  *bytes = plain > gated ? plain : gated;
   return ok();
 }
 
@@ -743,10 +787,10 @@ lq_status lq_gemm_grouped(const uint32_t* w_packed, int64_t E, int64_t m, int64_
   const int64_t width = gated ? m / 2 : m;
   st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
   if (st == LQ_OK) st = f6_rows_out(nullptr, 0, out, out_dtype, ldo, width, R);
-  const auto plan = f6_plan(E, m, K, a_rows, R, out_dtype, true, false);
+  const auto plan = f6_plan(E, m, K, a_rows, R, out_dtype, gated != 0, true, false);
   if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
   if (st != LQ_OK) return st;
-  lq::F6Product p = f6_product(w_packed, m, K, ldw, s, bias, act, gated, plan, workspace);
+  lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, act, gated);
   p.out = out;
   p.ldo = ldo;
   p.out_dt = out_dtype;
@@ -756,9 +800,7 @@ lq_status lq_gemm_grouped(const uint32_t* w_packed, int64_t E, int64_t m, int64_
   p.rows = rows;
   p.src_rows = static_cast<int>(a_rows);
   const hipStream_t hs = as_stream(stream);
-  hipError_t e = lq::launch_f6_image(a_lift, lift_dtype, a_rows, true, K, lda, plan.H, plan.NP,
-                                     workspace, hs);
-  if (e == hipSuccess) e = lq::launch_gemm_f6(p, plan.NP, hs);
+  const hipError_t e = f6_run(p, plan, K, a_lift, lift_dtype, lda, a_rows, workspace, hs);
   return hip_status(e, "lq_gemm_grouped launch");
 }
 
@@ -769,7 +811,7 @@ lq_status lq_gemm_join_workspace_size(int64_t E, int64_t m, int64_t K, int64_t R
   lq_status st = f6_sizes(E, m, K, R, out_dtype);
   if (st == LQ_OK) st = join_sizes(T, k);
   if (st != LQ_OK) return st;
-  *bytes = f6_plan(E, m, K, R, R, out_dtype, true, true).bytes;
+  *bytes = f6_plan(E, m, K, R, R, out_dtype, false, true, true).bytes;
   return ok();
 }
 
@@ -790,14 +832,14 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
     return fail(LQ_ERR_ALIGN, "misaligned offsets, pos or weight");
   st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
   if (st == LQ_OK) st = f6_rows_out(residual, ldr, out, out_dtype, ldo, m, T);
-  const auto plan = f6_plan(E, m, K, R, R, out_dtype, true, true);
+  const auto plan = f6_plan(E, m, K, R, R, out_dtype, false, true, true);
   if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
   if (st != LQ_OK) return st;
   const hipStream_t hs = as_stream(stream);
   float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.z_at);
   hipError_t e = hipSuccess;
   if (R > 0) {
-    lq::F6Product p = f6_product(w_packed, m, K, ldw, s, bias, LQ_ACT_NONE, 0, plan, workspace);
+    lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, LQ_ACT_NONE, 0);
     p.out = z;
     p.ldo = plan.ldz;
     p.out_dt = LQ_F32;
@@ -805,8 +847,7 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
     p.offsets = offsets;
     p.E = static_cast<int>(E);
     p.src_rows = static_cast<int>(R);
-    e = lq::launch_f6_image(a_lift, lift_dtype, R, true, K, lda, plan.H, plan.NP, workspace, hs);
-    if (e == hipSuccess) e = lq::launch_gemm_f6(p, plan.NP, hs);
+    e = f6_run(p, plan, K, a_lift, lift_dtype, lda, R, workspace, hs);
   }
   if (e == hipSuccess)
     e = lq::launch_join(z, R, m, plan.ldz, pos, weight, T, k, residual, ldr, out, ldo, out_dtype,
@@ -836,10 +877,8 @@ lq_status lq_route(const void* logits, lq_dtype dtype, int64_t T, int64_t E, int
       !aligned(pos, 4) || !aligned(rows, 4) || !aligned(offsets, 4))
     return fail(LQ_ERR_ALIGN, "misaligned pointer");
   const size_t need = lq::route_workspace_bytes(T, static_cast<int>(E));
-  if (need) {
-    st = f6_workspace(workspace, workspace_bytes, need);
-    if (st != LQ_OK) return st;
-  }
+  st = f6_workspace(workspace, workspace_bytes, need);
+  if (st != LQ_OK) return st;
   return hip_status(lq::launch_route(logits, dtype, T, static_cast<int>(E), ld, valid, k, renorm,
                                      ids, weight, pos, rows, offsets, workspace,
                                      as_stream(stream)),

@@ -169,7 +169,7 @@ struct F6Product {
   const uint8_t* img;          // parts of the activations
   uint32_t img_row_bytes;
   uint32_t img_bytes;
-  int groups;                  // groups of 256 positions, even
+  int groups;                  // groups per image row (an even number for H = 2)
   const uint32_t* w;           // [E][m][ldw]
   int m, ldw;
   const float* s;              // [E][m]
@@ -187,6 +187,32 @@ struct F6Product {
   int src_rows;                // rows of the image (with `rows`, one more of zeros follows)
   int row_tiles, token_tiles;  // set by the launcher
 };
+
+// The same for at most 16 rows per matrix (k_gemv_f6.hip), which splits its
+// activations itself.
+struct F6FewPlan {
+  int T, kv;                   // 16-row tiles per unit, waves that share a unit
+  int groups;                  // groups of 512 positions
+  int slices, slice_groups;
+  int row_blocks, blocks_per;  // blocks of units, and how many a workgroup takes
+  int tiles;                   // of 16 rows (grouped: at most)
+  int exchange_at;             // LDS bytes before the exchange
+  int64_t ldz;
+  size_t sums_bytes;           // of the slices' sums, 0 for one slice
+};
+F6FewPlan few_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
+                      bool grouped);
+struct F6Few {
+  F6Product p;                 // groups: of 512 positions; no image
+  const void* a;
+  int a_dt;
+  int64_t lda;
+  int K;
+  int kv, slices, slice_groups, row_blocks, blocks_per, exchange_at;
+  float* sums;                 // [slices][R][ldz]
+  int64_t ldz;
+};
+hipError_t launch_gemv_f6(const F6Few& f, const F6FewPlan& plan, int NP, hipStream_t st);
 
 // 16-bit activations -> parts image (k_f6_image.hip); H = 2 or 4, NP = 3 or 4.
 hipError_t launch_f6_image(const void* a, lq_dtype dt, int64_t rows, bool zero_row, int64_t K,
