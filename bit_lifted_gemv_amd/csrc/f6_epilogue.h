@@ -36,18 +36,23 @@ __device__ __forceinline__ void activate4(float (&z)[4], int act) {
   }
 }
 
-// -s and bias of four rows (the tiles hold -sum); rows past the last repeat it.
+// -s and bias of rows row .. row + 3 of m (the tiles hold -sum); 0 past the
+// last.  Buffer loads: 16 bytes at any float's address, range checked.
 struct RowScales {
   float s[4], b[4];
 };
-__device__ __forceinline__ RowScales row_scales(const float* s, const float* bias, int row, int n) {
-  RowScales r;
+__device__ __forceinline__ RowScales row_scales(const float* s, const float* bias, int row, int m) {
+  RowScales r{};
+  auto load = [&](const float* p, float (&v)[4]) {
+    const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<float*>(p), (short)0, m * 4, 0x00020000);
+    const auto x = __builtin_amdgcn_raw_buffer_load_b128(res, row * 4, 0, 0);
+    __builtin_memcpy(v, &x, 16);
+  };
+  load(s, r.s);
+  if (bias) load(bias, r.b);
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const int at = row + max(min(c, n - 1), 0);
-    r.s[c] = n > 0 ? -s[at] : 0.f;
-    r.b[c] = n > 0 && bias ? bias[at] : 0.f;
-  }
+  for (int c = 0; c < 4; ++c) r.s[c] = -r.s[c];
   return r;
 }
 __device__ __forceinline__ void scaled(const float4& v, const RowScales& r, float (&z)[4]) {

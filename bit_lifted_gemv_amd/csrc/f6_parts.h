@@ -105,11 +105,21 @@ __device__ __forceinline__ void unpack8(const uint4& v, bool bf16, float* x) {
   }
 }
 
-__device__ __forceinline__ uint32_t largest_bits(const float (&x)[32]) {
-  uint32_t largest = 0;
+// Float32 bits of the largest |x| of 16-bit values, two per word (an infinity
+// or a NaN counts as larger than any number).
+template <int N>
+__device__ __forceinline__ uint32_t largest_bits(const uint4 (&v)[N], bool bf16) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 most = {0, 0};
 #pragma unroll
-  for (int j = 0; j < 32; ++j) largest = max(largest, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-  return largest;
+  for (int i = 0; i < N; ++i) {
+    const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, q[j] & 0x7FFF7FFFu));
+  }
+  const uint16_t m = most[0] > most[1] ? most[0] : most[1];
+  return __float_as_uint(bf16 ? bf16_bits_to_float(m) : f16_bits_to_float(m));
 }
 
 // The parts of a block of 32 values (x in position order), whose scale byte

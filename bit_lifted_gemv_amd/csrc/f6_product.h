@@ -9,10 +9,12 @@ namespace f6 {
 
 // Tiles of TOK rows in expert e's run (0 past the last expert).  Offsets come
 // from the device unchecked: runs are cut to [0, R].
-__device__ __forceinline__ int run_tiles(const F6Product& a, int e, int TOK) {
+__device__ __forceinline__ int run_tiles(const F6Product& a, int e, int TOK, int& lo, int& end) {
+  lo = end = 0;
   if (e >= a.E) return 0;
-  const int lo = min(max(a.offsets[e], 0), a.R), hi = min(max(a.offsets[e + 1], lo), a.R);
-  return (hi - lo + TOK - 1) / TOK;
+  lo = min(max(a.offsets[e], 0), a.R);
+  end = min(max(a.offsets[e + 1], lo), a.R);
+  return (end - lo + TOK - 1) / TOK;
 }
 
 __device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive
@@ -30,25 +32,27 @@ __device__ __forceinline__ int wave_total(int v) {
   return v;
 }
 
-// The expert of live tile `tile`, its first row and the end of its run.
-__device__ __forceinline__ void find_run(const F6Product& a, int tile, int TOK, int lane,
+// The expert of tile `tile`, its first row and the end of its run; false past
+// the last tile.
+__device__ __forceinline__ bool find_run(const F6Product& a, int tile, int TOK, int lane,
                                          int& expert, int& row0, int& row_end) {
   int before = 0;
   for (int e0 = 0; e0 < a.E; e0 += 64) {
-    const int n = run_tiles(a, e0 + lane, TOK);
+    int lo, end;
+    const int n = run_tiles(a, e0 + lane, TOK, lo, end);
     const int upto = before + wave_scan(n, lane);
     const uint64_t hit = __ballot(upto > tile);
     if (hit) {
       const int l = __builtin_ctzll(hit);
       const int first = __shfl(upto - n, l);
       expert = __builtin_amdgcn_readfirstlane(e0 + l);
-      const int lo = min(max(a.offsets[expert], 0), a.R);
-      row_end = __builtin_amdgcn_readfirstlane(min(max(a.offsets[expert + 1], lo), a.R));
-      row0 = __builtin_amdgcn_readfirstlane(lo + (tile - first) * TOK);
-      return;
+      row_end = __builtin_amdgcn_readfirstlane(__shfl(end, l));
+      row0 = __builtin_amdgcn_readfirstlane(__shfl(lo, l)) + (tile - first) * TOK;
+      return true;
     }
     before = __shfl(upto, 63);
   }
+  return false;
 }
 
 __device__ __forceinline__ uint32_t lds_address(const void* p) {

@@ -20,15 +20,17 @@ __global__ void __launch_bounds__(256) f6_image_kernel(const uint16_t* __restric
   const int64_t row = idx / blocks;
   if (row >= rows) return;
   const int b = static_cast<int>(idx - row * blocks);
-  float x[32];
+  uint4 v[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int k = 32 * b + 8 * j;               // K % 8 == 0: a chunk is all in or out
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (k < K && row != zero_row) v = *reinterpret_cast<const uint4*>(a + row * lda + k);
-    unpack8(v, DT == LQ_BF16, x + 8 * j);
+    v[j] = make_uint4(0, 0, 0, 0);
+    if (k < K && row != zero_row) v[j] = *reinterpret_cast<const uint4*>(a + row * lda + k);
   }
-  const uint32_t e = block_exponent(largest_bits(x));
+  float x[32];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpack8(v[j], DT == LQ_BF16, x + 8 * j);
+  const uint32_t e = block_exponent(largest_bits(v, DT == LQ_BF16));
   u32x6 part[NP];
   split_block<NP>(x, e, part);
   constexpr int U = group_steps(H), per = H * U;  // blocks per group

@@ -116,7 +116,9 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   int tiles = a.token_tiles;
   if (a.offsets) {
     tiles = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) tiles += uniform(wave_total(run_tiles(a, e0 + lane, TOK)));
+    int lo, end;
+    for (int e0 = 0; e0 < a.E; e0 += 64)
+      tiles += uniform(wave_total(run_tiles(a, e0 + lane, TOK, lo, end)));
   }
   const int total = tiles * RT;
   const int chunk = (total + 7) / 8;
@@ -299,8 +301,8 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   const int strip = a.gated ? o / 64 : o / 128;
   const float* z0 = ex32 + strip * 32 * P::PITCH + (a.gated ? o % 64 : o % 128);
   const OutputTypes types = output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt);
-  RowScales rs = row_scales(s, bias, out0 + o, n), up = rs;
-  if (a.gated) up = row_scales(s, bias, half_m + out0 + o, n);
+  RowScales rs = row_scales(s, bias, out0 + o, a.m), up = rs;
+  if (a.gated) up = row_scales(s, bias, half_m + out0 + o, a.m);
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     if (t) __syncthreads();

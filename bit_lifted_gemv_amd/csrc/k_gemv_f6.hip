@@ -5,19 +5,23 @@
 //
 // A workgroup of 8 waves takes up to 16 tokens, a slice of the positions and a
 // run of row blocks.  It first splits its slice of the tokens into float6
-// parts, into LDS (no launch of its own: spread over the workgroups it costs
-// less than one), then streams the signs from HBM straight into registers, 16
-// bytes per lane and 16-row tile of 512 positions, DEPTH of them ahead.  A
-// wave works on a unit of T tiles (each operand read from LDS serves T
-// products), alone (KV = 1) or with KV - 1 others on interleaved groups of
-// the slice where there are too few rows to fill the chip; those add their
-// sums through LDS in wave order.  Gated: the first half of a unit's tiles
-// are gate rows, the second half the same outputs' up rows.
+// parts, into LDS (its own, so no launch for them; the signs' first loads are
+// behind the activations' meanwhile), then streams the signs from HBM
+// straight into registers, 16 bytes per lane and 16-row tile of 512
+// positions, DEPTH of them ahead.  A wave works on a unit of T tiles (each
+// operand read from LDS serves T products), alone (KV = 1) or with KV - 1
+// others on interleaved groups of the slice where there are too few rows to
+// fill the chip; those add their sums through LDS in wave order.  Gated: the
+// first half of a unit's tiles are gate rows, the second half the same
+// outputs' up rows.
 //
 // One slice: the epilogue follows at once, a lane holding four consecutive
-// outputs of a token.  More (activations longer than LDS, or few rows): each
-// slice's float32 sums go to the workspace and a reduction adds them in order
-// (k_gemv_f6's second kernel, or the join).  Bound by reading the signs once.
+// outputs of a token.  More: each slice's float32 sums, scaled (and the first
+// with the bias), go to the workspace and a second kernel adds them in order
+// and finishes (the join adds them itself).  A workgroup of many rows and few
+// positions converts little for the signs it streams, one of few rows and
+// many positions needs no second launch: few_f6_plan weighs the two.  Bound
+// by reading the signs once, and by latency for the smallest calls.
 #include "f6_epilogue.h"
 #include "f6_parts.h"
 #include "f6_product.h"
@@ -31,7 +35,6 @@ using namespace f6;
 constexpr uint32_t kRsrcWord3 = 0x00020000u;
 constexpr uint32_t kFar = 0x40000000u;     // past every weight range (<= 2^30 bytes), also twice
 constexpr int kWaves = 8;
-constexpr int kTok = 16;
 
 template <int U>
 __device__ __forceinline__ f32x4 mfma(const i32x8& a, const i32x8& b, const f32x4& c, int scale) {
@@ -78,7 +81,53 @@ __device__ __forceinline__ void group_products(const uint8_t* g, int gl, const u
   }
 }
 
-template <int NP, int T, int DEPTH>
+// One block of 32 positions of a token: 64 bytes of 16-bit values, zeros past
+// K and for an index out of range.
+struct Block {
+  uint4 v[4];
+};
+__device__ __forceinline__ Block load_block(const F6Few& f, int row, int k0) {
+  Block b;
+  const F6Product& a = f.p;
+  bool live = true;
+  if (a.rows) {
+    row = a.rows[row];
+    live = row >= 0 && row < a.src_rows;
+  }
+  const auto* src = static_cast<const uint16_t*>(f.a) + static_cast<int64_t>(live ? row : 0) * f.lda;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) b.v[j] = make_uint4(0, 0, 0, 0);
+  if (live && k0 + 32 <= f.K) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b.v[j] = *reinterpret_cast<const uint4*>(src + k0 + 8 * j);
+  } else if (live) {                            // the last block of a row
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      if (k0 + 8 * j < f.K) b.v[j] = *reinterpret_cast<const uint4*>(src + k0 + 8 * j);
+  }
+  return b;
+}
+
+template <int NP, bool bf16>
+__device__ __forceinline__ void store_block(const Block& b, int place, uint8_t* g) {
+  float x[32];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) unpack8(b.v[j], bf16, x + 8 * j);
+  const uint32_t e = block_exponent(largest_bits(b.v, bf16));
+  u32x6 part[NP];
+  split_block<NP>(x, e, part);
+  const int gl = place / 4, u = place % 4;
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    const int at = (u * NP + p) * 4 + gl;
+    *reinterpret_cast<uint4*>(g + 16 * at) =
+        make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
+    *reinterpret_cast<uint2*>(g + tail_offset(4, NP) + 8 * at) = make_uint2(part[p][4], part[p][5]);
+  }
+  g[exp_offset(4, NP) + place] = static_cast<uint8_t>(e);
+}
+
+template <int NP, int T, int DEPTH, bool BF16>
 __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
   extern __shared__ __align__(256) uint8_t lds[];
   const F6Product& a = f.p;
@@ -87,74 +136,48 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // ---- which tokens, slice and row blocks
-  int tile = blockIdx.z, expert = 0, row0 = tile * kTok, row_end = a.R;
-  if (a.offsets) {
-    int tiles = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64)
-      tiles += __builtin_amdgcn_readfirstlane(wave_total(run_tiles(a, e0 + lane, kTok)));
-    if (tile >= tiles) return;
-    find_run(a, tile, kTok, lane, expert, row0, row_end);
-  }
-  const int tokens = min(kTok, row_end - row0);
+  int tile = blockIdx.z, expert = 0, row0 = tile * f.tok, row_end = a.R;
+  if (a.offsets && !find_run(a, tile, f.tok, lane, expert, row0, row_end)) return;
+  const int tokens = min(f.tok, row_end - row0);
   const int slice = blockIdx.y;
   const int g0 = slice * f.slice_groups, ng = min(f.slice_groups, a.groups - g0);
 
-  // ---- the slice's parts into LDS: [group][token][GB]
-  {
-    const auto* src = static_cast<const uint16_t*>(f.a);
-    const int blocks = ng * 16;
-    for (int i = tid; i < tokens * blocks; i += 64 * kWaves) {
-      const int t = i / blocks, b = i - t * blocks;
-      int r = row0 + t;
-      bool live = true;
-      if (a.rows) {
-        r = a.rows[r];
-        live = r >= 0 && r < a.src_rows;
-      }
-      const int k0 = (g0 * 16 + b) * 32;
-      float x[32];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (live && k0 + 8 * j < f.K)
-          v = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(r) * f.lda + k0 + 8 * j);
-        unpack8(v, f.a_dt == LQ_BF16, x + 8 * j);
-      }
-      const uint32_t e = block_exponent(largest_bits(x));
-      u32x6 part[NP];
-      split_block<NP>(x, e, part);
-      const int gl = b / 4 % 4, u = b % 4;
-      uint8_t* g = lds + (b / 16 * tokens + t) * GB;
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int at = (u * NP + p) * 4 + gl;
-        *reinterpret_cast<uint4*>(g + 16 * at) =
-            make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
-        *reinterpret_cast<uint2*>(g + tail_offset(4, NP) + 8 * at) =
-            make_uint2(part[p][4], part[p][5]);
-      }
-      g[exp_offset(4, NP) + 4 * gl + u] = static_cast<uint8_t>(e);
+  // ---- the slice's parts into LDS, [group][token][GB]: all but each thread's
+  // last block here, the next one on its way while one is split
+  const int blocks = ng * 16, all = tokens * blocks;
+  int i = tid, t_now = i / blocks, b_now = i - t_now * blocks;
+  Block now{};
+  if (i < all) now = load_block(f, row0 + t_now, (g0 * 16 + b_now) * 32);
+  auto split_now = [&]() {
+    if (i < all)
+      store_block<NP, BF16>(now, b_now % 16, lds + (b_now / 16 * tokens + t_now) * GB);
+  };
+  for (int left = all; left > 64 * kWaves; left -= 64 * kWaves) {
+    const int next = i + 64 * kWaves;
+    int t = t_now, b = b_now + 64 * kWaves;
+    while (b >= blocks) {
+      b -= blocks;
+      ++t;
     }
+    Block ahead{};
+    if (next < all) ahead = load_block(f, row0 + t, (g0 * 16 + b) * 32);
+    split_now();
+    now = ahead;
+    i = next;
+    t_now = t;
+    b_now = b;
   }
-  __syncthreads();
 
-  // ---- units
+  // ---- units, and their first signs
   const int KV = f.kv, part = wave % KV, sub = wave / KV, subs = kWaves / KV;
   const int i16 = lane & 15, gl = lane >> 4;
   const uint32_t* w = a.w + static_cast<int64_t>(expert) * a.m * a.ldw;
   const __amdgpu_buffer_rsrc_t wres = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint32_t*>(w), (short)0,
       static_cast<int>(static_cast<uint32_t>(a.m) * a.ldw * 4u), kRsrcWord3);
-  const float* s = a.s + static_cast<int64_t>(expert) * a.m;
-  const float* bias = a.bias ? a.bias + static_cast<int64_t>(expert) * a.m : nullptr;
   const int half_m = a.m / 2, out_m = a.gated ? half_m : a.m;
   const int unit_outs = a.gated ? 8 * T : 16 * T;
-  const uint32_t two = held(0x22222222u);
-  const uint8_t* mine = lds + min(i16, tokens - 1) * GB;
   const int n = (ng - part + KV - 1) / KV;      // this wave's groups: part, part + KV, ...
-  f32x4* exchange = reinterpret_cast<f32x4*>(lds + f.exchange_at);
-  const OutputTypes types = output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt);
-
   uint32_t at[T];                               // byte offsets of the unit's rows
   uint4 ring[DEPTH][T];
   auto aim = [&](int block) {
@@ -180,12 +203,36 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
       __builtin_memcpy(&ring[d][t], &r, 16);
     }
   };
-
+  // scales of a block's outputs (gated: rows), loaded with its first signs
+  const float* s = a.s + static_cast<int64_t>(expert) * a.m;
+  const float* bias = a.bias && slice == 0 ? a.bias + static_cast<int64_t>(expert) * a.m : nullptr;
+  RowScales scales[T];
+  auto column = [&](int block, int t) {
+    return (block * subs + sub) * unit_outs + (a.gated ? t % (T > 1 ? T / 2 : 1) : t) * 16 + 4 * gl;
+  };
+  auto load_scales = [&](int block) {
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+      const int o = column(block, t);
+      scales[t] = row_scales(s, bias, a.gated && t >= T / 2 ? half_m + o : o, a.m);
+    }
+  };
   const int b0 = blockIdx.x * f.blocks_per, b1 = min(b0 + f.blocks_per, f.row_blocks);
   aim(b0);
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d) load(d, d);
-  for (int block = b0; block < b1; ++block) {
+  load_scales(b0);
+  __builtin_amdgcn_sched_barrier(0);
+
+  split_now();
+  __syncthreads();
+
+  const uint32_t two = held(0x22222222u);
+  const uint8_t* mine = lds + min(i16, tokens - 1) * GB;
+  f32x4* exchange = reinterpret_cast<f32x4*>(lds + f.exchange_at);
+  const OutputTypes types = output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt);
+
+  for (int rb = b0; rb < b1; ++rb) {
     f32x4 acc[T] = {};
     for (int j = 0; j < n; j += DEPTH) {
 #pragma unroll
@@ -195,14 +242,17 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
         load(d, j + d + DEPTH);
       }
     }
-    const int out0 = (block * subs + sub) * unit_outs;
-    if (block + 1 < b1) {
-      aim(block + 1);
+    RowScales its[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) its[t] = scales[t];
+    if (rb + 1 < b1) {
+      aim(rb + 1);
 #pragma unroll
       for (int d = 0; d < DEPTH; ++d) load(d, d);
+      load_scales(rb + 1);
     }
     if (KV > 1) {
-      if (block > b0) __syncthreads();
+      if (rb > b0) __syncthreads();
 #pragma unroll
       for (int t = 0; t < T; ++t) exchange[(wave * T + t) * 64 + lane] = acc[t];
       __syncthreads();
@@ -213,92 +263,91 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
     }
     if (i16 >= tokens) continue;
     const int64_t row = row0 + i16;
-    if (f.slices > 1) {
-      // sums of this slice: [slice][row][m]
+    const bool whole = f.sums == nullptr;
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const int o = out0 + (a.gated && T > 1 ? t % (T / 2) : t) * 16 + 4 * gl;
-        const int zr = a.gated && t >= T / 2 ? half_m + o : o;
-        float* z = f.sums + (slice * static_cast<int64_t>(a.R) + row) * f.ldz + zr;
-        const int left = out_m - o;
+    for (int t = 0; t < T; ++t) {
+      const int o = column(rb, t), left = min(4, out_m - o);
+      const int col = a.gated && t >= T / 2 ? half_m + o : o;
+      float z[4];
+      scaled(make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]), its[t], z);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < left) z[c] = acc[t][c];
+      for (int c = 0; c < 4; ++c) acc[t][c] = z[c];
+      if (!whole) {
+        float* to = f.sums + (slice * static_cast<int64_t>(a.R) + row) * f.ldz + col;
+        if (left == 4 && col % 4 == 0) *reinterpret_cast<f32x4*>(to) = acc[t];
+        else
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c < left) to[c] = z[c];
       }
-      continue;
     }
+    if (!whole) continue;
 #pragma unroll
-    for (int t = 0; t < (T > 1 ? T : 1); ++t) {
+    for (int t = 0; t < T; ++t) {
       if (a.gated && t >= T / 2) break;
-      const int o = out0 + t * 16 + 4 * gl;
-      const int left = min(4, out_m - o);
+      const int o = column(rb, t), left = min(4, out_m - o);
       if (left <= 0) continue;
-      float y[4];
-      scaled(make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]),
-             row_scales(s, bias, o, left), y);
+      float y[4] = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
       activate4(y, a.act);
       if (a.gated) {
-        float g[4];
-        const f32x4& v = acc[T > 1 ? t + T / 2 < T ? t + T / 2 : t : 0];
-        scaled(make_float4(v[0], v[1], v[2], v[3]), row_scales(s, bias, half_m + o, left), g);
+        const f32x4& up = acc[t + T / 2 < T ? t + T / 2 : t];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] *= g[c];
+        for (int c = 0; c < 4; ++c) y[c] *= up[c];
       }
       finish4(y, left, types, a.residual, row * a.ldr + o, a.out, row * a.ldo + o);
     }
   }
 }
 
-// The slices' sums added in order, and the epilogue: a thread per row and
-// four outputs.
-__global__ void __launch_bounds__(256) gemv_f6_reduce_kernel(F6Few f) {
+// The slices' scaled sums added in order, and the epilogue: a thread per row
+// and four outputs, four slices' loads on their way at once.
+__global__ void __launch_bounds__(128) gemv_f6_reduce_kernel(F6Few f) {
   const F6Product& a = f.p;
-  const int half_m = a.m / 2, out_m = a.gated ? half_m : a.m;
-  const int o = (blockIdx.x * 256 + threadIdx.x) * 4;
+  const int out_m = a.gated ? a.m / 2 : a.m;
+  const int o = (blockIdx.x * 128 + threadIdx.x) * 4;
+  const int64_t row = blockIdx.y;
   const int n = min(4, out_m - o);
-  const int row = blockIdx.y;
   if (n <= 0) return;
-  int expert = 0;
-  if (a.offsets) {
-    // the last run that begins at or before this row; outside every run the
-    // row is left as it was
-    int lo = 0, hi = a.E;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (a.offsets[mid] <= row) lo = mid;
-      else hi = mid;
-    }
-    if (a.offsets[lo] > row || a.offsets[lo + 1] <= row) return;
-    expert = lo;
-  }
-  const float* s = a.s + static_cast<int64_t>(expert) * a.m;
-  const float* bias = a.bias ? a.bias + static_cast<int64_t>(expert) * a.m : nullptr;
-  auto sum = [&](int col) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const float* z = f.sums + static_cast<int64_t>(row) * f.ldz + col;
-    const int64_t step = static_cast<int64_t>(a.R) * f.ldz;
-    for (int q = 0; q < f.slices; ++q)
+  // rows outside the runs are left as they were
+  if (a.offsets && (row < a.offsets[0] || row >= a.offsets[a.E])) return;
+  const int64_t step = static_cast<int64_t>(a.R) * f.ldz;
+  auto sum = [&](int col, float (&v)[4]) {
+    const float* z = f.sums + row * f.ldz + col;
+    const bool whole = col % 4 == 0;            // rows are padded to whole fours
+    for (int q = 0; q < f.slices; q += 4) {
+      float x[4][4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] += z[q * step + min(c, n - 1)];
-    return make_float4(v[0], v[1], v[2], v[3]);
+      for (int c = 0; c < 4; ++c) {
+        const float* from = z + min(q + c, f.slices - 1) * step;
+        if (whole) {
+          const float4 y = *reinterpret_cast<const float4*>(from);
+          x[c][0] = y.x; x[c][1] = y.y; x[c][2] = y.z; x[c][3] = y.w;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[c][j] = from[min(j, n - 1)];
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += q + c < f.slices ? x[c][j] : 0.f;
+    }
   };
-  float y[4];
-  scaled(sum(o), row_scales(s, bias, o, n), y);
+  float y[4] = {}, up[4] = {};
+  sum(o, y);
+  if (a.gated) sum(out_m + o, up);
   activate4(y, a.act);
   if (a.gated) {
-    float g[4];
-    scaled(sum(half_m + o), row_scales(s, bias, half_m + o, n), g);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] *= g[c];
+    for (int j = 0; j < 4; ++j) y[j] *= up[j];
   }
-  const OutputTypes types = output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt);
-  const int64_t r = row;
-  finish4(y, n, types, a.residual, r * a.ldr + o, a.out, r * a.ldo + o);
+  finish4(y, n, output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt), a.residual,
+          row * a.ldr + o, a.out, row * a.ldo + o);
 }
 
-template <int NP, int T, int DEPTH>
+template <int NP, int T, int DEPTH, bool BF16>
 hipError_t launch(const F6Few& f, int tiles, hipStream_t st) {
-  auto* k = gemv_f6_kernel<NP, T, DEPTH>;
+  auto* k = gemv_f6_kernel<NP, T, DEPTH, BF16>;
   static const hipError_t big = hipFuncSetAttribute(
       reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
   if (big != hipSuccess) return big;
@@ -306,9 +355,9 @@ hipError_t launch(const F6Few& f, int tiles, hipStream_t st) {
   const int lds = f.exchange_at + (f.kv > 1 ? kWaves * T * 1024 : 0);
   k<<<grid, 64 * kWaves, lds, st>>>(f);
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && f.slices > 1) {
+  if (e == hipSuccess && f.sums && f.p.out) {
     const int out_m = f.p.gated ? f.p.m / 2 : f.p.m;
-    gemv_f6_reduce_kernel<<<dim3((out_m + 1023) / 1024, f.p.R), 256, 0, st>>>(f);
+    gemv_f6_reduce_kernel<<<dim3((out_m + 511) / 512, f.p.R), 128, 0, st>>>(f);
     e = hipGetLastError();
   }
   return e;
@@ -316,35 +365,61 @@ hipError_t launch(const F6Few& f, int tiles, hipStream_t st) {
 
 }  // namespace
 
-// Slices, units and workgroups: every choice from the sizes.
+// Every choice from the sizes: tokens per tile, the rows of a workgroup and
+// its slice of the positions, by an estimate of the time.  Measured: a
+// workgroup's conversions 2.5 us and 1.7 us per 512 blocks of 32 positions
+// (0.7 of it arithmetic, the rest every workgroup's loads of them); a compute unit's share of the HBM rate 21 KB per us (16 with
+// T = 1, where reading the operands from LDS is the limit); a second launch 3 us
+// (the join has one anyway) and its sums at about 4 TB/s.
 F6FewPlan few_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
-                      bool grouped) {
+                      bool grouped, bool join) {
   F6FewPlan p{};
   const int64_t runs = grouped ? (E < R ? E : R) : 1;
+  const int64_t cus = num_cus();
   p.groups = static_cast<int>(padded_positions(K) / 512);
-  p.tiles = static_cast<int>(grouped ? R / kTok + runs : (R + kTok - 1) / kTok);
-  const int tokens = static_cast<int>(R < kTok ? R : kTok);
-  // LDS holds a slice of up to `tokens` tokens; 8 KB per tile of a unit stay for the exchange
-  const int fit = (163840 - 4 * kWaves * 1024) / (group_bytes(4, NP) * tokens);
-  p.slices = (p.groups + fit - 1) / fit;
-  const int64_t tiles16 = (m + 15) / 16;
-  const int64_t waves = static_cast<int64_t>(num_cus()) * kWaves;
-  auto units = [&](int T) { return (tiles16 + T - 1) / T * p.slices * runs; };
-  p.T = 1;
-  for (int T : {4, 2})
-    if (p.T == 1 && units(T) * 2 >= waves) p.T = T;
-  if (gated && p.T == 1) p.T = 2;
-  p.kv = 1;
-  while (p.kv < 8 && units(p.T) * p.kv * 2 <= waves && p.kv * p.slices * 2 <= p.groups) p.kv *= 2;
-  p.slice_groups = (p.groups + p.slices - 1) / p.slices;
-  p.slices = (p.groups + p.slice_groups - 1) / p.slice_groups;
-  const int64_t unit_rows = 16 * p.T * (kWaves / p.kv);
-  p.row_blocks = static_cast<int>((m + unit_rows - 1) / unit_rows);
-  // enough workgroups for every compute unit, and no more conversions than that
-  const int64_t all = static_cast<int64_t>(p.row_blocks) * p.slices * runs;
-  const int64_t per = all / (2 * num_cus());
-  p.blocks_per = static_cast<int>(per < 1 ? 1 : per > p.row_blocks ? p.row_blocks : per);
-  p.exchange_at = (tokens * p.slice_groups * group_bytes(4, NP) + 255) / 256 * 256;
+  // a tile holds twice the average run, so that few runs need a second one
+  const int64_t average = (R + runs - 1) / runs;
+  p.tok = !grouped ? static_cast<int>(R < 16 ? R : 16) : average <= 2 ? 4 : average <= 4 ? 8 : 16;
+  p.tiles = static_cast<int>(grouped ? R / p.tok + runs : (R + p.tok - 1) / p.tok);
+  const int gb = group_bytes(4, NP);
+  const int fit = (163840 - kWaves * 1024 * 4) / (gb * p.tok);
+  double best = 1e30;
+  for (int T = gated ? 2 : 1; T <= 4; T *= 2)
+    for (int kv = 1; kv <= 8; kv *= 2)
+      for (int per = 1; per <= 4; per *= 2) {
+        const int64_t unit_rows = 16 * T * (kWaves / kv);
+        const int64_t row_blocks = (m + unit_rows - 1) / unit_rows;
+        if (per > row_blocks) break;
+        const int64_t wgs = (row_blocks + per - 1) / per * runs;
+        // slices: as many as LDS needs, and the next counts that fill whole rounds of compute units
+        int last = 0;
+        for (int want = 0; want <= 4; ++want) {
+          int64_t slices = want == 0 ? 1 : want * cus / wgs;
+          const int64_t least = (p.groups + fit - 1) / fit;
+          if (slices < least) slices = least;
+          if (slices > p.groups) slices = p.groups;
+          const int sg = static_cast<int>((p.groups + slices - 1) / slices);
+          slices = (p.groups + sg - 1) / sg;
+          if (slices == last || sg < kv) continue;
+          last = static_cast<int>(slices);
+          const int64_t rounds = (wgs * slices + cus - 1) / cus;
+          const double convert = 2.5 + 1.7 * ((average < p.tok ? average : p.tok) * sg * 16) / 512.0;
+          const double stream = per * (unit_rows * sg * 64 / (T == 1 ? 16e3 : 21e3) + 0.3);
+          double us = rounds * (convert + stream);
+          if (slices > 1)
+            us += (join ? 0.0 : 3.0) + static_cast<double>(slices) * R * m * 8 / 4e6;
+          if (us < best * 0.999) {
+            best = us;
+            p.T = T;
+            p.kv = kv;
+            p.blocks_per = per;
+            p.row_blocks = static_cast<int>(row_blocks);
+            p.slice_groups = sg;
+            p.slices = static_cast<int>(slices);
+          }
+        }
+      }
+  p.exchange_at = (p.tok * p.slice_groups * gb + 255) / 256 * 256;
   p.ldz = (m + 3) / 4 * 4;
   p.sums_bytes = p.slices > 1 ? static_cast<size_t>(p.slices) * R * p.ldz * 4 : 0;
   return p;
@@ -352,7 +427,9 @@ F6FewPlan few_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, in
 
 hipError_t launch_gemv_f6(const F6Few& f, const F6FewPlan& plan, int NP, hipStream_t st) {
 #define LQ_FEW(np, t, d) \
-  if (NP == np && plan.T == t) return launch<np, t, d>(f, plan.tiles, st)
+  if (NP == np && plan.T == t)                                       \
+  return f.a_dt == LQ_BF16 ? launch<np, t, d, true>(f, plan.tiles, st) \
+                           : launch<np, t, d, false>(f, plan.tiles, st)
   LQ_FEW(3, 1, 6);
   LQ_FEW(3, 2, 4);
   LQ_FEW(3, 4, 2);

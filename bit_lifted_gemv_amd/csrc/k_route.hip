@@ -3,16 +3,19 @@
 // of the (token, choice) pairs by expert, as offsets, rows and positions.
 //
 // Two launches (one when a single workgroup holds every token).  A workgroup
-// of 16 waves takes runs of 64 tokens; a wave takes one token at a time,
-// lane l holding the logits of experts l, l + 64, ... as order-preserving
-// integers.  A choice is a maximum over the wave (data-parallel moves within
-// and across rows of lanes, no LDS), then the lowest expert among equal
-// ones.  A token chooses an expert at most once, so a run's choices are one
-// 64-bit mask of tokens per expert in LDS: counts and stable ranks are
-// popcounts of it, whatever order the waves set the bits in.  The first
-// launch writes the choices and each workgroup's counts per expert; the
-// second adds the counts before its own (at most 256 workgroups) and
-// scatters.  Bound by launch latency and the E logits per token read once.
+// of 16 waves takes runs of 64 tokens.  Up to 256 experts a token has 16
+// lanes with up to 16 logits each (a wave four tokens, their minima taken by
+// rotations within a row of lanes); beyond, a wave of 64 lanes each.  16-bit
+// logits are held as one integer, inverted order-preserving bits above the
+// expert, so that one minimum gives value and lowest expert at once; float32
+// logits take a second one for the expert.  (One token per wave and two
+// maxima for every type cost 22 us for 16384 x 256 bfloat16, k = 8.)
+// A token chooses an expert at most once, so a run's choices are one 64-bit
+// mask of tokens per expert in LDS: counts and stable ranks are popcounts of
+// it, whatever order the waves set the bits in.  The first launch writes the
+// choices and each workgroup's counts per expert; the second adds the counts
+// before its own (about 256 workgroups) and scatters.  Bound by launch
+// latency and vector instructions; the logits are read once.
 #include "lq_internal.h"
 
 namespace lq {
@@ -20,18 +23,28 @@ namespace {
 
 constexpr int kRun = 64;                 // tokens per mask
 constexpr int kThreads = 1024;
-constexpr int kMaxGroups = 256;
+constexpr int kGroups = 256;             // workgroups, unless that makes kMaxPer runs each
+constexpr int kMaxPer = 1023;            // counts are 16 bits: 64 kMaxPer < 2^16
 
 // Order-preserving bits of a float; 0 for what is never chosen (NaN, -inf).
+// -0 and +0 are equal logits: both take the bits of +0.
 __device__ __forceinline__ uint32_t order_bits(float v) {
-  const uint32_t u = __float_as_uint(v);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u || u == 0xFF800000u) return 0;
-  // -0 and +0 are equal logits: both take the bits of +0
-  if ((u & 0x7FFFFFFFu) == 0) return 0x80000000u;
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(v), size = u & 0x7FFFFFFFu;
+  const uint32_t o = size == 0 ? 0x80000000u : u & 0x80000000u ? ~u : u | 0x80000000u;
+  return size > 0x7F800000u || u == 0xFF800000u ? 0u : o;
 }
 __device__ __forceinline__ float from_order_bits(uint32_t b) {
   return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
+}
+// The same for the 16 bits of a float16 or bfloat16.
+__device__ __forceinline__ uint32_t order_bits16(uint32_t u, uint32_t inf) {
+  const uint32_t size = u & 0x7FFFu;
+  const uint32_t o = size == 0 ? 0x8000u : u & 0x8000u ? ~u & 0xFFFFu : u | 0x8000u;
+  return size > inf || u == (inf | 0x8000u) ? 0u : o;
+}
+__device__ __forceinline__ float from_order_bits16(uint32_t b, bool bf16) {
+  const uint16_t u = static_cast<uint16_t>(b & 0x8000u ? b & 0x7FFFu : ~b);
+  return bf16 ? bf16_bits_to_float(u) : f16_bits_to_float(u);
 }
 
 template <int CTRL, int ROW_MASK>
@@ -40,79 +53,26 @@ __device__ __forceinline__ uint32_t moved(uint32_t keep, uint32_t v) {
       static_cast<int>(keep), static_cast<int>(v), CTRL, ROW_MASK, 0xF, false));
 }
 
-// Largest value over the wave, in every lane's hands (a scalar).
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, moved<0x111, 0xF>(0, v));   // row_shr 1, 2, 4, 8
-  v = max(v, moved<0x112, 0xF>(0, v));
-  v = max(v, moved<0x114, 0xF>(0, v));
-  v = max(v, moved<0x118, 0xF>(0, v));
-  v = max(v, moved<0x142, 0xA>(0, v));   // row_bcast 15
-  v = max(v, moved<0x143, 0xC>(0, v));   // row_bcast 31
-  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
-}
-
-__device__ __forceinline__ float wave_sum(float v) {   // fixed order
-  for (int d = 32; d; d /= 2) v += __shfl_xor(v, d);
+// Smallest value over a token's L lanes, in all of them.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+  v = min(v, moved<0x128, 0xF>(v, v));   // row_ror 8, 4, 2, 1
+  v = min(v, moved<0x124, 0xF>(v, v));
+  v = min(v, moved<0x122, 0xF>(v, v));
+  v = min(v, moved<0x121, 0xF>(v, v));
+  if (L == 64) {
+    v = min(v, moved<0x142, 0xA>(v, v)); // row_bcast 15, 31
+    v = min(v, moved<0x143, 0xC>(v, v));
+    v = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+  }
   return v;
 }
 
-// The choices of one token by one wave: lane i < k gets choice i.
-template <int N>
-__device__ __forceinline__ void choose(const void* logits, int dt, int64_t base, int E, int k,
-                                       bool renorm, int lane, int& id, float& weight) {
-  uint32_t b[N];
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {   // fixed order
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int e = 64 * j + lane;
-    float v = -INFINITY;
-    if (e < E)
-      v = dt == LQ_F32 ? static_cast<const float*>(logits)[base + e]
-          : dt == LQ_F16 ? f16_bits_to_float(static_cast<const uint16_t*>(logits)[base + e])
-                         : bf16_bits_to_float(static_cast<const uint16_t*>(logits)[base + e]);
-    b[j] = order_bits(v);
-  }
-  id = -1;
-  weight = 0.f;
-  float top = 0.f, total = 0.f;
-  uint32_t mine = 0;
-  for (int i = 0; i < k; ++i) {
-    uint32_t best = b[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) best = max(best, b[j]);
-    const uint32_t largest = wave_max(best);
-    if (largest == 0) break;             // nothing left to choose
-    uint32_t far = 0;                    // ~expert, so that the largest is the lowest expert
-#pragma unroll
-    for (int j = N - 1; j >= 0; --j)
-      if (b[j] == largest) far = ~static_cast<uint32_t>(64 * j + lane);
-    const uint32_t e = ~wave_max(far);
-    const float v = from_order_bits(largest);
-    if (i == 0) {
-      top = v;
-      if (!renorm) {
-        // softmax over every expert; +inf logits share the whole weight
-        float t = 0.f;
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (b[j]) {
-            const float x = from_order_bits(b[j]);
-            t += x == top ? 1.f : expf(x - top);
-          }
-        total = wave_sum(t);
-      }
-    }
-    const float p = v == top ? 1.f : expf(v - top);
-    if (renorm) total += p;
-    if (lane == i) {
-      id = static_cast<int>(e);
-      weight = p;
-      mine = largest;
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (e == static_cast<uint32_t>(64 * j + lane)) b[j] = 0;
-  }
-  if (mine) weight /= total;
+  for (int d = L / 2; d; d /= 2) v += __shfl_xor(v, d);
+  return v;
 }
 
 struct RouteArgs {
@@ -121,30 +81,142 @@ struct RouteArgs {
   int64_t ld;
   const uint8_t* valid;
   int T, E, k, renorm;
+  int wide;                              // rows of logits allow 16-byte loads
   int* ids;
   float* weight;
   int* pos;
   int* rows;
   int* offsets;
-  int* counts;                           // [groups][E]
+  uint16_t* counts;                      // [groups][counts_pitch]
+  int counts_pitch;
   int groups, per;                       // workgroups, runs of 64 tokens per workgroup
 };
 
-// Positions of the pairs of run `run` from base[e] (LDS, the next free one
-// of each expert) and the run's masks.
-__device__ __forceinline__ void scatter(const RouteArgs& a, int run, const uint64_t* mask,
-                                        const int* base, int tid) {
-  for (int i = tid; i < kRun * a.k; i += kThreads) {
-    const int t = run * kRun + i / a.k;
-    if (t >= a.T) break;
-    const int64_t at = static_cast<int64_t>(t) * a.k + i % a.k;
-    const int e = a.ids[at];
-    int p = -1;
-    if (e >= 0) {
-      p = base[e] + __popcll(mask[e] & ((uint64_t{1} << (t % kRun)) - 1));
-      a.rows[p] = t;
+constexpr uint32_t kNone = 0xFFFFFFFFu;   // a key behind every logit's
+
+// The choices of one token by L lanes of N logits each: lane l gets choices
+// l and l + L (id -1: none).  DT is the logits' type.
+template <int L, int N, int DT>
+__device__ __forceinline__ void choose(const RouteArgs& a, int t, bool live, int lane,
+                                       int (&id)[2], float (&weight)[2]) {
+  constexpr bool kPacked = DT != LQ_F32;
+  constexpr int kVec = DT == LQ_F32 ? 4 : 8;           // logits of a 16-byte load
+  const int E = a.E;
+  const uint32_t inf = DT == LQ_F16 ? 0x7C00u : 0x7F80u;
+  uint32_t b[N];
+  // expert of logit j of this lane
+  const bool wide = N >= kVec && a.wide;
+  auto expert = [&](int j) {
+    return wide ? (j / kVec * L + lane) * kVec + j % kVec : j * L + lane;
+  };
+  if (!live) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) b[j] = kNone;
+  } else if (N >= kVec && wide) {                      // E is a multiple of kVec then
+#pragma unroll
+    for (int v = 0; v < N / kVec; ++v) {
+      const int e = (v * L + lane) * kVec;
+      uint4 q = make_uint4(0, 0, 0, 0);
+      const bool in = e < E;
+      const int64_t at = static_cast<int64_t>(t) * a.ld + e;
+      if (in)
+        q = kPacked ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.logits) + at)
+                    : *reinterpret_cast<const uint4*>(static_cast<const float*>(a.logits) + at);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) {
+        if (kPacked) {
+          const uint32_t o = order_bits16(w[c / 2] >> (16 * (c % 2)) & 0xFFFFu, inf);
+          b[v * kVec + c] = in && o ? ~o << 16 | static_cast<uint32_t>(e + c) : kNone;
+        } else {
+          b[(v * kVec + c) % N] = in ? ~order_bits(__uint_as_float(w[c % 4])) : kNone;
+        }
+      }
     }
-    a.pos[at] = p;
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int e = j * L + lane;
+      const int64_t at = static_cast<int64_t>(t) * a.ld + min(e, E - 1);
+      if (kPacked) {
+        const uint32_t o = order_bits16(static_cast<const uint16_t*>(a.logits)[at], inf);
+        b[j] = e < E && o ? ~o << 16 | static_cast<uint32_t>(e) : kNone;
+      } else {
+        b[j] = e < E ? ~order_bits(static_cast<const float*>(a.logits)[at]) : kNone;
+      }
+    }
+  }
+  auto value = [&](uint32_t key) {
+    return kPacked ? from_order_bits16(~key >> 16, DT == LQ_BF16) : from_order_bits(~key);
+  };
+  float all = 0.f;                                     // renorm == 0: softmax over every expert
+  if (!a.renorm) {
+    uint32_t first = kNone;
+#pragma unroll
+    for (int j = 0; j < N; ++j) first = min(first, b[j]);
+    const float top = value(lanes_min<L>(first));
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (b[j] != kNone) {
+        const float y = value(b[j]);
+        all += y == top ? 1.f : expf(y - top);         // +inf logits share the whole weight
+      }
+    all = lanes_sum<L>(all);
+  }
+  // k times the smallest key (the largest logit).  Packed keys differ, so
+  // subtracting the smallest and one wraps that one past every other, and
+  // `passed` is what was subtracted so far.
+  int valid = 0;
+  if (kPacked) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) valid += b[j] != kNone;
+#pragma unroll
+    for (int d = L / 2; d; d /= 2) valid += __shfl_xor(valid, d);
+  }
+  uint32_t key[2] = {kNone, kNone}, top_key = kNone, passed = 0;
+  for (int i = 0; i < a.k; ++i) {
+    uint32_t best = b[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) best = min(best, b[j]);
+    const uint32_t least = lanes_min<L>(best);
+    uint32_t k0;
+    int e;
+    if (kPacked) {
+      k0 = i < valid ? least + passed : kNone;
+      e = static_cast<int>(k0 & 0xFFFFu);
+#pragma unroll
+      for (int j = 0; j < N; ++j) b[j] -= least + 1;
+      passed += least + 1;
+    } else {
+      uint32_t low = kNone;                            // the lowest expert with it
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        low = b[j] == least ? min(low, static_cast<uint32_t>(expert(j))) : low;
+      e = static_cast<int>(lanes_min<L>(low));
+      k0 = least;
+#pragma unroll
+      for (int j = 0; j < N; ++j) b[j] = expert(j) == e ? kNone : b[j];
+    }
+    if (i == 0) top_key = k0;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (i == lane + c * L) {
+        id[c] = e;
+        key[c] = k0;
+      }
+  }
+  const float top = value(top_key);
+  float p[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const float v = value(key[c]);
+    p[c] = key[c] == kNone ? 0.f : v == top ? 1.f : expf(v - top);
+  }
+  const float total = a.renorm ? lanes_sum<L>(p[0] + p[1]) : all;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    weight[c] = key[c] == kNone ? 0.f : p[c] / total;
+    if (key[c] == kNone) id[c] = -1;
   }
 }
 
@@ -163,86 +235,135 @@ __device__ __forceinline__ int scan_workgroup(int v, int tid, int* part) {
   return before + x - v;
 }
 
-template <int N, bool ONE>
+template <int L, int N, int DT, bool ONE>
 __global__ void __launch_bounds__(kThreads) route_choose_kernel(RouteArgs a) {
-  __shared__ uint64_t mask[64 * N];
-  __shared__ int total[64 * N];
+  __shared__ uint64_t mask[L * N];
+  __shared__ int total[L * N];
   __shared__ int part[16];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int E = a.E;
+  const int tid = threadIdx.x, lane = tid % L;
+  const int E = a.E, k = a.k;
   if (tid < E) total[tid] = 0;
+  int id[2] = {-1, -1};
+  float weight[2];
   for (int r = 0; r < a.per; ++r) {
     const int run = blockIdx.x * a.per + r;
     if (tid < E) mask[tid] = 0;
     __syncthreads();
-    for (int q = wave; q < kRun; q += 16) {
+    for (int q = tid / L; q < kRun; q += kThreads / L) {
       const int t = run * kRun + q;
       if (t >= a.T) break;
-      int id = -1;
-      float weight = 0.f;
-      if (!a.valid || a.valid[t])
-        choose<N>(a.logits, a.dt, static_cast<int64_t>(t) * a.ld, E, a.k, a.renorm, lane, id,
-                  weight);
-      if (lane < a.k) {
-        a.ids[static_cast<int64_t>(t) * a.k + lane] = id;
-        a.weight[static_cast<int64_t>(t) * a.k + lane] = weight;
-        if (id >= 0)
-          atomicOr(reinterpret_cast<unsigned long long*>(&mask[id]), 1ull << q);
+      choose<L, N, DT>(a, t, !a.valid || a.valid[t], lane, id, weight);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int i = lane + c * L;
+        if (i < k) {
+          a.ids[static_cast<int64_t>(t) * k + i] = id[c];
+          a.weight[static_cast<int64_t>(t) * k + i] = weight[c];
+          if (id[c] >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mask[id[c]]), 1ull << q);
+        }
       }
     }
     __syncthreads();
     if (tid < E) total[tid] += __popcll(mask[tid]);
   }
   if (!ONE) {
-    if (tid < E) a.counts[static_cast<int64_t>(blockIdx.x) * E + tid] = total[tid];
+    if (tid < E)
+      a.counts[static_cast<int64_t>(blockIdx.x) * a.counts_pitch + tid] =
+          static_cast<uint16_t>(total[tid]);
     return;
   }
   const int n = tid < E ? total[tid] : 0;
   const int before = scan_workgroup(n, tid, part);
+  __shared__ int used;
   if (tid < E) {
     total[tid] = before;
     a.offsets[tid] = before;
-    if (tid == E - 1) {
-      a.offsets[E] = before + n;
-      part[0] = before + n;
-    }
+    if (tid == E - 1) a.offsets[E] = used = before + n;
   }
   __syncthreads();
-  scatter(a, 0, mask, total, tid);
-  for (int i = part[0] + tid; i < a.T * a.k; i += kThreads) a.rows[i] = -1;
+  if (L == 16) {
+    // every token's choices are still in its lanes
+    const int t = tid / L;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int i = lane + c * L;
+      if (t < a.T && i < k) {
+        int p = -1;
+        if (id[c] >= 0) {
+          p = total[id[c]] + __popcll(mask[id[c]] & ((uint64_t{1} << t) - 1));
+          a.rows[p] = t;
+        }
+        a.pos[t * k + i] = p;
+      }
+    }
+  } else {
+    for (int at = tid; at < a.T * k; at += kThreads) {
+      const int t = at / k, e = a.ids[at];
+      int p = -1;
+      if (e >= 0) {
+        p = total[e] + __popcll(mask[e] & ((uint64_t{1} << t) - 1));
+        a.rows[p] = t;
+      }
+      a.pos[at] = p;
+    }
+  }
+  for (int i = used + tid; i < a.T * k; i += kThreads) a.rows[i] = -1;
 }
 
-template <int N>
+template <int EMAX>
 __global__ void __launch_bounds__(kThreads) route_scatter_kernel(RouteArgs a) {
-  __shared__ uint64_t mask[64 * N];
-  __shared__ int base[64 * N];
+  __shared__ uint64_t mask[EMAX];
+  __shared__ int base[EMAX], all[EMAX];
   __shared__ int part[16];
   __shared__ int used;
   const int tid = threadIdx.x;
-  const int E = a.E;
-  // counts of every workgroup: those before this one, and all
-  int mine = 0, all = 0;
-  for (int e = tid; e < 64 * N; e += kThreads) base[e] = 0, mask[e] = 0;
+  const int E = a.E, k = a.k;
+  for (int e = tid; e < EMAX; e += kThreads) base[e] = all[e] = 0;
+  // the first run's choices, on their way while the counts are added
+  int first[2] = {-1, -1};
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int i = tid + c * kThreads;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * a.per * kRun * k + i;
+    if (i < kRun * k && at < static_cast<int64_t>(a.T) * k) first[c] = a.ids[at];
+  }
   __syncthreads();
   {
-    // thread (q, e): every (kThreads / E)-th workgroup's count of expert e
-    const int lanes = kThreads / E;
-    const int q = tid / E, e = tid % E;
+    // thread (q, e): every lanes-th workgroup's counts of experts 2 e, 2 e + 1;
+    // integer sums, so the order of the additions does not matter
+    const int pairs = (E + 1) / 2, lanes = kThreads / pairs;
+    const int q = tid / pairs, e = tid % pairs;
     if (q < lanes) {
-#pragma unroll 8
-      for (int g = q; g < a.groups; g += lanes) {
-        const int c = a.counts[static_cast<int64_t>(g) * E + e];
-        all += c;
-        mine += g < static_cast<int>(blockIdx.x) ? c : 0;
+      const auto* counts = reinterpret_cast<const uint32_t*>(a.counts);
+      int sum[2] = {0, 0}, mine[2] = {0, 0};
+      for (int g0 = q; g0 < a.groups; g0 += 16 * lanes) {
+        uint32_t c[16];                                // sixteen loads on their way at once
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int g = min(g0 + x * lanes, a.groups - 1);
+          c[x] = counts[static_cast<int64_t>(g) * (a.counts_pitch / 2) + e];
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const int g = g0 + x * lanes;
+          if (g >= a.groups) c[x] = 0;
+          sum[0] += c[x] & 0xFFFFu;
+          sum[1] += c[x] >> 16;
+          if (g >= static_cast<int>(blockIdx.x)) c[x] = 0;
+          mine[0] += c[x] & 0xFFFFu;
+          mine[1] += c[x] >> 16;
+        }
       }
-      // integer sums: the order of the additions does not matter
-      atomicAdd(&base[e], mine);
-      atomicAdd(reinterpret_cast<int*>(&mask[e]), all);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (2 * e + c < E) {
+          atomicAdd(&base[2 * e + c], mine[c]);
+          atomicAdd(&all[2 * e + c], sum[c]);
+        }
     }
   }
   __syncthreads();
-  const int n = tid < E ? static_cast<int>(mask[tid]) : 0;
+  const int n = tid < E ? all[tid] : 0;
   const int before = scan_workgroup(n, tid, part);
   if (tid < E) {
     base[tid] += before;
@@ -257,46 +378,73 @@ __global__ void __launch_bounds__(kThreads) route_scatter_kernel(RouteArgs a) {
     __syncthreads();
     if (tid < E) mask[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < kRun * a.k; i += kThreads) {
-      const int q = i / a.k, t = run * kRun + q;
-      if (t >= a.T) break;
-      const int e = a.ids[static_cast<int64_t>(t) * a.k + i % a.k];
-      if (e >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mask[e]), 1ull << q);
+    const int64_t at0 = static_cast<int64_t>(run) * kRun * k;
+    const int pairs = static_cast<int>(min(static_cast<int64_t>(kRun) * k,
+                                           max(static_cast<int64_t>(a.T) * k - at0, int64_t{0})));
+    int e[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int i = tid + c * kThreads;
+      e[c] = r == 0 ? first[c] : i < pairs ? a.ids[at0 + i] : -1;
+      if (e[c] >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mask[e[c]]), 1ull << (i / k));
     }
     __syncthreads();
-    scatter(a, run, mask, base, tid);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int i = tid + c * kThreads, q = i / k;
+      if (i >= pairs) continue;
+      int p = -1;
+      if (e[c] >= 0) {
+        p = base[e[c]] + __popcll(mask[e[c]] & ((uint64_t{1} << q) - 1));
+        a.rows[p] = run * kRun + q;
+      }
+      a.pos[at0 + i] = p;
+    }
     __syncthreads();
     if (tid < E) base[tid] += __popcll(mask[tid]);
   }
-  const int pairs = a.T * a.k;
+  const int64_t pairs = static_cast<int64_t>(a.T) * k;
   for (int64_t i = used + static_cast<int64_t>(blockIdx.x) * kThreads + tid; i < pairs;
        i += static_cast<int64_t>(a.groups) * kThreads)
     a.rows[i] = -1;
 }
 
-int runs_of(int64_t T) { return static_cast<int>((T + kRun - 1) / kRun); }
+int64_t runs_of(int64_t T) { return (T + kRun - 1) / kRun; }
+int per_of(int64_t T) {
+  const int64_t per = (runs_of(T) + kGroups - 1) / kGroups;
+  return static_cast<int>(per < kMaxPer ? per : kMaxPer);
+}
+int groups_of(int64_t T) { return static_cast<int>((runs_of(T) + per_of(T) - 1) / per_of(T)); }
+int pitch_of(int E) { return (E + 1) / 2 * 2; }
 
-template <int N>
+template <int L, int N, int DT>
 hipError_t launch(RouteArgs a, hipStream_t st) {
-  const int runs = runs_of(a.T);
-  if (runs <= 1) {
+  if (runs_of(a.T) <= 1) {
     a.groups = a.per = 1;
-    route_choose_kernel<N, true><<<1, kThreads, 0, st>>>(a);
+    route_choose_kernel<L, N, DT, true><<<1, kThreads, 0, st>>>(a);
     return hipGetLastError();
   }
-  a.per = (runs + kMaxGroups - 1) / kMaxGroups;
-  a.groups = (runs + a.per - 1) / a.per;
-  route_choose_kernel<N, false><<<a.groups, kThreads, 0, st>>>(a);
-  route_scatter_kernel<N><<<a.groups, kThreads, 0, st>>>(a);
+  a.per = per_of(a.T);
+  a.groups = groups_of(a.T);
+  route_choose_kernel<L, N, DT, false><<<a.groups, kThreads, 0, st>>>(a);
+  if (a.E <= 256) route_scatter_kernel<256><<<a.groups, kThreads, 0, st>>>(a);
+  else route_scatter_kernel<1024><<<a.groups, kThreads, 0, st>>>(a);
   return hipGetLastError();
+}
+
+template <int DT>
+hipError_t by_experts(const RouteArgs& a, hipStream_t st) {
+  if (a.E <= 64) return launch<16, 4, DT>(a, st);
+  if (a.E <= 128) return launch<16, 8, DT>(a, st);
+  if (a.E <= 256) return launch<16, 16, DT>(a, st);
+  return launch<64, 16, DT>(a, st);
 }
 
 }  // namespace
 
 size_t route_workspace_bytes(int64_t T, int E) {
-  const int64_t runs = runs_of(T);
-  if (runs <= 1) return 0;
-  return static_cast<size_t>(runs < kMaxGroups ? runs : kMaxGroups) * E * 4;
+  if (runs_of(T) <= 1) return 0;
+  return static_cast<size_t>(groups_of(T)) * pitch_of(E) * 2;
 }
 
 hipError_t launch_route(const void* logits, lq_dtype dt, int64_t T, int E, int64_t ld,
@@ -311,17 +459,17 @@ hipError_t launch_route(const void* logits, lq_dtype dt, int64_t T, int E, int64
   a.E = E;
   a.k = k;
   a.renorm = renorm;
+  const int vec = dt == LQ_F32 ? 4 : 8;
+  a.wide = E % vec == 0 && ld % vec == 0 && reinterpret_cast<uint64_t>(logits) % 16 == 0;
   a.ids = ids;
   a.weight = weight;
   a.pos = pos;
   a.rows = rows;
   a.offsets = offsets;
-  a.counts = static_cast<int*>(ws);
-  if (E <= 64) return launch<1>(a, st);
-  if (E <= 128) return launch<2>(a, st);
-  if (E <= 256) return launch<4>(a, st);
-  if (E <= 512) return launch<8>(a, st);
-  return launch<16>(a, st);
+  a.counts = static_cast<uint16_t*>(ws);
+  a.counts_pitch = pitch_of(E);
+  if (dt == LQ_F32) return by_experts<LQ_F32>(a, st);
+  return dt == LQ_F16 ? by_experts<LQ_F16>(a, st) : by_experts<LQ_BF16>(a, st);
 }
 
 }  // namespace lq

@@ -205,7 +205,8 @@ struct F6Plan {
   lq::F6FewPlan fp;
   int NP;
   int64_t row_bytes, image_rows;
-  size_t sums_at, z_at;        // slices' sums of the few-row kernel; float32 rows of lq_gemm_join
+  int z_slices;                // float32 rows of lq_gemm_join: slices, offset, pitch
+  size_t z_at;
   int64_t ldz;
   size_t bytes;
 };
@@ -222,14 +223,21 @@ F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtyp
   // few rows: up to 16 in all, or about 8 a run on average
   p.few = R <= kFewRows || (grouped && R <= kFewRowsPerRun * (E < R ? E : R));
   if (p.few) {
-    p.fp = lq::few_f6_plan(E, m, K, R < 1 ? 1 : R, gated, p.NP, grouped);
+    p.fp = lq::few_f6_plan(E, m, K, R < 1 ? 1 : R, gated, p.NP, grouped, join);
     p.bytes = round256(p.fp.sums_bytes);
+    if (join) {                // the join reads the slices itself, one or several
+      p.z_slices = p.fp.slices;
+      p.ldz = p.fp.ldz;
+      p.bytes = round256(static_cast<size_t>(p.fp.slices) * R * p.ldz * 4);
+      return p;
+    }
   } else {
     p.row_bytes = lq::f6::row_bytes(K, 2, p.NP);
     p.image_rows = rows + (grouped ? 1 : 0);      // a row of zeros behind the last
     p.bytes = round256(static_cast<size_t>(p.image_rows * p.row_bytes));
   }
   if (join) {
+    p.z_slices = 1;
     p.z_at = p.bytes;
     p.ldz = (m + 3) / 4 * 4;
     p.bytes += static_cast<size_t>(R) * p.ldz * 4;
@@ -249,13 +257,14 @@ hipError_t f6_run(lq::F6Product& p, const F6Plan& plan, int64_t K, const void* a
     f.a_dt = a_dt;
     f.lda = lda;
     f.K = static_cast<int>(K);
+    f.tok = plan.fp.tok;
     f.kv = plan.fp.kv;
     f.slices = plan.fp.slices;
     f.slice_groups = plan.fp.slice_groups;
     f.row_blocks = plan.fp.row_blocks;
     f.blocks_per = plan.fp.blocks_per;
     f.exchange_at = plan.fp.exchange_at;
-    f.sums = static_cast<float*>(workspace);
+    f.sums = plan.fp.slices > 1 || plan.z_slices ? static_cast<float*>(workspace) : nullptr;
     f.ldz = plan.fp.ldz;
     return lq::launch_gemv_f6(f, plan.fp, plan.NP, st);
   }
@@ -840,7 +849,7 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
   hipError_t e = hipSuccess;
   if (R > 0) {
     lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, LQ_ACT_NONE, 0);
-    p.out = z;
+    p.out = plan.few ? nullptr : z;
     p.ldo = plan.ldz;
     p.out_dt = LQ_F32;
     p.R = static_cast<int>(R);
@@ -850,7 +859,7 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
     e = f6_run(p, plan, K, a_lift, lift_dtype, lda, R, workspace, hs);
   }
   if (e == hipSuccess)
-    e = lq::launch_join(z, R, m, plan.ldz, pos, weight, T, k, residual, ldr, out, ldo, out_dtype,
+    e = lq::launch_join(z, plan.z_slices, R, m, plan.ldz, pos, weight, T, k, residual, ldr, out, ldo, out_dtype,
                         hs);
   return hip_status(e, "lq_gemm_join launch");
 }

@@ -195,21 +195,21 @@ struct F6FewPlan {
   int groups;                  // groups of 512 positions
   int slices, slice_groups;
   int row_blocks, blocks_per;  // blocks of units, and how many a workgroup takes
-  int tiles;                   // of 16 rows (grouped: at most)
+  int tok, tiles;              // tokens per tile, tiles (grouped: at most)
   int exchange_at;             // LDS bytes before the exchange
   int64_t ldz;
   size_t sums_bytes;           // of the slices' sums, 0 for one slice
 };
 F6FewPlan few_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
-                      bool grouped);
+                      bool grouped, bool join);
 struct F6Few {
-  F6Product p;                 // groups: of 512 positions; no image
+  F6Product p;                 // groups: of 512 positions; no image; out null: only the sums
   const void* a;
   int a_dt;
   int64_t lda;
   int K;
-  int kv, slices, slice_groups, row_blocks, blocks_per, exchange_at;
-  float* sums;                 // [slices][R][ldz]
+  int tok, kv, slices, slice_groups, row_blocks, blocks_per, exchange_at;
+  float* sums;                 // [slices][R][ldz] scaled sums, or null: outputs at once
   int64_t ldz;
 };
 hipError_t launch_gemv_f6(const F6Few& f, const F6FewPlan& plan, int NP, hipStream_t st);
@@ -219,9 +219,10 @@ hipError_t launch_f6_image(const void* a, lq_dtype dt, int64_t rows, bool zero_r
                            int64_t lda, int H, int NP, void* img, hipStream_t st);
 hipError_t launch_gemm_f6(const F6Product& p, int NP, hipStream_t st);
 
-// out = residual + sum_j weight z[pos] (k_join.hip); ldz a multiple of 4.
-hipError_t launch_join(const float* z, int64_t R, int64_t m, int64_t ldz, const int* pos,
-                       const float* weight, int64_t T, int k, const void* residual, int64_t ldr,
+// out = residual + sum_j weight z[pos] (k_join.hip), z the sum of `slices`
+// arrays [R][ldz]; ldz a multiple of 4.
+hipError_t launch_join(const float* z, int slices, int64_t R, int64_t m, int64_t ldz,
+                       const int* pos, const float* weight, int64_t T, int k, const void* residual, int64_t ldr,
                        void* out, int64_t ldo, int dt, hipStream_t st);
 
 // Router (k_route.hip), E <= 1024, k <= 32.

@@ -453,8 +453,12 @@ class _On:
     def __init__(self, device: torch.device, stream):
         self.device = device
         self.stream = stream
-        self.handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
         self.guard = None
+        if stream is None:
+            # the raw handle: torch.cuda.current_stream builds a Stream object (2 us)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            self.handle = stream.cuda_stream
 
     def __enter__(self):
         if self.device.index != torch.cuda.current_device():
@@ -666,10 +670,10 @@ def route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None, re
         L = lib()
         check(L.lq_route_workspace_size(T, E, k, ctypes.byref(n)))
         ws = on.workspace(n.value)
-        pairs = torch.empty((3, T, k), dtype=torch.int32, device=dev)
+        ids, pos, rows = torch.empty((3, T, k), dtype=torch.int32, device=dev).unbind()
         weight = torch.empty((T, k), dtype=torch.float32, device=dev)
         offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        ids, pos, rows = pairs[0], pairs[1], pairs[2].view(-1)
+        rows = rows.view(-1)
         check(L.lq_route(_ptr(logits), code, T, E, ld, _ptr(valid), k, int(renorm), _ptr(ids),
                          _ptr(weight), _ptr(pos), _ptr(rows), _ptr(offsets), _ptr(ws), n.value,
                          on.handle))
