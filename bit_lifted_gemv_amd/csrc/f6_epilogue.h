@@ -13,6 +13,22 @@ __device__ __forceinline__ float sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
 }
 
+// z (1 + erf(z / sqrt 2)) / 2.  1 - erf(x) for x >= 0 by Abramowitz and Stegun
+// 7.1.26, a polynomial in 1 / (1 + p x) times exp(-x^2), within 1.5e-7: with
+// erfc itself at hand the factor of a negative z needs no difference from 1.
+__device__ __forceinline__ float gelu(float z) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(1.f + 0.3275911f * x);
+  float p = 1.061405429f;
+  p = p * t - 1.453152027f;
+  p = p * t + 1.421413741f;
+  p = p * t - 0.284496736f;
+  p = p * t + 0.254829592f;
+  // exp(-x^2) as 2^(-x^2 log2 e)
+  const float half_erfc = 0.5f * p * t * __builtin_amdgcn_exp2f(-1.44269504088896341f * x * x);
+  return z * (z < 0.f ? half_erfc : 1.f - half_erfc);
+}
+
 __device__ __forceinline__ void activate4(float (&z)[4], int act) {
   switch (act) {
     case LQ_ACT_RELU:
@@ -25,7 +41,7 @@ __device__ __forceinline__ void activate4(float (&z)[4], int act) {
       break;
     case LQ_ACT_GELU:
 #pragma unroll
-      for (int c = 0; c < 4; ++c) z[c] = 0.5f * z[c] * (1.f + erff(z[c] * 0.70710678118654752f));
+      for (int c = 0; c < 4; ++c) z[c] = gelu(z[c]);
       break;
     case LQ_ACT_GELU_TANH:                                            // (1 + tanh u) / 2 = sigmoid(2 u)
 #pragma unroll
@@ -62,16 +78,17 @@ __device__ __forceinline__ void scaled(const float4& v, const RowScales& r, floa
   z[3] = v.w * r.s[3] + r.b[3];
 }
 
-__device__ __forceinline__ float load_typed(const void* p, int dt, int64_t i) {
-  return dt == LQ_F32 ? static_cast<const float*>(p)[i]
-                      : dt == LQ_F16 ? f16_bits_to_float(static_cast<const uint16_t*>(p)[i])
-                                     : bf16_bits_to_float(static_cast<const uint16_t*>(p)[i]);
+// Two values rounded to nearest even, one packed word.
+__device__ __forceinline__ uint32_t round16x2(float lo, float hi, int dt) {
+  if (dt == LQ_F16)
+    return float_to_f16_bits_rne(lo) | static_cast<uint32_t>(float_to_f16_bits_rne(hi)) << 16;
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
-
-// Round to nearest even; a NaN stays one.
-__device__ __forceinline__ uint16_t round16(float v, int dt) {
-  if (dt == LQ_F16) return float_to_f16_bits_rne(v);
-  return v != v ? uint16_t{0x7FC0} : float_to_bf16_bits_rne(v);
+__device__ __forceinline__ float value16(uint32_t bits, int dt) {
+  const uint16_t b = static_cast<uint16_t>(bits);
+  return dt == LQ_F16 ? f16_bits_to_float(b) : bf16_bits_to_float(b);
 }
 
 // `wide`: four consecutive outputs go in one access of 8 or 16 bytes.
@@ -88,42 +105,77 @@ __host__ __device__ __forceinline__ OutputTypes output_types(const void* out, in
   return {dt, bits % (4 * esz) == 0};
 }
 
-// y[0 .. 3]: outputs of four columns of one token, the first n of them
-// inside; adds the residual and stores.
-__device__ __forceinline__ void finish4(float (&y)[4], int n, const OutputTypes& types,
-                                        const void* residual, int64_t at_residual, void* out,
-                                        int64_t at) {
-  const int dt = types.dt;
-  if (types.wide && n == 4) {
-    if (dt == LQ_F32) {
-      if (residual) {
-        const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(residual) + at_residual);
-        y[0] += r.x; y[1] += r.y; y[2] += r.z; y[3] += r.w;
-      }
-      *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+// The residual of four columns of one token, the first n of them inside, as
+// it lies in memory (its conversion waits for its arrival).
+struct Residual {
+  uint32_t w[4];
+};
+__device__ __forceinline__ Residual load_residual(int n, const OutputTypes& types,
+                                                  const void* residual, int64_t at) {
+  Residual r{};
+  if (!residual || n <= 0) return r;
+  if (types.dt == LQ_F32) {
+    const auto* p = static_cast<const uint32_t*>(residual) + at;
+    if (types.wide && n == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
     } else {
-      if (residual) {
-        const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(residual) + at_residual);
-        const uint16_t q[4] = {static_cast<uint16_t>(r.x), static_cast<uint16_t>(r.x >> 16),
-                               static_cast<uint16_t>(r.y), static_cast<uint16_t>(r.y >> 16)};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          y[j] += dt == LQ_F16 ? f16_bits_to_float(q[j]) : bf16_bits_to_float(q[j]);
-      }
-      uint2 v;
-      v.x = round16(y[0], dt) | static_cast<uint32_t>(round16(y[1], dt)) << 16;
-      v.y = round16(y[2], dt) | static_cast<uint32_t>(round16(y[3], dt)) << 16;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = v;
+      for (int c = 0; c < 4; ++c)
+        if (c < n) r.w[c] = p[c];
+    }
+  } else {
+    const auto* p = static_cast<const uint16_t*>(residual) + at;
+    if (types.wide && n == 4) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      r.w[0] = v.x; r.w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) r.w[c / 2] |= static_cast<uint32_t>(p[c]) << (16 * (c % 2));
+    }
+  }
+  return r;
+}
+
+// Adds the residual to y and stores the first n of four outputs.
+__device__ __forceinline__ void store4(float (&y)[4], int n, const OutputTypes& types,
+                                       const Residual& r, bool add, void* out, int64_t at) {
+  if (types.dt == LQ_F32) {
+    if (add) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y[c] += __uint_as_float(r.w[c]);
+    }
+    float* to = static_cast<float*>(out) + at;
+    if (types.wide && n == 4) {
+      *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) to[c] = y[c];
     }
     return;
   }
+  if (add) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j >= n) break;
-    if (residual) y[j] += load_typed(residual, dt, at_residual + j);
-    if (dt == LQ_F32) static_cast<float*>(out)[at + j] = y[j];
-    else static_cast<uint16_t*>(out)[at + j] = round16(y[j], dt);
+    for (int c = 0; c < 4; ++c) y[c] += value16(r.w[c / 2] >> (16 * (c % 2)), types.dt);
   }
+  const uint2 v = make_uint2(round16x2(y[0], y[1], types.dt), round16x2(y[2], y[3], types.dt));
+  uint16_t* to = static_cast<uint16_t*>(out) + at;
+  if (types.wide && n == 4) {
+    *reinterpret_cast<uint2*>(to) = v;
+  } else {
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < n) to[c] = static_cast<uint16_t>(w[c / 2] >> (16 * (c % 2)));
+  }
+}
+
+__device__ __forceinline__ void finish4(float (&y)[4], int n, const OutputTypes& types,
+                                        const void* residual, int64_t at_residual, void* out,
+                                        int64_t at) {
+  store4(y, n, types, load_residual(n, types, residual, at_residual), residual != nullptr, out, at);
 }
 
 }  // namespace f6

@@ -72,7 +72,7 @@ __device__ __forceinline__ i32x4 resource(const void* p, uint32_t bytes) {
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <int NP, int WR, int WK, int TT>
+template <int NP, int WR, int WK, int TT, bool ONE>
 struct Shape {
   static constexpr int NW = WR * WK;                   // waves
   static constexpr int SEC = WK == 4 ? 2 : 1;          // groups per stage
@@ -88,22 +88,26 @@ struct Shape {
   static constexpr int WL = ROWS / 32 / NW;             // loads of signs per wave and unit
   static constexpr int STAGE = IMG_LOADS * 1024;
   static constexpr int SIGNS = ROWS * 32;               // a unit of signs
-  static constexpr int MAX_LDS = NW == 4 ? 81920 : 163840;  // two workgroups per unit, or one
-  static constexpr int RING = (MAX_LDS - 2 * SIGNS) / STAGE;
-  static constexpr int S = RING > 4 ? 4 : RING;
-  // loads that may still be on their way when the next stage must have
-  // landed: those of the stages behind it, less those behind its signs
-  static constexpr int WAIT = (UNIT == 1 && S > 3 ? 1 : S - 2) * IL;
+  // a workgroup to itself on a compute unit, or two of four waves
+  static constexpr int MAX_LDS = ONE ? 163840 : 81920;
+  static constexpr int RING = UNIT == 1 ? MAX_LDS / (STAGE + SIGNS) : (MAX_LDS - 2 * SIGNS) / STAGE;
+  static constexpr int S_MOST = UNIT == 1 ? 6 : 4;
+  static constexpr int S = RING > S_MOST ? S_MOST : RING;
+  static constexpr int SR = UNIT == 1 ? S : 2;         // units of signs in LDS
+  // loads that may still be on their way when the next stage and its signs
+  // must have landed: those of the stages behind it
+  static constexpr int WAIT = (S - 2) * (UNIT == 1 ? IL + WL : IL);
   static constexpr int PITCH = 132;                    // floats per token in the final exchange
   static constexpr int EXCHANGE = NW * 32 * PITCH * 4;
-  static constexpr int LDS = S * STAGE + 2 * SIGNS > EXCHANGE ? S * STAGE + 2 * SIGNS : EXCHANGE;
+  static constexpr int OPERANDS = S * STAGE + SR * SIGNS;
+  static constexpr int LDS = OPERANDS > EXCHANGE ? OPERANDS : EXCHANGE;
   static_assert(S >= 2 && LDS <= MAX_LDS && NU >= 1 && WL >= 1);
-  static_assert((S - 1) * IL + WL < 64);
+  static_assert((S - 1) * (IL + WL) + WL < 64);
 };
 
-template <int NP, int WR, int WK, int TT>
+template <int NP, int WR, int WK, int TT, bool ONE>
 __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
-  using P = Shape<NP, WR, WK, TT>;
+  using P = Shape<NP, WR, WK, TT, ONE>;
   constexpr int SEC = P::SEC, NU = P::NU, TOK = P::TOK, ROWS = P::ROWS, NW = P::NW;
   extern __shared__ __align__(1024) uint8_t lds[];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -120,11 +124,12 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
     for (int e0 = 0; e0 < a.E; e0 += 64)
       tiles += uniform(wave_total(run_tiles(a, e0 + lane, TOK, lo, end)));
   }
-  const int total = tiles * RT;
+  const int total = tiles * RT * a.slices;
   const int chunk = (total + 7) / 8;
   const int at = static_cast<int>(blockIdx.x & 7) * chunk + static_cast<int>(blockIdx.x >> 3);
   if (static_cast<int>(blockIdx.x >> 3) >= chunk || at >= total) return;
-  const int pair = at / (2 * RT), in = at - pair * 2 * RT;
+  const int slice = a.slices == 1 ? 0 : at / (tiles * RT), here = at - slice * tiles * RT;
+  const int pair = here / (2 * RT), in = here - pair * 2 * RT;
   const int wide = min(2, tiles - 2 * pair);
   int tile = 2 * pair + in % wide;
   const int rt = in / wide;
@@ -134,7 +139,7 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
 
   const uint32_t* w = a.w + static_cast<int64_t>(expert) * a.m * a.ldw;
   const float* s = a.s + static_cast<int64_t>(expert) * a.m;
-  const float* bias = a.bias ? a.bias + static_cast<int64_t>(expert) * a.m : nullptr;
+  const float* bias = a.bias && slice == 0 ? a.bias + static_cast<int64_t>(expert) * a.m : nullptr;
   const int half_m = a.m / 2;
   const int outs = a.gated ? ROWS / 2 : ROWS;          // outputs of the tile
   const int out0 = rt * outs;
@@ -166,22 +171,24 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
       row = min(out0 + lr, a.m - 1);
     sign_src[i] = static_cast<uint32_t>(row) * a.ldw * 4u + (c & 1) * 16;
   }
-  const int stages = a.groups / SEC, units = a.groups / 2;
+  // this slice's units of 256 positions
+  const int unit0 = slice * a.slice_units, units = min(a.slice_units, a.groups / 2 - unit0);
+  const int stages = units * P::UNIT, stage0 = unit0 * P::UNIT;
   const uint32_t lds0 = lds_address(lds);
   constexpr int SIGNS_AT = P::S * P::STAGE;
   // past the end: the last one again, into a slot nobody reads
   auto issue_parts = [&](int stage, int slot) {
-    const uint32_t off = min(stage, stages - 1) * SEC * P::GB;
+    const uint32_t off = (stage0 + min(stage, stages - 1)) * SEC * P::GB;
 #pragma unroll
     for (int i = 0; i < P::IL; ++i)
       load_to_lds(lds0 + slot * P::STAGE + min(wave + NW * i, P::IMG_LOADS - 1) * 1024,
                   part_src[i], ires, off);
   };
-  auto issue_signs = [&](int unit) {
-    const uint32_t off = min(unit, units - 1) * 32;
+  auto issue_signs = [&](int unit, int slot) {
+    const uint32_t off = (unit0 + min(unit, units - 1)) * 32;
 #pragma unroll
     for (int i = 0; i < P::WL; ++i)
-      load_to_lds(lds0 + SIGNS_AT + (unit & 1) * P::SIGNS + (wave + NW * i) * 1024, sign_src[i],
+      load_to_lds(lds0 + SIGNS_AT + slot * P::SIGNS + (wave + NW * i) * 1024, sign_src[i],
                   wres, off);
   };
 
@@ -218,20 +225,20 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
         scale[t][p] = static_cast<int>(ex[t] >> (16 * h + 8 * step_u(u)) & 255u) - 4 * p;
   };
   // j: group of the pair that the unit covers
-  auto read_words = [&](int unit, int j, int u) {
+  auto read_words = [&](int slot, int j, int u) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       word[q] = *reinterpret_cast<const uint32_t*>(
-          lds + SIGNS_AT + (unit & 1) * P::SIGNS + (wr * 128 + 32 * q + i32) * 32 + h * 16 +
+          lds + SIGNS_AT + slot * P::SIGNS + (wr * 128 + 32 * q + i32) * 32 + h * 16 +
           8 * (j + step_group(u)) + 4 * step_u(u));
   };
 
-  issue_signs(0);
-  issue_parts(0, 0);
-  issue_signs(1);
 #pragma unroll
-  for (int i = 1; i < P::S; ++i) issue_parts(i, i);
-  wait_and_barrier<P::WL + (P::S - 1) * P::IL>();
+  for (int i = 0; i < P::S; ++i) {
+    if (i < P::SR) issue_signs(i, i);
+    issue_parts(i, i);
+  }
+  wait_and_barrier<(P::SR - 1) * P::WL + (P::S - 1) * P::IL>();
   read_words(0, 0, 0);
   read_exponents(0, 0);
 #pragma unroll
@@ -245,8 +252,9 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   // The order below is kept by the scheduling barriers: four products, then
   // the reads that refill their operand; the next step's signs are expanded
   // between the step's last products, each as its operand is free.
-  int slot = 0;
+  int slot = 0, sign_slot = 0;
   for (int unit = 0; unit < units; ++unit) {
+    const int next_sign = sign_slot + 1 == P::SR ? 0 : sign_slot + 1;
 #pragma unroll
     for (int j = 0; j < P::UNIT; ++j) {
       const int next = slot + 1 == P::S ? 0 : slot + 1;
@@ -273,11 +281,11 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
               if (last) {
                 // the next stage has landed and nobody reads this one any more
                 wait_and_barrier<P::WAIT>();
-                if (unit_ends) issue_signs(unit + 2);
+                if (unit_ends) issue_signs(unit + P::SR, sign_slot);
                 issue_parts(unit * P::UNIT + j + P::S, slot);
               }
-              if (last && unit_ends) read_words(unit + 1, 0, nu);
-              else read_words(unit, last ? j + 1 : j, nu);
+              if (last && unit_ends) read_words(next_sign, 0, nu);
+              else read_words(sign_slot, last ? j + 1 : j, nu);
               read_exponents(nslot, nu);
             }
             read_part(nslot, nu, t, p);
@@ -288,6 +296,7 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
       }
       slot = next;
     }
+    sign_slot = next_sign;
   }
   wait_and_barrier<0>();
 
@@ -301,10 +310,24 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   const int strip = a.gated ? o / 64 : o / 128;
   const float* z0 = ex32 + strip * 32 * P::PITCH + (a.gated ? o % 64 : o % 128);
   const OutputTypes types = output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt);
-  RowScales rs = row_scales(s, bias, out0 + o, a.m), up = rs;
+  const RowScales rs = row_scales(s, bias, out0 + o, a.m);
+  RowScales up = rs;
   if (a.gated) up = row_scales(s, bias, half_m + out0 + o, a.m);
+  const int64_t slice_row = row0 + static_cast<int64_t>(slice) * a.R;
+  // a chunk of tokens: their residuals are on their way before the sums are added
+  constexpr int CHUNK = 16 / WK < 4 ? 16 / WK : 4;
+  auto load_chunk = [&](int t, int tk, Residual (&r)[CHUNK]) {
+#pragma unroll
+    for (int c = 0; c < CHUNK; ++c) {
+      const int token = 32 * t + tk + c * tk_step;
+      const bool live = tk + c * tk_step < 32 && token < tokens;
+      r[c] = load_residual(live ? n : 0, types, a.residual, (slice_row + token) * a.ldr + out0 + o);
+    }
+  };
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
+    Residual r[CHUNK];
+    load_chunk(t, tk0, r);
     if (t) __syncthreads();
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -315,35 +338,44 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
                         acc[q][t][4 * r4 + 3]);
     __syncthreads();
     const int stop = n > 0 ? min(32, tokens - 32 * t) : 0;
-    for (int tk = tk0; tk < stop; tk += tk_step) {
-      const float* z = z0 + tk * P::PITCH;
-      auto sum = [&](const float* from) {              // the WK partial sums, in order
-        float4 v = *reinterpret_cast<const float4*>(from);
+    for (int tk = tk0; tk < stop; tk += CHUNK * tk_step) {
+      Residual next[CHUNK];
+      load_chunk(t, tk + CHUNK * tk_step, next);
 #pragma unroll
-        for (int k = 1; k < WK; ++k) {
-          const float4 x = *reinterpret_cast<const float4*>(from + k * WR * 32 * P::PITCH);
-          v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+      for (int c = 0; c < CHUNK; ++c) {
+        const int token = tk + c * tk_step;
+        if (token >= stop) break;
+        const float* z = z0 + token * P::PITCH;
+        auto sum = [&](const float* from) {            // the WK partial sums, in order
+          float4 v = *reinterpret_cast<const float4*>(from);
+#pragma unroll
+          for (int k = 1; k < WK; ++k) {
+            const float4 x = *reinterpret_cast<const float4*>(from + k * WR * 32 * P::PITCH);
+            v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+          }
+          return v;
+        };
+        float y[4];
+        scaled(sum(z), rs, y);
+        activate4(y, a.act);
+        if (a.gated) {
+          float g[4];
+          scaled(sum(z + 64), up, g);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) y[j] *= g[j];
         }
-        return v;
-      };
-      float y[4];
-      scaled(sum(z), rs, y);
-      activate4(y, a.act);
-      if (a.gated) {
-        float g[4];
-        scaled(sum(z + 64), up, g);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] *= g[c];
+        store4(y, n, types, r[c], a.residual != nullptr, a.out,
+               (slice_row + 32 * t + token) * a.ldo + out0 + o);
       }
-      const int64_t row = row0 + 32 * t + tk;
-      finish4(y, n, types, a.residual, row * a.ldr + out0 + o, a.out, row * a.ldo + out0 + o);
+#pragma unroll
+      for (int c = 0; c < CHUNK; ++c) r[c] = next[c];
     }
   }
 }
 
-template <int NP, int WR, int WK, int TT>
+template <int NP, int WR, int WK, int TT, bool ONE>
 hipError_t launch(const F6Product& p, hipStream_t st) {
-  using P = Shape<NP, WR, WK, TT>;
+  using P = Shape<NP, WR, WK, TT, ONE>;
   F6Product a = p;
   const int64_t outs = a.gated ? P::ROWS / 2 : P::ROWS;
   const int64_t out_m = a.gated ? a.m / 2 : a.m;
@@ -351,9 +383,9 @@ hipError_t launch(const F6Product& p, hipStream_t st) {
   int64_t tiles = (a.R + P::TOK - 1) / P::TOK;
   if (a.offsets) tiles = a.R / P::TOK + (a.E < a.R ? a.E : a.R);
   a.token_tiles = static_cast<int>(tiles);
-  const int64_t grid = (tiles * a.row_tiles + 7) / 8 * 8;
+  const int64_t grid = (tiles * a.row_tiles * a.slices + 7) / 8 * 8;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  auto* k = gemm_f6_kernel<NP, WR, WK, TT>;
+  auto* k = gemm_f6_kernel<NP, WR, WK, TT, ONE>;
   static const hipError_t big = hipFuncSetAttribute(
       reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, P::LDS);
   if (big != hipSuccess) return big;
@@ -362,29 +394,51 @@ hipError_t launch(const F6Product& p, hipStream_t st) {
 }
 
 template <int NP>
-hipError_t choose(const F6Product& p, hipStream_t st) {
-  // rows per tile: the tallest that still leaves a workgroup per compute
-  // unit; 64 tokens unless the runs are short
-  const int64_t out_m = p.gated ? p.m / 2 : p.m;
-  const int64_t runs = p.offsets ? (p.E < p.R ? p.E : p.R) : 1;
-  const bool two = p.R > 32 * runs;
-  auto count = [&](int WR, int TT) {
-    const int64_t outs = (p.gated ? 64 : 128) * WR;
-    return (p.R / (32 * TT) + runs) * ((out_m + outs - 1) / outs);
-  };
-  const int64_t cus = num_cus();
-  if constexpr (NP == 3)
-    if (two && count(4, 2) >= cus) return launch<NP, 4, 1, 2>(p, st);
-  if (two && count(2, 2) >= cus) return launch<NP, 2, 4, 2>(p, st);
-  if (count(4, 1) >= 2 * cus) return launch<NP, 4, 1, 1>(p, st);
-  if (count(2, 1) >= cus) return launch<NP, 2, 2, 1>(p, st);
-  return launch<NP, 1, 4, 1>(p, st);
+hipError_t by_shape(const F6Product& p, int shape, hipStream_t st) {
+  switch (shape) {
+    case 4120: if constexpr (NP == 3) return launch<NP, 4, 1, 2, false>(p, st); break;
+    case 2220: return launch<NP, 2, 2, 2, false>(p, st);
+    case 2421: return launch<NP, 2, 4, 2, true>(p, st);
+    case 4221: if constexpr (NP == 3) return launch<NP, 4, 2, 2, true>(p, st); break;
+    case 4110: return launch<NP, 4, 1, 1, false>(p, st);
+    case 2210: return launch<NP, 2, 2, 1, false>(p, st);
+    case 2211: return launch<NP, 2, 2, 1, true>(p, st);
+    case 2411: return launch<NP, 2, 4, 1, true>(p, st);
+    case 1410: return launch<NP, 1, 4, 1, false>(p, st);
+    case 1411: return launch<NP, 1, 4, 1, true>(p, st);
+    default: break;
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-hipError_t launch_gemm_f6(const F6Product& p, int NP, hipStream_t st) {
-  return NP == 3 ? choose<3>(p, st) : choose<4>(p, st);
+F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
+                        bool grouped) {
+  F6ManyPlan p{};
+  const int64_t cus = num_cus(), units = padded_positions(K) / 256;
+  const int64_t runs = grouped ? (E < R ? E : R) : 1;
+  const int64_t out_m = gated ? m / 2 : m;
+  const bool two = R > 32 * runs;
+  auto count = [&](int WR, int TT) {
+    const int64_t outs = (gated ? 64 : 128) * WR;
+    return (R / (32 * TT) + runs) * ((out_m + outs - 1) / outs);
+  };
+  p.slices = 1;
+  if (NP == 3 && two && count(4, 2) >= cus) p.shape = 4120;
+  else if (two && count(2, 2) >= cus) p.shape = 2421;
+  else if (count(4, 1) >= 2 * cus) p.shape = 4110;
+  else if (count(2, 1) >= cus) p.shape = 2210;
+  else p.shape = 1410;
+  p.slice_units = static_cast<int>((units + p.slices - 1) / p.slices);
+  p.slices = static_cast<int>((units + p.slice_units - 1) / p.slice_units);
+  p.ldz = (m + 3) / 4 * 4;
+  p.sums_bytes = p.slices > 1 ? static_cast<size_t>(p.slices) * R * p.ldz * 4 : 0;
+  return p;
+}
+
+hipError_t launch_gemm_f6(const F6Product& p, int shape, int NP, hipStream_t st) {
+  return NP == 3 ? by_shape<3>(p, shape, st) : by_shape<4>(p, shape, st);
 }
 
 }  // namespace lq

@@ -27,6 +27,8 @@
 #include "f6_product.h"
 #include "lq_internal.h"
 
+#include <cstring>
+
 namespace lq {
 namespace {
 
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
     }
     if (i16 >= tokens) continue;
     const int64_t row = row0 + i16;
-    const bool whole = f.sums == nullptr;
+    const bool whole = a.sums == nullptr;
 #pragma unroll
     for (int t = 0; t < T; ++t) {
       const int o = column(rb, t), left = min(4, out_m - o);
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[t][c] = z[c];
       if (!whole) {
-        float* to = f.sums + (slice * static_cast<int64_t>(a.R) + row) * f.ldz + col;
+        float* to = a.sums + (slice * static_cast<int64_t>(a.R) + row) * a.ldz + col;
         if (left == 4 && col % 4 == 0) *reinterpret_cast<f32x4*>(to) = acc[t];
         else
 #pragma unroll
@@ -299,68 +301,16 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
   }
 }
 
-// The slices' scaled sums added in order, and the epilogue: a thread per row
-// and four outputs, four slices' loads on their way at once.
-__global__ void __launch_bounds__(128) gemv_f6_reduce_kernel(F6Few f) {
-  const F6Product& a = f.p;
-  const int out_m = a.gated ? a.m / 2 : a.m;
-  const int o = (blockIdx.x * 128 + threadIdx.x) * 4;
-  const int64_t row = blockIdx.y;
-  const int n = min(4, out_m - o);
-  if (n <= 0) return;
-  // rows outside the runs are left as they were
-  if (a.offsets && (row < a.offsets[0] || row >= a.offsets[a.E])) return;
-  const int64_t step = static_cast<int64_t>(a.R) * f.ldz;
-  auto sum = [&](int col, float (&v)[4]) {
-    const float* z = f.sums + row * f.ldz + col;
-    const bool whole = col % 4 == 0;            // rows are padded to whole fours
-    for (int q = 0; q < f.slices; q += 4) {
-      float x[4][4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const float* from = z + min(q + c, f.slices - 1) * step;
-        if (whole) {
-          const float4 y = *reinterpret_cast<const float4*>(from);
-          x[c][0] = y.x; x[c][1] = y.y; x[c][2] = y.z; x[c][3] = y.w;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[c][j] = from[min(j, n - 1)];
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += q + c < f.slices ? x[c][j] : 0.f;
-    }
-  };
-  float y[4] = {}, up[4] = {};
-  sum(o, y);
-  if (a.gated) sum(out_m + o, up);
-  activate4(y, a.act);
-  if (a.gated) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] *= up[j];
-  }
-  finish4(y, n, output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt), a.residual,
-          row * a.ldr + o, a.out, row * a.ldo + o);
-}
-
 template <int NP, int T, int DEPTH, bool BF16>
 hipError_t launch(const F6Few& f, int tiles, hipStream_t st) {
   auto* k = gemv_f6_kernel<NP, T, DEPTH, BF16>;
   static const hipError_t big = hipFuncSetAttribute(
       reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
   if (big != hipSuccess) return big;
-  const dim3 grid((f.row_blocks + f.blocks_per - 1) / f.blocks_per, f.slices, tiles);
+  const dim3 grid((f.row_blocks + f.blocks_per - 1) / f.blocks_per, f.p.slices, tiles);
   const int lds = f.exchange_at + (f.kv > 1 ? kWaves * T * 1024 : 0);
   k<<<grid, 64 * kWaves, lds, st>>>(f);
-  hipError_t e = hipGetLastError();
-  if (e == hipSuccess && f.sums && f.p.out) {
-    const int out_m = f.p.gated ? f.p.m / 2 : f.p.m;
-    gemv_f6_reduce_kernel<<<dim3((out_m + 511) / 512, f.p.R), 128, 0, st>>>(f);
-    e = hipGetLastError();
-  }
-  return e;
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -371,11 +321,10 @@ hipError_t launch(const F6Few& f, int tiles, hipStream_t st) {
 // (0.7 of it arithmetic, the rest every workgroup's loads of them); a compute unit's share of the HBM rate 21 KB per us (16 with
 // T = 1, where reading the operands from LDS is the limit); a second launch 3 us
 // (the join has one anyway) and its sums at about 4 TB/s.
-F6FewPlan few_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
-                      bool grouped, bool join) {
+static F6FewPlan find_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
+                           bool grouped, bool join, int64_t cus) {
   F6FewPlan p{};
   const int64_t runs = grouped ? (E < R ? E : R) : 1;
-  const int64_t cus = num_cus();
   p.groups = static_cast<int>(padded_positions(K) / 512);
   // a tile holds twice the average run, so that few runs need a second one
   const int64_t average = (R + runs - 1) / runs;
@@ -423,6 +372,28 @@ F6FewPlan few_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, in
   p.ldz = (m + 3) / 4 * 4;
   p.sums_bytes = p.slices > 1 ? static_cast<size_t>(p.slices) * R * p.ldz * 4 : 0;
   return p;
+}
+
+// The search takes some microseconds: each thread keeps the plans of the
+// shapes it met last (they follow from the sizes alone).
+F6FewPlan few_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
+                      bool grouped, bool join) {
+  struct Entry {
+    int64_t key[6] = {-1, -1, -1, -1, -1, -1};
+    F6FewPlan plan;
+  };
+  constexpr int kKept = 64;
+  thread_local Entry kept[kKept];
+  const int64_t cus = num_cus();
+  const int64_t key[6] = {E, m, K, R, cus, NP * 8 + gated * 4 + grouped * 2 + join};
+  uint64_t hash = 0;
+  for (int64_t k : key) hash = (hash + static_cast<uint64_t>(k)) * 0x9E3779B97F4A7C15ull;
+  Entry& e = kept[hash >> 58];
+  if (std::memcmp(e.key, key, sizeof key)) {
+    e.plan = find_plan(E, m, K, R, gated, NP, grouped, join, cus);
+    std::memcpy(e.key, key, sizeof key);
+  }
+  return e.plan;
 }
 
 hipError_t launch_gemv_f6(const F6Few& f, const F6FewPlan& plan, int NP, hipStream_t st) {

@@ -203,10 +203,11 @@ lq_status route_sizes(int64_t T, int64_t E, int32_t k) {
 struct F6Plan {
   bool few;
   lq::F6FewPlan fp;
+  lq::F6ManyPlan mp;
   int NP;
   int64_t row_bytes, image_rows;
-  int z_slices;                // float32 rows of lq_gemm_join: slices, offset, pitch
-  size_t z_at;
+  int slices;
+  size_t sums_at;              // float32 [slices][R][ldz]: the slices' sums, lq_gemm_join's rows
   int64_t ldz;
   size_t bytes;
 };
@@ -224,31 +225,31 @@ F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtyp
   p.few = R <= kFewRows || (grouped && R <= kFewRowsPerRun * (E < R ? E : R));
   if (p.few) {
     p.fp = lq::few_f6_plan(E, m, K, R < 1 ? 1 : R, gated, p.NP, grouped, join);
-    p.bytes = round256(p.fp.sums_bytes);
-    if (join) {                // the join reads the slices itself, one or several
-      p.z_slices = p.fp.slices;
-      p.ldz = p.fp.ldz;
-      p.bytes = round256(static_cast<size_t>(p.fp.slices) * R * p.ldz * 4);
-      return p;
-    }
+    p.slices = p.fp.slices;
   } else {
+    p.mp = lq::many_f6_plan(E, m, K, R, gated, p.NP, grouped);
+    p.slices = p.mp.slices;
     p.row_bytes = lq::f6::row_bytes(K, 2, p.NP);
     p.image_rows = rows + (grouped ? 1 : 0);      // a row of zeros behind the last
     p.bytes = round256(static_cast<size_t>(p.image_rows * p.row_bytes));
   }
-  if (join) {
-    p.z_slices = 1;
-    p.z_at = p.bytes;
-    p.ldz = (m + 3) / 4 * 4;
-    p.bytes += static_cast<size_t>(R) * p.ldz * 4;
-  }
+  p.sums_at = p.bytes;
+  p.ldz = (m + 3) / 4 * 4;
+  // the join reads the rows of one slice too
+  if (join || p.slices > 1) p.bytes += static_cast<size_t>(p.slices) * R * p.ldz * 4;
   return p;
 }
 
 // The product of a checked call: conversion where it is a launch of its own,
 // then the kernel.  p lacks only what the plan decides.
 hipError_t f6_run(lq::F6Product& p, const F6Plan& plan, int64_t K, const void* a, lq_dtype a_dt,
-                  int64_t lda, int64_t a_rows, void* workspace, hipStream_t st) {
+                  int64_t lda, int64_t a_rows, bool join, void* workspace, hipStream_t st) {
+  const bool to_sums = join || plan.slices > 1;
+  p.slices = plan.slices;
+  p.ldz = plan.ldz;
+  p.sums = to_sums ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.sums_at)
+                   : nullptr;
+  hipError_t e;
   if (plan.few) {
     lq::F6Few f{};
     p.groups = plan.fp.groups;
@@ -259,22 +260,31 @@ hipError_t f6_run(lq::F6Product& p, const F6Plan& plan, int64_t K, const void* a
     f.K = static_cast<int>(K);
     f.tok = plan.fp.tok;
     f.kv = plan.fp.kv;
-    f.slices = plan.fp.slices;
     f.slice_groups = plan.fp.slice_groups;
     f.row_blocks = plan.fp.row_blocks;
     f.blocks_per = plan.fp.blocks_per;
     f.exchange_at = plan.fp.exchange_at;
-    f.sums = plan.fp.slices > 1 || plan.z_slices ? static_cast<float*>(workspace) : nullptr;
-    f.ldz = plan.fp.ldz;
-    return lq::launch_gemv_f6(f, plan.fp, plan.NP, st);
+    e = lq::launch_gemv_f6(f, plan.fp, plan.NP, st);
+  } else {
+    p.img = static_cast<const uint8_t*>(workspace);
+    p.img_row_bytes = static_cast<uint32_t>(plan.row_bytes);
+    p.img_bytes = static_cast<uint32_t>(plan.image_rows * plan.row_bytes);
+    p.groups = static_cast<int>(lq::f6::padded_positions(K) / lq::f6::group_positions(2));
+    p.slice_units = plan.mp.slice_units;
+    e = lq::launch_f6_image(a, a_dt, a_rows, plan.image_rows > a_rows, K, lda, plan.NP, workspace,
+                            st);
+    lq::F6Product q = p;
+    if (to_sums) {             // plain scaled rows, in their own order
+      q.act = LQ_ACT_NONE;
+      q.gated = 0;
+      q.residual = nullptr;
+      q.out = p.sums;
+      q.ldo = p.ldz;
+      q.out_dt = LQ_F32;
+    }
+    if (e == hipSuccess) e = lq::launch_gemm_f6(q, plan.mp.shape, plan.NP, st);
   }
-  p.img = static_cast<const uint8_t*>(workspace);
-  p.img_row_bytes = static_cast<uint32_t>(plan.row_bytes);
-  p.img_bytes = static_cast<uint32_t>(plan.image_rows * plan.row_bytes);
-  p.groups = static_cast<int>(lq::f6::padded_positions(K) / lq::f6::group_positions(2));
-  hipError_t e = lq::launch_f6_image(a, a_dt, a_rows, plan.image_rows > a_rows, K, lda, 2, plan.NP,
-                                     workspace, st);
-  if (e == hipSuccess) e = lq::launch_gemm_f6(p, plan.NP, st);
+  if (e == hipSuccess && plan.slices > 1 && !join) e = lq::launch_f6_reduce(p, st);
   return e;
 }
 
@@ -758,7 +768,7 @@ lq_status lq_gemm_ep(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw
   p.R = static_cast<int>(B);
   p.src_rows = static_cast<int>(B);
   const hipStream_t hs = as_stream(stream);
-  const hipError_t e = f6_run(p, plan, K, a_lift, lift_dtype, lda, B, workspace, hs);
+  const hipError_t e = f6_run(p, plan, K, a_lift, lift_dtype, lda, B, false, workspace, hs);
   return hip_status(e, "lq_gemm_ep launch");
 }
 
@@ -809,7 +819,7 @@ lq_status lq_gemm_grouped(const uint32_t* w_packed, int64_t E, int64_t m, int64_
   p.rows = rows;
   p.src_rows = static_cast<int>(a_rows);
   const hipStream_t hs = as_stream(stream);
-  const hipError_t e = f6_run(p, plan, K, a_lift, lift_dtype, lda, a_rows, workspace, hs);
+  const hipError_t e = f6_run(p, plan, K, a_lift, lift_dtype, lda, a_rows, false, workspace, hs);
   return hip_status(e, "lq_gemm_grouped launch");
 }
 
@@ -845,21 +855,18 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
   if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
   if (st != LQ_OK) return st;
   const hipStream_t hs = as_stream(stream);
-  float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.z_at);
+  float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.sums_at);
   hipError_t e = hipSuccess;
   if (R > 0) {
     lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, LQ_ACT_NONE, 0);
-    p.out = plan.few ? nullptr : z;
-    p.ldo = plan.ldz;
-    p.out_dt = LQ_F32;
     p.R = static_cast<int>(R);
     p.offsets = offsets;
     p.E = static_cast<int>(E);
     p.src_rows = static_cast<int>(R);
-    e = f6_run(p, plan, K, a_lift, lift_dtype, lda, R, workspace, hs);
+    e = f6_run(p, plan, K, a_lift, lift_dtype, lda, R, true, workspace, hs);
   }
   if (e == hipSuccess)
-    e = lq::launch_join(z, plan.z_slices, R, m, plan.ldz, pos, weight, T, k, residual, ldr, out, ldo, out_dtype,
+    e = lq::launch_join(z, plan.slices, R, m, plan.ldz, pos, weight, T, k, residual, ldr, out, ldo, out_dtype,
                         hs);
   return hip_status(e, "lq_gemm_join launch");
 }

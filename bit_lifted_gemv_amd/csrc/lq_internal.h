@@ -186,6 +186,9 @@ struct F6Product {
   const int* rows;             // image row of each row, or null: its own
   int src_rows;                // rows of the image (with `rows`, one more of zeros follows)
   int row_tiles, token_tiles;  // set by the launcher
+  int slices, slice_units;     // of the positions, in units of 256
+  float* sums;                 // [slices][R][ldz] scaled sums of the slices, or null
+  int64_t ldz;
 };
 
 // The same for at most 16 rows per matrix (k_gemv_f6.hip), which splits its
@@ -203,21 +206,31 @@ struct F6FewPlan {
 F6FewPlan few_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
                       bool grouped, bool join);
 struct F6Few {
-  F6Product p;                 // groups: of 512 positions; no image; out null: only the sums
+  F6Product p;                 // groups: of 512 positions; no image; sums null: outputs at once
   const void* a;
   int a_dt;
   int64_t lda;
   int K;
-  int tok, kv, slices, slice_groups, row_blocks, blocks_per, exchange_at;
-  float* sums;                 // [slices][R][ldz] scaled sums, or null: outputs at once
-  int64_t ldz;
+  int tok, kv, slice_groups, row_blocks, blocks_per, exchange_at;
 };
 hipError_t launch_gemv_f6(const F6Few& f, const F6FewPlan& plan, int NP, hipStream_t st);
 
-// 16-bit activations -> parts image (k_f6_image.hip); H = 2 or 4, NP = 3 or 4.
+// 16-bit activations -> parts image (k_f6_image.hip); NP = 3 or 4.
 hipError_t launch_f6_image(const void* a, lq_dtype dt, int64_t rows, bool zero_row, int64_t K,
-                           int64_t lda, int H, int NP, void* img, hipStream_t st);
-hipError_t launch_gemm_f6(const F6Product& p, int NP, hipStream_t st);
+                           int64_t lda, int NP, void* img, hipStream_t st);
+// Tile shape (its four template digits) and slices of the product for many rows.
+struct F6ManyPlan {
+  int shape, slices, slice_units;
+  int64_t ldz;
+  size_t sums_bytes;
+};
+F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
+                        bool grouped);
+hipError_t launch_gemm_f6(const F6Product& p, int shape, int NP, hipStream_t st);
+
+// The slices' sums added in order, then activation, gate, residual and store
+// (k_f6_reduce.hip).
+hipError_t launch_f6_reduce(const F6Product& p, hipStream_t st);
 
 // out = residual + sum_j weight z[pos] (k_join.hip), z the sum of `slices`
 // arrays [R][ldz]; ldz a multiple of 4.
