@@ -26,31 +26,38 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive
   return v;
 }
 
-__device__ __forceinline__ int wave_total(int v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
-  return v;
+// What a wave knows of 64 experts' runs, lane e of expert e0 + e: bounds, and
+// tiles up to and with it.
+struct Runs {
+  int lo, end, tiles, upto;
+};
+__device__ __forceinline__ Runs load_runs(const F6Product& a, int e0, int before, int TOK, int lane) {
+  Runs r;
+  r.tiles = run_tiles(a, e0 + lane, TOK, r.lo, r.end);
+  r.upto = before + wave_scan(r.tiles, lane);
+  return r;
 }
-
-// The expert of tile `tile`, its first row and the end of its run; false past
-// the last tile.
+// The expert of tile `tile`, its first row and the end of its run, if it is
+// one of these 64.
+__device__ __forceinline__ bool find_in(const Runs& r, int e0, int tile, int TOK, int& expert,
+                                        int& row0, int& row_end) {
+  const uint64_t hit = __ballot(r.upto > tile);
+  if (!hit) return false;
+  const int l = __builtin_ctzll(hit);
+  const int first = __shfl(r.upto - r.tiles, l);
+  expert = __builtin_amdgcn_readfirstlane(e0 + l);
+  row_end = __builtin_amdgcn_readfirstlane(__shfl(r.end, l));
+  row0 = __builtin_amdgcn_readfirstlane(__shfl(r.lo, l) + (tile - first) * TOK);
+  return true;
+}
+// The same over all experts; false past the last tile.
 __device__ __forceinline__ bool find_run(const F6Product& a, int tile, int TOK, int lane,
                                          int& expert, int& row0, int& row_end) {
   int before = 0;
   for (int e0 = 0; e0 < a.E; e0 += 64) {
-    int lo, end;
-    const int n = run_tiles(a, e0 + lane, TOK, lo, end);
-    const int upto = before + wave_scan(n, lane);
-    const uint64_t hit = __ballot(upto > tile);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      const int first = __shfl(upto - n, l);
-      expert = __builtin_amdgcn_readfirstlane(e0 + l);
-      row_end = __builtin_amdgcn_readfirstlane(__shfl(end, l));
-      row0 = __builtin_amdgcn_readfirstlane(__shfl(lo, l)) + (tile - first) * TOK;
-      return true;
-    }
-    before = __shfl(upto, 63);
+    const Runs r = load_runs(a, e0, before, TOK, lane);
+    if (find_in(r, e0, tile, TOK, expert, row0, row_end)) return true;
+    before = __shfl(r.upto, 63);
   }
   return false;
 }

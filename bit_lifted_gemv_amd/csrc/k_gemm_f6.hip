@@ -118,11 +118,13 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   // workgroups of an XCD (every eighth block) share parts and signs in its L2
   const int RT = a.row_tiles;
   int tiles = a.token_tiles;
+  Runs runs{};                           // of the last 64 experts: all of them up to 64
   if (a.offsets) {
     tiles = 0;
-    int lo, end;
-    for (int e0 = 0; e0 < a.E; e0 += 64)
-      tiles += uniform(wave_total(run_tiles(a, e0 + lane, TOK, lo, end)));
+    for (int e0 = 0; e0 < a.E; e0 += 64) {
+      runs = load_runs(a, e0, tiles, TOK, lane);
+      tiles = uniform(__shfl(runs.upto, 63));
+    }
   }
   const int total = tiles * RT * a.slices;
   const int chunk = (total + 7) / 8;
@@ -134,7 +136,10 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   int tile = 2 * pair + in % wide;
   const int rt = in / wide;
   int expert = 0, row0 = tile * TOK, row_end = a.R;
-  if (a.offsets) find_run(a, tile, TOK, lane, expert, row0, row_end);
+  if (a.offsets) {
+    if (a.E <= 64) find_in(runs, 0, tile, TOK, expert, row0, row_end);
+    else find_run(a, tile, TOK, lane, expert, row0, row_end);
+  }
   const int tokens = min(TOK, row_end - row0);
 
   const uint32_t* w = a.w + static_cast<int64_t>(expert) * a.m * a.ldw;
@@ -397,15 +402,12 @@ template <int NP>
 hipError_t by_shape(const F6Product& p, int shape, hipStream_t st) {
   switch (shape) {
     case 4120: if constexpr (NP == 3) return launch<NP, 4, 1, 2, false>(p, st); break;
-    case 2220: return launch<NP, 2, 2, 2, false>(p, st);
     case 2421: return launch<NP, 2, 4, 2, true>(p, st);
     case 4221: if constexpr (NP == 3) return launch<NP, 4, 2, 2, true>(p, st); break;
     case 4110: return launch<NP, 4, 1, 1, false>(p, st);
     case 2210: return launch<NP, 2, 2, 1, false>(p, st);
-    case 2211: return launch<NP, 2, 2, 1, true>(p, st);
     case 2411: return launch<NP, 2, 4, 1, true>(p, st);
     case 1410: return launch<NP, 1, 4, 1, false>(p, st);
-    case 1411: return launch<NP, 1, 4, 1, true>(p, st);
     default: break;
   }
   return hipErrorInvalidValue;
@@ -420,16 +422,38 @@ F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
   const int64_t runs = grouped ? (E < R ? E : R) : 1;
   const int64_t out_m = gated ? m / 2 : m;
   const bool two = R > 32 * runs;
+  // tiles of 128 WR rows and 32 TT tokens; of runs, half end inside a tile
   auto count = [&](int WR, int TT) {
-    const int64_t outs = (gated ? 64 : 128) * WR;
-    return (R / (32 * TT) + runs) * ((out_m + outs - 1) / outs);
+    const int64_t outs = (gated ? 64 : 128) * WR, tok = 32 * TT;
+    const int64_t tiles = grouped ? R / tok + (runs + 1) / 2 : (R + tok - 1) / tok;
+    return tiles * ((out_m + outs - 1) / outs);
   };
+  // The tallest tile that fills the compute units, measured on each side:
+  // 512 x 64 in two workgroups of four waves per unit (4096 x 8192 -> 28672:
+  // 1175 us; 256 x 64 in eight waves 1400), or in one of eight where there is
+  // one tile each (1024 x 19456 -> 8192: 231 against 243); 256 x 64 (512 x
+  // 20480 -> 8192: 135; 512 x 64 in eight waves 174, 256 x 32 152); 256 x 32 in
+  // eight waves for one tile each (64 x 8192 -> 28672: 36; four waves 39).
+  // Where 128 x 32 tiles leave units empty, the positions are split into
+  // slices (64 x 10240 -> 4096: 4 slices 20, one 31), down to 512 positions
+  // each, or 8192 to put two workgroups on a unit (24 x 68096 -> 8192: 8
+  // slices 46, 4 slices 51).
   p.slices = 1;
-  if (NP == 3 && two && count(4, 2) >= cus) p.shape = 4120;
-  else if (two && count(2, 2) >= cus) p.shape = 2421;
+  if (NP == 3 && two && count(4, 2) > cus) p.shape = 4120;
+  else if (NP == 3 && two && count(4, 2) * 5 >= cus * 4) p.shape = 4221;
+  else if (two && count(2, 2) * 5 >= cus * 4) p.shape = 2421;
   else if (count(4, 1) >= 2 * cus) p.shape = 4110;
-  else if (count(2, 1) >= cus) p.shape = 2210;
-  else p.shape = 1410;
+  else if (count(2, 1) > cus) p.shape = 2210;
+  else if (count(2, 1) * 4 >= cus * 3) p.shape = 2411;
+  else {
+    p.shape = 1410;
+    const int64_t tiles = count(1, 1);
+    const int64_t one = cus / tiles, both = 2 * cus / tiles;
+    p.slices = static_cast<int>(units / (both < 1 ? 1 : both) >= 32 ? both : one);
+    if (p.slices > units / 2) p.slices = static_cast<int>(units / 2);
+    if (p.slices > 16) p.slices = 16;
+    if (p.slices < 1) p.slices = 1;
+  }
   p.slice_units = static_cast<int>((units + p.slices - 1) / p.slices);
   p.slices = static_cast<int>((units + p.slice_units - 1) / p.slice_units);
   p.ldz = (m + 3) / 4 * 4;

@@ -212,7 +212,7 @@ struct F6Plan {
   size_t bytes;
 };
 
-constexpr int64_t kFewRows = 16, kFewRowsPerRun = 8;
+constexpr int64_t kFewRows = 16, kFewRowsPerRun = 8, kFewBytes = 10 << 20;
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -221,8 +221,12 @@ F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtyp
                bool gated, bool grouped, bool join) {
   F6Plan p{};
   p.NP = f6_parts_count(out_dtype);
-  // few rows: up to 16 in all, or about 8 a run on average
-  p.few = R <= kFewRows || (grouped && R <= kFewRowsPerRun * (E < R ? E : R));
+  // few rows: up to 16 in all, or so few signs that reading them for every 16
+  // rows costs less than the other kernel's launches (32 x 10240 -> 4096: 17 us
+  // on either; 64 x 4096 -> 2048: 11 against 14; 48 x 10240 -> 4096: 24 against
+  // 19), or about 8 a run on average
+  p.few = grouped ? R <= kFewRowsPerRun * (E < R ? E : R)
+                  : R <= kFewRows || (R + 15) / 16 * m * (K / 8) <= kFewBytes;
   if (p.few) {
     p.fp = lq::few_f6_plan(E, m, K, R < 1 ? 1 : R, gated, p.NP, grouped, join);
     p.slices = p.fp.slices;

@@ -11,6 +11,7 @@ uint32 words).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -441,42 +442,37 @@ def gemm(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor, K: Optio
 
 
 # ------------------------------------- products with an epilogue, experts, router
-class _On:
-    """The device and stream that one of the calls below runs on: the
-    tensors' device (current or not) and its current stream, or `stream`.
-    Temporary workspaces come from torch's allocator on that stream, a new
-    one for every call, so that calls on two streams or captured graphs never
-    share one."""
+def _elsewhere(device: torch.device) -> bool:
+    """Whether the tensors' device is not the current one (the calls below then
+    run under it)."""
+    return device.index != torch.cuda.current_device()
 
-    __slots__ = ("device", "stream", "handle", "guard")
 
-    def __init__(self, device: torch.device, stream):
-        self.device = device
-        self.stream = stream
-        self.guard = None
-        if stream is None:
-            # the raw handle: torch.cuda.current_stream builds a Stream object (2 us)
-            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
-        else:
-            self.handle = stream.cuda_stream
+def _handle(device: torch.device, stream) -> int:
+    """The HIP stream of a call: `stream`, or the device's current one (its raw
+    handle: torch.cuda.current_stream builds a Stream object, 2 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+@functools.lru_cache(maxsize=4096)
+def _bytes_needed(call: str, *sizes: int) -> int:
+    n = _sz(0)
+    check(getattr(lib(), call)(*sizes, ctypes.byref(n)))
+    return n.value
 
-    def workspace(self, nbytes: int) -> Optional[torch.Tensor]:
-        if not nbytes:
-            return None
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        if self.stream is not None:
-            ws.record_stream(self.stream)
-        return ws
+
+def _temporary(nbytes: int, device: torch.device, stream) -> Optional[torch.Tensor]:
+    """A workspace from torch's allocator on the call's stream, a new one for
+    every call, so that calls on two streams or captured graphs never share
+    one; returned memory is reused in stream order."""
+    if not nbytes:
+        return None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
 
 
 def _same_device(device: torch.device, **tensors: Optional[torch.Tensor]) -> None:
@@ -491,7 +487,7 @@ def _plain(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tupl
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -499,7 +495,7 @@ def _plain(name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tupl
 
 def _pitch(name: str, t: torch.Tensor, shape: tuple, dtype: Optional[torch.dtype] = None) -> int:
     """Row pitch of a matrix whose rows are dense and may lie apart."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
@@ -556,19 +552,20 @@ def gemm_ep(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
     dev = a_lift.device
     _experts(w_packed, s, bias, (m,))
     _same_device(dev, w_packed=w_packed, s=s, bias=bias, residual=residual, out=out)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return gemm_ep(w_packed, s, a_lift, bias, act, gated, residual, out_dtype, out, stream)
     lda = _lifted(a_lift)
     width = m // 2 if gated else m
     code = _act(act)
-    with _On(dev, stream) as on:
-        out, ldo = _target(out, B, width, out_dtype, a_lift)
-        ldr = 0 if residual is None else _pitch("residual", residual, (B, width), out.dtype)
-        n = _sz(0)
-        L = lib()
-        check(L.lq_gemm_ep_workspace_size(m, K, B, _dt(out), ctypes.byref(n)))
-        ws = on.workspace(n.value)
-        check(L.lq_gemm_ep(_ptr(w_packed), m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift), lda, B,
-                           _ptr(bias), code, int(gated), _ptr(residual), ldr, _ptr(out), _dt(out),
-                           ldo, _ptr(ws), n.value, on.handle))
+    out, ldo = _target(out, B, width, out_dtype, a_lift)
+    odt = _dt(out)
+    ldr = 0 if residual is None else _pitch("residual", residual, (B, width), out.dtype)
+    nb = _bytes_needed("lq_gemm_ep_workspace_size", m, K, B, odt)
+    ws = _temporary(nb, dev, stream)
+    check(lib().lq_gemm_ep(_ptr(w_packed), m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift), lda, B,
+                           _ptr(bias), code, int(gated), _ptr(residual), ldr, _ptr(out), odt, ldo,
+                           _ptr(ws), nb, _handle(dev, stream)))
     return out
 
 
@@ -589,19 +586,20 @@ def gemm_grouped(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
     _plain("offsets", offsets, torch.int32, (E + 1,))
     _plain("rows", rows, torch.int32, (R,))
     _same_device(dev, w_packed=w_packed, s=s, bias=bias, offsets=offsets, rows=rows, out=out)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return gemm_grouped(w_packed, s, a_lift, offsets, rows, bias, act, gated, out_dtype,
+                                out, stream)
     lda = _lifted(a_lift)
-    width = m // 2 if gated else m
     code = _act(act)
-    with _On(dev, stream) as on:
-        out, ldo = _target(out, R, width, out_dtype, a_lift)
-        n = _sz(0)
-        L = lib()
-        check(L.lq_gemm_grouped_workspace_size(E, m, K, n_rows, R, _dt(out), ctypes.byref(n)))
-        ws = on.workspace(n.value)
-        check(L.lq_gemm_grouped(_ptr(w_packed), E, m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift),
+    out, ldo = _target(out, R, m // 2 if gated else m, out_dtype, a_lift)
+    odt = _dt(out)
+    nb = _bytes_needed("lq_gemm_grouped_workspace_size", E, m, K, n_rows, R, odt)
+    ws = _temporary(nb, dev, stream)
+    check(lib().lq_gemm_grouped(_ptr(w_packed), E, m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift),
                                 lda, n_rows, _ptr(rows), _ptr(offsets), R, _ptr(bias), code,
-                                int(gated), _ptr(out), _dt(out), ldo, _ptr(ws), n.value,
-                                on.handle))
+                                int(gated), _ptr(out), odt, ldo, _ptr(ws), nb,
+                                _handle(dev, stream)))
     return out
 
 
@@ -623,18 +621,20 @@ def gemm_join(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
     _plain("weight", weight, torch.float32, (T, k))
     _same_device(dev, w_packed=w_packed, s=s, bias=bias, offsets=offsets, pos=pos, weight=weight,
                  residual=residual, out=out)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return gemm_join(w_packed, s, a_lift, offsets, pos, weight, bias, residual, out_dtype,
+                             out, stream)
     lda = _lifted(a_lift)
-    with _On(dev, stream) as on:
-        out, ldo = _target(out, T, m, out_dtype, a_lift)
-        ldr = 0 if residual is None else _pitch("residual", residual, (T, m), out.dtype)
-        n = _sz(0)
-        L = lib()
-        check(L.lq_gemm_join_workspace_size(E, m, K, R, T, k, _dt(out), ctypes.byref(n)))
-        ws = on.workspace(n.value)
-        check(L.lq_gemm_join(_ptr(w_packed), E, m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift),
+    out, ldo = _target(out, T, m, out_dtype, a_lift)
+    odt = _dt(out)
+    ldr = 0 if residual is None else _pitch("residual", residual, (T, m), out.dtype)
+    nb = _bytes_needed("lq_gemm_join_workspace_size", E, m, K, R, T, k, odt)
+    ws = _temporary(nb, dev, stream)
+    check(lib().lq_gemm_join(_ptr(w_packed), E, m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift),
                              lda, _ptr(offsets), R, _ptr(bias), _ptr(pos), _ptr(weight), T, k,
-                             _ptr(residual), ldr, _ptr(out), _dt(out), ldo, _ptr(ws), n.value,
-                             on.handle))
+                             _ptr(residual), ldr, _ptr(out), odt, ldo, _ptr(ws), nb,
+                             _handle(dev, stream)))
     return out
 
 
@@ -663,20 +663,20 @@ def route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None, re
         valid = valid.view(torch.uint8)
     _plain("valid", valid, torch.uint8, (T,))
     _same_device(dev, valid=valid)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return route(logits, k, valid, renorm, stream)
     ld = _pitch("logits", logits, (T, E))
     code = _dt(logits)
-    with _On(dev, stream) as on:
-        n = _sz(0)
-        L = lib()
-        check(L.lq_route_workspace_size(T, E, k, ctypes.byref(n)))
-        ws = on.workspace(n.value)
-        ids, pos, rows = torch.empty((3, T, k), dtype=torch.int32, device=dev).unbind()
-        weight = torch.empty((T, k), dtype=torch.float32, device=dev)
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        rows = rows.view(-1)
-        check(L.lq_route(_ptr(logits), code, T, E, ld, _ptr(valid), k, int(renorm), _ptr(ids),
-                         _ptr(weight), _ptr(pos), _ptr(rows), _ptr(offsets), _ptr(ws), n.value,
-                         on.handle))
+    nb = _bytes_needed("lq_route_workspace_size", T, E, k)
+    ws = _temporary(nb, dev, stream)
+    ids, pos, rows = torch.empty((3, T, k), dtype=torch.int32, device=dev).unbind()
+    rows = rows.view(-1)
+    weight = torch.empty((T, k), dtype=torch.float32, device=dev)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    check(lib().lq_route(_ptr(logits), code, T, E, ld, _ptr(valid), k, int(renorm), _ptr(ids),
+                         _ptr(weight), _ptr(pos), _ptr(rows), _ptr(offsets), _ptr(ws), nb,
+                         _handle(dev, stream)))
     return Routing(ids, weight, pos, rows, offsets)
 
 

@@ -24,8 +24,8 @@ def size(f, *args):
 
 
 def ep(L, **over):
-    a = dict(w=P, m=64, K=128, ldw=4, s=P, a=P, dt=BF16, lda=128, B=300, bias=None, act=0, gated=0,
-             res=None, ldr=0, out=P, odt=BF16, ldo=64, ws=P, n=1 << 30)
+    a = dict(w=P, m=4096, K=4096, ldw=128, s=P, a=P, dt=BF16, lda=4096, B=300, bias=None, act=0,
+             gated=0, res=None, ldr=0, out=P, odt=BF16, ldo=4096, ws=P, n=1 << 30)
     a.update(over)
     return L.lq_gemm_ep(a["w"], a["m"], a["K"], a["ldw"], a["s"], a["a"], a["dt"], a["lda"], a["B"],
                         a["bias"], a["act"], a["gated"], a["res"], a["ldr"], a["out"], a["odt"],
@@ -36,12 +36,12 @@ def ep(L, **over):
     (dict(w=None), NULL), (dict(s=None), NULL), (dict(a=None), NULL), (dict(out=None), NULL),
     (dict(dt=F32), DTYPE), (dict(dt=7), DTYPE), (dict(odt=9), DTYPE), (dict(act=5), UNSUPPORTED),
     (dict(act=-1), UNSUPPORTED), (dict(m=0), SHAPE), (dict(m=63, gated=1), SHAPE), (dict(K=0), SHAPE),
-    (dict(K=124), SHAPE), (dict(K=(1 << 22) + 8, lda=1 << 23, ldw=1 << 18), SHAPE), (dict(B=0), SHAPE),
-    (dict(B=-1), SHAPE), (dict(B=1 << 31), SHAPE), (dict(ldw=3), SHAPE), (dict(ldw=6), ALIGN),
-    (dict(m=1 << 20, ldw=1024), SHAPE), (dict(lda=120), SHAPE), (dict(lda=132), ALIGN),
+    (dict(K=4092), SHAPE), (dict(K=(1 << 22) + 8, lda=1 << 23, ldw=1 << 18), SHAPE), (dict(B=0), SHAPE),
+    (dict(B=-1), SHAPE), (dict(B=1 << 31), SHAPE), (dict(ldw=3), SHAPE), (dict(ldw=130), ALIGN),
+    (dict(m=1 << 20, ldw=1024), SHAPE), (dict(lda=120), SHAPE), (dict(lda=4100), ALIGN),
     (dict(w=P + 8), ALIGN), (dict(a=P + 8), ALIGN), (dict(s=MIS), ALIGN), (dict(bias=MIS), ALIGN),
     (dict(ldo=63), SHAPE), (dict(res=P, ldr=63), SHAPE), (dict(out=P + 1), ALIGN),
-    (dict(res=P + 1, ldr=64), ALIGN), (dict(odt=F32, out=MIS), ALIGN), (dict(ws=None), WORKSPACE),
+    (dict(res=P + 1, ldr=4096), ALIGN), (dict(odt=F32, out=MIS), ALIGN), (dict(ws=None), WORKSPACE),
     (dict(n=0), WORKSPACE), (dict(ws=P + 16), ALIGN), (dict(B=1 << 22, K=1024, ldw=32, lda=1024), SHAPE),
 ])
 def test_gemm_ep_refusals(L, over, status):
@@ -52,11 +52,11 @@ def test_gemm_ep_refusals(L, over, status):
 def test_gemm_ep_workspace(L):
     f = L.lq_gemm_ep_workspace_size
     assert size(f, 64, 128, 3, BF16) == 0          # few rows, short: none
-    need = size(f, 64, 128, 300, BF16)
+    need = size(f, 4096, 4096, 300, BF16)
     assert need > 0
     assert ep(L, n=need - 1) == WORKSPACE
     assert size(f, 8192, 68096, 16, BF16) > 0      # sums of the slices
-    assert size(f, 64, 128, 300, F32) > size(f, 64, 128, 300, BF16)
+    assert size(f, 4096, 4096, 300, F32) > need
     n = ctypes.c_size_t(0)
     assert f(64, 128, 3, BF16, None) == NULL
     assert f(0, 128, 3, BF16, ctypes.byref(n)) == SHAPE
