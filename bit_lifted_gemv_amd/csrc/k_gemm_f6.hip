@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   const uint32_t two = held(0x22222222u);
   f32x16 acc[4][TT] = {};
   i32x8 b[TT][NP], sign[4];
-  uint32_t word[4], ex[TT];
+  uint32_t word[4][NU], ex[TT];            // of a stage: every step of the wave
   int scale[TT][NP];
   auto step_group = [&](int) { return SEC == 2 ? wk >> 1 : 0; };
   auto step_u = [&](int u) { return SEC == 2 ? wk & 1 : wk * NU + u; };
@@ -215,11 +215,11 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
     b[t][p][0] = lo.x; b[t][p][1] = lo.y; b[t][p][2] = lo.z; b[t][p][3] = lo.w;
     b[t][p][4] = hi.x; b[t][p][5] = hi.y; b[t][p][6] = 0; b[t][p][7] = 0;
   };
-  auto read_exponents = [&](int slot, int u) {
+  auto read_exponents = [&](int slot) {
 #pragma unroll
     for (int t = 0; t < TT; ++t)
       ex[t] = *reinterpret_cast<const uint32_t*>(
-          lds + slot * P::STAGE + step_group(u) * TOK * P::GB + (32 * t + i32) * P::GB +
+          lds + slot * P::STAGE + step_group(0) * TOK * P::GB + (32 * t + i32) * P::GB +
           exp_offset(2, NP));
   };
   auto set_scales = [&](int u) {
@@ -229,13 +229,20 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
       for (int p = 0; p < NP; ++p)
         scale[t][p] = static_cast<int>(ex[t] >> (16 * h + 8 * step_u(u)) & 255u) - 4 * p;
   };
-  // j: group of the pair that the unit covers
-  auto read_words = [&](int slot, int j, int u) {
+  // j: group of the pair that the unit covers; one step's word, or both
+  auto read_words = [&](int slot, int j) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      word[q] = *reinterpret_cast<const uint32_t*>(
-          lds + SIGNS_AT + slot * P::SIGNS + (wr * 128 + 32 * q + i32) * 32 + h * 16 +
-          8 * (j + step_group(u)) + 4 * step_u(u));
+    for (int q = 0; q < 4; ++q) {
+      const uint8_t* at = lds + SIGNS_AT + slot * P::SIGNS + (wr * 128 + 32 * q + i32) * 32 +
+                          h * 16 + 8 * (j + step_group(0));
+      if constexpr (NU == 2) {
+        const uint2 w2 = *reinterpret_cast<const uint2*>(at);
+        word[q][0] = w2.x;
+        word[q][1] = w2.y;
+      } else {
+        word[q][0] = *reinterpret_cast<const uint32_t*>(at + 4 * step_u(0));
+      }
+    }
   };
 
 #pragma unroll
@@ -244,14 +251,14 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
     issue_parts(i, i);
   }
   wait_and_barrier<(P::SR - 1) * P::WL + (P::S - 1) * P::IL>();
-  read_words(0, 0, 0);
-  read_exponents(0, 0);
+  read_words(0, 0);
+  read_exponents(0);
 #pragma unroll
   for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int p = 0; p < NP; ++p) read_part(0, 0, t, p);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) sign[q] = expand_signs(word[q], two);
+  for (int q = 0; q < 4; ++q) sign[q] = expand_signs(word[q][0], two);
   set_scales(0);
 
   // The order below is kept by the scheduling barriers: four products, then
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
               acc[q][t] = mfma(sign[q], b[t][p], acc[q][t], scale[t][p]);
               if (refill) {
                 __builtin_amdgcn_sched_barrier(0);
-                sign[q] = expand_signs(word[q], two);
+                sign[q] = expand_signs(word[q][nu], two);
               }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -288,10 +295,10 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
                 wait_and_barrier<P::WAIT>();
                 if (unit_ends) issue_signs(unit + P::SR, sign_slot);
                 issue_parts(unit * P::UNIT + j + P::S, slot);
+                if (unit_ends) read_words(next_sign, 0);
+                else read_words(sign_slot, j + 1);
+                read_exponents(nslot);
               }
-              if (last && unit_ends) read_words(next_sign, 0, nu);
-              else read_words(sign_slot, last ? j + 1 : j, nu);
-              read_exponents(nslot, nu);
             }
             read_part(nslot, nu, t, p);
             if (refill) set_scales(nu);
