@@ -26,24 +26,35 @@ constexpr int kThreads = 1024;
 constexpr int kGroups = 256;             // workgroups, unless that makes kMaxPer runs each
 constexpr int kMaxPer = 1023;            // counts are 16 bits: 64 kMaxPer < 2^16
 
-// Order-preserving bits of a float; 0 for what is never chosen (NaN, -inf).
-// -0 and +0 are equal logits: both take the bits of +0.
-__device__ __forceinline__ uint32_t order_bits(float v) {
-  const uint32_t u = __float_as_uint(v), size = u & 0x7FFFFFFFu;
-  const uint32_t o = size == 0 ? 0x80000000u : u & 0x80000000u ? ~u : u | 0x80000000u;
-  return size > 0x7F800000u || u == 0xFF800000u ? 0u : o;
+// Keys: inverted order-preserving bits, so that the largest logit has the
+// smallest key; kNone, behind every logit's, for what is never chosen (NaN,
+// -inf).  -0 and +0 are equal logits: both take the key of +0.  Selects and
+// bit operations only: written with branches, each of a lane's logits cost
+// its own load, wait and jumps.
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t key_of(uint32_t u) {       // a float's bits
+  u = u == 0x80000000u ? 0u : u;
+  const uint32_t sign = static_cast<uint32_t>(static_cast<int32_t>(u) >> 31);
+  const uint32_t k = ~(u ^ (sign | 0x80000000u));
+  const bool none = static_cast<int>((u & 0x7FFFFFFFu) > 0x7F800000u) | static_cast<int>(u == 0xFF800000u);
+  return none ? kNone : k;
 }
-__device__ __forceinline__ float from_order_bits(uint32_t b) {
-  return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b);
+__device__ __forceinline__ float value_of(uint32_t key) {
+  const uint32_t b = ~key;
+  return __uint_as_float(b ^ (b & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
 }
-// The same for the 16 bits of a float16 or bfloat16.
-__device__ __forceinline__ uint32_t order_bits16(uint32_t u, uint32_t inf) {
-  const uint32_t size = u & 0x7FFFu;
-  const uint32_t o = size == 0 ? 0x8000u : u & 0x8000u ? ~u & 0xFFFFu : u | 0x8000u;
-  return size > inf || u == (inf | 0x8000u) ? 0u : o;
+// The same for the 16 bits of a float16 or bfloat16, with the expert in the
+// lower half: one minimum gives value and lowest expert.
+__device__ __forceinline__ uint32_t key_of16(uint32_t u, uint32_t inf, uint32_t expert) {
+  u = u == 0x8000u ? 0u : u;
+  const uint32_t sign = (u >> 15) * 0xFFFFu;
+  const uint32_t k = (~(u ^ (sign | 0x8000u)) << 16) | expert;
+  const bool none = static_cast<int>((u & 0x7FFFu) > inf) | static_cast<int>(u == (inf | 0x8000u));
+  return none ? kNone : k;
 }
-__device__ __forceinline__ float from_order_bits16(uint32_t b, bool bf16) {
-  const uint16_t u = static_cast<uint16_t>(b & 0x8000u ? b & 0x7FFFu : ~b);
+__device__ __forceinline__ float value_of16(uint32_t key, bool bf16) {
+  const uint32_t b = ~key >> 16;
+  const uint16_t u = static_cast<uint16_t>(b ^ (b & 0x8000u ? 0x8000u : 0xFFFFu));
   return bf16 ? bf16_bits_to_float(u) : f16_bits_to_float(u);
 }
 
@@ -92,8 +103,6 @@ struct RouteArgs {
   int groups, per;                       // workgroups, runs of 64 tokens per workgroup
 };
 
-constexpr uint32_t kNone = 0xFFFFFFFFu;   // a key behind every logit's
-
 // The choices of one token by L lanes of N logits each: lane l gets choices
 // l and l + L (id -1: none).  DT is the logits' type.
 template <int L, int N, int DT>
@@ -109,45 +118,38 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int t, bool live, int
   auto expert = [&](int j) {
     return wide ? (j / kVec * L + lane) * kVec + j % kVec : j * L + lane;
   };
-  if (!live) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) b[j] = kNone;
-  } else if (N >= kVec && wide) {                      // E is a multiple of kVec then
+  const int64_t at = static_cast<int64_t>(t) * a.ld;
+  if (wide) {                                          // E is a multiple of kVec then
+    uint4 q[(N + kVec - 1) / kVec];
 #pragma unroll
     for (int v = 0; v < N / kVec; ++v) {
-      const int e = (v * L + lane) * kVec;
-      uint4 q = make_uint4(0, 0, 0, 0);
-      const bool in = e < E;
-      const int64_t at = static_cast<int64_t>(t) * a.ld + e;
-      if (in)
-        q = kPacked ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.logits) + at)
-                    : *reinterpret_cast<const uint4*>(static_cast<const float*>(a.logits) + at);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      const int64_t from = at + min((v * L + lane) * kVec, E - kVec);
+      q[v] = kPacked ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.logits) + from)
+                     : *reinterpret_cast<const uint4*>(static_cast<const float*>(a.logits) + from);
+    }
 #pragma unroll
-      for (int c = 0; c < kVec; ++c) {
-        if (kPacked) {
-          const uint32_t o = order_bits16(w[c / 2] >> (16 * (c % 2)) & 0xFFFFu, inf);
-          b[v * kVec + c] = in && o ? ~o << 16 | static_cast<uint32_t>(e + c) : kNone;
-        } else {
-          b[(v * kVec + c) % N] = in ? ~order_bits(__uint_as_float(w[c % 4])) : kNone;
-        }
-      }
+    for (int v = 0; v < N / kVec; ++v) {
+      const uint32_t w[4] = {q[v].x, q[v].y, q[v].z, q[v].w};
+#pragma unroll
+      for (int c = 0; c < kVec; ++c)
+        b[(v * kVec + c) % N] = kPacked ? w[c / 2] >> (16 * (c % 2)) & 0xFFFFu : w[c % 4];
     }
   } else {
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int e = j * L + lane;
-      const int64_t at = static_cast<int64_t>(t) * a.ld + min(e, E - 1);
-      if (kPacked) {
-        const uint32_t o = order_bits16(static_cast<const uint16_t*>(a.logits)[at], inf);
-        b[j] = e < E && o ? ~o << 16 | static_cast<uint32_t>(e) : kNone;
-      } else {
-        b[j] = e < E ? ~order_bits(static_cast<const float*>(a.logits)[at]) : kNone;
-      }
+      const int64_t from = at + min(j * L + lane, E - 1);
+      b[j] = kPacked ? static_cast<const uint16_t*>(a.logits)[from]
+                     : static_cast<const uint32_t*>(a.logits)[from];
     }
   }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int e = expert(j);
+    const uint32_t k = kPacked ? key_of16(b[j], inf, static_cast<uint32_t>(e)) : key_of(b[j]);
+    b[j] = static_cast<int>(e < E) & static_cast<int>(live) ? k : kNone;
+  }
   auto value = [&](uint32_t key) {
-    return kPacked ? from_order_bits16(~key >> 16, DT == LQ_BF16) : from_order_bits(~key);
+    return kPacked ? value_of16(key, DT == LQ_BF16) : value_of(key);
   };
   float all = 0.f;                                     // renorm == 0: softmax over every expert
   if (!a.renorm) {
