@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
     for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int p = 0; p < NP; ++p)
-        scale[t][p] = static_cast<int>(ex[t] >> (16 * h + 8 * step_u(u)) & 255u) - 4 * p;
+        scale[t][p] = static_cast<int>(ex[t] >> (16 * h + 8 * step_u(u)) & 255u) - part_shift(p);
   };
   // j: group of the pair that the unit covers; one step's word, or both
   auto read_words = [&](int slot, int j) {

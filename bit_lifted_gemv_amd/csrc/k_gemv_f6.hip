@@ -73,7 +73,7 @@ __device__ __forceinline__ void group_products(const uint8_t* g, int gl, const u
       const i32x8 s = expand_signs(words[t][u], two);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        const int scale = static_cast<int>(ex - 0x04040404u * p);
+        const int scale = static_cast<int>(ex - 0x01010101u * part_shift(p));
         if (u == 0) acc[t] = mfma<0>(s, b[p], acc[t], scale);
         if (u == 1) acc[t] = mfma<1>(s, b[p], acc[t], scale);
         if (u == 2) acc[t] = mfma<2>(s, b[p], acc[t], scale);

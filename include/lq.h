@@ -442,7 +442,7 @@ lq_status lq_gemm(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw,
  * Arithmetic: every value is carried by float6 (E2M3) parts of 4 significant
  * bits with one power of two per 32 positions of a token, three parts for
  * 16-bit outputs (within 2^-14 of the 32 positions' largest value), four for
- * float32 (2^-18); exact products with the signs, float32 sums in a fixed
+ * float32 (2^-19); exact products with the signs, float32 sums in a fixed
  * order (deterministic); epilogue in float32.  A token that holds an
  * infinity or a NaN gives NaN in all of its outputs.
  */
