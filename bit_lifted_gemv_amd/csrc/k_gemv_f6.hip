@@ -18,10 +18,15 @@
 // One slice: the epilogue follows at once, a lane holding four consecutive
 // outputs of a token.  More: each slice's float32 sums, scaled (and the first
 // with the bias), go to the workspace and a second kernel adds them in order
-// and finishes (the join adds them itself).  A workgroup of many rows and few
+// and finishes (k_f6_reduce.hip; the join adds them itself).  A workgroup of many rows and few
 // positions converts little for the signs it streams, one of few rows and
 // many positions needs no second launch: few_f6_plan weighs the two.  Bound
 // by reading the signs once, and by latency for the smallest calls.
+//
+// Measured (MI355X): 1 x 10240 -> 4096 in 6.4 us (activations there after 1 us,
+// split after 2.3, signs done after 4.1, stored after 5.1); 5 x 68096 -> 8192
+// 17 us here (split 4.6 us, then signs at 6.9 TB/s) and 5 in the reduction; 16 x
+// 8192 -> 2 x 14336 gated 11 and 5; one token to 8 experts of 2816 x 4096: 10.2.
 #include "f6_epilogue.h"
 #include "f6_parts.h"
 #include "f6_product.h"
@@ -304,11 +309,13 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
 template <int NP, int T, int DEPTH, bool BF16>
 hipError_t launch(const F6Few& f, int tiles, hipStream_t st) {
   auto* k = gemv_f6_kernel<NP, T, DEPTH, BF16>;
-  static const hipError_t big = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
-  if (big != hipSuccess) return big;
   const dim3 grid((f.row_blocks + f.blocks_per - 1) / f.blocks_per, f.p.slices, tiles);
   const int lds = f.exchange_at + (f.kv > 1 ? kWaves * T * 1024 : 0);
+  if (lds > 64 * 1024) {                   // per call: the attribute belongs to the current device
+    const hipError_t big = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (big != hipSuccess) return big;
+  }
   k<<<grid, 64 * kWaves, lds, st>>>(f);
   return hipGetLastError();
 }
@@ -318,9 +325,10 @@ hipError_t launch(const F6Few& f, int tiles, hipStream_t st) {
 // Every choice from the sizes: tokens per tile, the rows of a workgroup and
 // its slice of the positions, by an estimate of the time.  Measured: a
 // workgroup's conversions 2.5 us and 1.7 us per 512 blocks of 32 positions
-// (0.7 of it arithmetic, the rest every workgroup's loads of them); a compute unit's share of the HBM rate 21 KB per us (16 with
-// T = 1, where reading the operands from LDS is the limit); a second launch 3 us
-// (the join has one anyway) and its sums at about 4 TB/s.
+// (0.7 of it the conversions alone); a compute unit's share of the HBM rate
+// 21 KB per us (16 with T = 1, where reading the operands from LDS is the
+// limit); a second launch 3 us (the join has one anyway) and its sums at
+// about 4 TB/s.
 static F6FewPlan find_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
                            bool grouped, bool join, int64_t cus) {
   F6FewPlan p{};

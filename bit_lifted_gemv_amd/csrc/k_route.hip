@@ -15,7 +15,8 @@
 // it, whatever order the waves set the bits in.  The first launch writes the
 // choices and each workgroup's counts per expert; the second adds the counts
 // before its own (about 256 workgroups) and scatters.  Bound by launch
-// latency and vector instructions; the logits are read once.
+// latency (24 x 64: 5.2 us; 16384 x 256: 9 us and 8 us); the logits are read
+// once.
 #include "lq_internal.h"
 
 namespace lq {
