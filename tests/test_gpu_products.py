@@ -511,3 +511,126 @@ def test_wrapper_refusals(dev):
         lq.gemm_grouped(w[None], s[None], a, torch.zeros(3, dtype=torch.int32, device=dev))
     with pytest.raises(lq.LQError):
         lq.route(torch.zeros(2, 4, device=dev), 5)
+
+
+# Each tile of the many-row kernel, and its slices of the positions: (m, K, B)
+MANY = [
+    (28672, 256, 641),                     # 512 x 64 in two workgroups of four waves (float32: 256 x 64)
+    (8192, 256, 1023),                     # 512 x 64 in eight waves
+    (8190, 512, 500),                      # 256 x 64
+    (262200, 256, 17),                     # 512 x 32
+    (38402, 1024, 60),                     # 256 x 32 in four waves
+    (28672, 1032, 57),                     # 256 x 32 in eight
+    (4096, 8192, 250), (4100, 8200, 40),   # 128 x 32, one slice and four
+    (1000, 65536, 20), (514, 49160, 90),   # sixteen slices and fewer, odd lengths
+]
+
+
+@pytest.mark.parametrize("dtype,out_dtype", [(BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("m,K,B", MANY)
+def test_gemm_ep_many_rows(dev, m, K, B, dtype, out_dtype):
+    print(m, K, B, dtype, out_dtype, flush=True)
+    w, s, bias, a, gen = data(dev, m + K + B, m, K, B, dtype)
+    s = s * (4096 / K) ** 0.5 if K > 4096 else s       # sums of K terms in the range of the others
+    pick = torch.randperm(m // 2, generator=gen)[:min(m // 2, 600)].cuda()
+    both = torch.cat([pick, pick + m // 2])            # outputs checked, as gate and up rows
+    res = torch.randn(B, m, generator=gen).to(out_dtype).cuda()
+    out = lq.gemm_ep(w, s, a, bias=bias, act="silu", residual=res, out_dtype=out_dtype)
+    z, dz = product64(w[both], s[both], a, bias[both], out_dtype)
+    dz = dz * max(1.0, K / 4096)                       # the bound of the sum grows with its length
+    check(out[:, both], *finish64(z, dz, "silu", False), res[:, both])
+    half = res[:, :m // 2].contiguous()
+    out = lq.gemm_ep(w, s, a, bias=bias, act="gelu", gated=True, residual=half, out_dtype=out_dtype)
+    check(out[:, pick], *finish64(z, dz, "gelu", True), half[:, pick])
+    assert torch.equal(lq.gemm_ep(w, s, a, bias=bias, act="gelu", gated=True, residual=half.clone(),
+                                  out_dtype=out_dtype), out)
+
+
+LONG_RUNS = [  # (E, m, K, tokens, R): slices of the positions over ragged runs, and short runs of many experts
+    (2, 500, 32768, 60, 60), (3, 64, 65536, 5, 12), (1, 96, 40960, 30, 30), (128, 2048, 512, 300, 2048),
+    (5, 1000, 16384, 64, 200),
+]
+
+
+@pytest.mark.parametrize("E,m,K,T,R", LONG_RUNS)
+def test_experts_long_positions(dev, E, m, K, T, R):
+    """Rows in and out of the experts where the positions are split; the last three rows are in no run."""
+    print(E, m, K, T, R, flush=True)
+    w, s, bias, a, gen = data(dev, E + m + K, m, K, T, BF16, E=E)
+    s = s * (4096 / K) ** 0.5 if K > 4096 else s
+    off, _ = runs_of(gen, E, R - 3, "random")
+    rows = torch.randint(0, T, (R,), generator=gen).to(torch.int32).cuda()
+    grow = max(1.0, K / 4096)
+    for gated in (False, True):
+        out = torch.full((R, m // 2 if gated else m), 9.0, dtype=BF16, device=dev)
+        lq.gemm_grouped(w, s, a, off, rows=rows, bias=bias, act="silu", gated=gated, out=out)
+        y, dy = grouped64(w, s, bias, a, rows, off, "silu", gated, BF16)
+        check(out[:R - 3], y, dy * grow)
+        assert (out[R - 3:] == 9).all()
+    own = a[rows.long()].contiguous()
+    pos = torch.randperm(R - 3, generator=gen)[:(R - 3) // 2 * 2].reshape(-1, 2).to(torch.int32).cuda()
+    weight = torch.rand(pos.shape, generator=gen).cuda()
+    out = lq.gemm_join(w, s, own, off, pos, weight, bias=bias)
+    z, dz = grouped64(w, s, bias, own, None, off, "none", False, BF16)
+    y = sum(weight[:, j:j + 1].double() * z[pos[:, j].long()] for j in range(2))
+    dy = sum(weight[:, j:j + 1].double() * (grow * dz[pos[:, j].long()] + 2.0**-20 * z[pos[:, j].long()].abs())
+             for j in range(2))
+    check(out, y, dy)
+
+
+@pytest.mark.parametrize("B", [40, 250])
+def test_many_rows_pitches_and_nonfinite(dev, B):
+    """The many-row kernel (B = 40: four slices): rows that lie apart, random bits behind K, outputs
+    that no wide store fits, the residual in place, a token with an infinity, zeros and 2^90."""
+    m, K = 4098, 8136
+    w, s, bias, a, gen = data(dev, 91, m, K, B, F16, extra=8)
+    s = s * 0.7
+    pick = torch.randperm(m // 2, generator=gen)[:200].cuda()
+    wide = torch.full((B, K + 56), float("nan"), dtype=F16, device=dev)
+    wide[:, :K] = a
+    for gated in (False, True):
+        n, at = (m // 2, torch.cat([pick, pick + m // 2])) if gated else (m, pick)
+        buf = torch.full((B, n + 5), 7.0, dtype=F16, device=dev)
+        res = torch.randn(B, n, generator=gen).to(F16).cuda()
+        view = buf[:, 3:3 + n]
+        view.copy_(res)
+        lq.gemm_ep(w, s, wide[:, :K], bias=bias, act="relu", gated=gated, residual=view, out=view)
+        z, dz = product64(w[at], s[at], a, bias[at], F16)
+        check(view[:, pick], *finish64(z, 2 * dz, "relu", gated), res[:, pick])
+        assert (buf[:, :3] == 7).all() and (buf[:, 3 + n:] == 7).all()
+        assert torch.equal(lq.gemm_ep(w, s, a, bias=bias, act="relu", gated=gated, residual=res), view)
+    clean = lq.gemm_ep(w, s, a)
+    a[1, 77] = float("-inf")
+    out = lq.gemm_ep(w, s, a)
+    keep = [i for i in range(B) if i != 1]
+    assert torch.isnan(out[1]).all() and torch.equal(out[keep], clean[keep])
+    assert (lq.gemm_ep(w, s, torch.zeros_like(a)) == 0).all()
+    b = torch.randn(B, K, generator=gen).to(BF16).cuda()
+    ref, big = lq.gemm_ep(w, s, b), lq.gemm_ep(w, s, (b.float() * 2.0**90).to(BF16))
+    assert torch.equal(big.float() * 2.0**-90, ref.float())
+
+
+@pytest.mark.parametrize("m,K,B", [(4096, 8192, 40), (4096, 8192, 250), (8192, 68096, 5)])
+def test_gemm_ep_graphs_and_streams(dev, m, K, B):
+    """Two captured graphs (slices, parts image, or both as the sizes give) replayed at the same time
+    on two streams, three times with new inputs, each equal to the eager call."""
+    w, s, bias, a, gen = data(dev, 95, m, K, B, BF16)
+    xs = [a, a.flip(0).contiguous()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    graphs, outs = [], []
+    for st, x in zip(streams, xs):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            outs.append(lq.gemm_ep(w, s, x, bias=bias, act="silu"))
+        graphs.append(g)
+    for rep in range(3):
+        for x in xs:
+            x.copy_(torch.randn(B, K, generator=gen).to(BF16))
+        torch.cuda.synchronize()
+        for st, g in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for x, o in zip(xs, outs):
+            assert torch.equal(lq.gemm_ep(w, s, x, bias=bias, act="silu"), o), rep
