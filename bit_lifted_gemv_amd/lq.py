@@ -734,6 +734,19 @@ class DeviceLayer:
         al = lift(a, self.t_inv, self.M, self.d, self.D, out_dtype=torch.float32)
         return gemv(self.w, self.s, al, self.K)
 
+    def forward_ep(self, a: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+                   gated: bool = False, residual: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None,
+                   lift_dtype: torch.dtype = torch.float16) -> torch.Tensor:
+        """act(o + bias) + residual (or the gated form) in out_dtype (default
+        a's type) for any number of tokens: the lift into 16 bits, then
+        lq_gemm_ep."""
+        if out_dtype is None:
+            out_dtype = a.dtype
+        al = lift(a, self.t_inv, self.M, self.d, self.D, out_dtype=lift_dtype)
+        return gemm_ep(self.w, self.s, al, bias=bias, act=act, gated=gated, residual=residual,
+                       out_dtype=out_dtype)
+
 
 class DeviceExperts:
     """A mixture-of-experts MLP resident on the GPU: E experts of 1-bit lifted

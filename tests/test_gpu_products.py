@@ -634,3 +634,26 @@ def test_gemm_ep_graphs_and_streams(dev, m, K, B):
         torch.cuda.synchronize()
         for x, o in zip(xs, outs):
             assert torch.equal(lq.gemm_ep(w, s, x, bias=bias, act="silu"), o), rep
+
+
+@pytest.mark.parametrize("B", [1, 20, 200])
+def test_layer_with_epilogue(dev, B):
+    """DeviceLayer.forward_ep against the float64 layer of the oracle: 2e-3 of each token's largest
+    output (the layer bar) for the lifted values' rounding to float16, and the output's own."""
+    import numpy as np
+    from bit_lifted_gemv_amd import synth
+    from oracle import lq_oracle as O
+    L = synth.make_layer(m=768, n=1024, d=8, D=19, B=B, seed=B, dtype="bf16")
+    layer = lq.DeviceLayer.from_synth(L, device=dev)
+    a = lq.to_torch_16(L.a, L.dtype).to(dev)
+    ref = torch.from_numpy(np.ascontiguousarray(O.forward(L.packed, L.K, L.M, L.t_inv, L.s, L.a, L.d, L.D, L.dtype))).to(dev)
+    bias = torch.randn(768, device=dev)
+    res = torch.randn(B, 384, device=dev).to(BF16)
+    z = ref.double() + bias.double()
+    want = act64(z[:, :384], "silu") * z[:, 384:] + res.double()
+    out = layer.forward_ep(a, bias=bias, act="silu", gated=True, residual=res)
+    assert out.dtype == BF16 and out.shape == (B, 384)
+    bar = 2e-3 * (want.abs().amax(1, keepdim=True) + ref.double().abs().amax(1, keepdim=True) * 2)
+    assert ((out.double() - want).abs() <= bar + want.abs() * 2.0**-8).all()
+    plain = layer.forward_ep(a, out_dtype=F32)
+    assert O.rel_err_colmax(plain.cpu().numpy(), ref.cpu().numpy()) <= 2e-3
