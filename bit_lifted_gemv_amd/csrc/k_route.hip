@@ -14,9 +14,10 @@
 // mask of tokens per expert in LDS: counts and stable ranks are popcounts of
 // it, whatever order the waves set the bits in.  The first launch writes the
 // choices and each workgroup's counts per expert; the second adds the counts
-// before its own (about 256 workgroups) and scatters.  Bound by launch
-// latency (24 x 64: 5.2 us; 16384 x 256: 9 us and 8 us); the logits are read
-// once.
+// before its own (about 256 workgroups) and scatters.  It reads every
+// workgroup's counts, so these are 8 bits where a workgroup has few tokens
+// (both launches, 16384 x 256: 17.8 us, 18.4 us with 16 bits throughout).
+// Bound by launch latency (24 x 64: 5.3 us); the logits are read once.
 #include "lq_internal.h"
 
 namespace lq {
@@ -25,7 +26,8 @@ namespace {
 constexpr int kRun = 64;                 // tokens per mask
 constexpr int kThreads = 1024;
 constexpr int kGroups = 256;             // workgroups, unless that makes kMaxPer runs each
-constexpr int kMaxPer = 1023;            // counts are 16 bits: 64 kMaxPer < 2^16
+constexpr int kMaxPer = 1023;            // counts are 16 bits: 64 kMaxPer < 2^16,
+constexpr int kNarrowPer = 3;            // or 8, up to this many runs: 64 kNarrowPer < 2^8
 
 // Keys: inverted order-preserving bits, so that the largest logit has the
 // smallest key; kNone, behind every logit's, for what is never chosen (NaN,
@@ -99,8 +101,9 @@ struct RouteArgs {
   int* pos;
   int* rows;
   int* offsets;
-  uint16_t* counts;                      // [groups][counts_pitch]
+  uint32_t* counts;                      // [groups][counts_pitch] words of 4 or 2 counts
   int counts_pitch;
+  int narrow;                            // counts of 8 bits
   int groups, per;                       // workgroups, runs of 64 tokens per workgroup
 };
 
@@ -270,9 +273,16 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(RouteArgs a) {
     if (tid < E) total[tid] += __popcll(mask[tid]);
   }
   if (!ONE) {
-    if (tid < E)
-      a.counts[static_cast<int64_t>(blockIdx.x) * a.counts_pitch + tid] =
-          static_cast<uint16_t>(total[tid]);
+    __syncthreads();
+    const int per_word = a.narrow ? 4 : 2;
+    if (tid < a.counts_pitch) {
+      uint32_t w = 0;
+      for (int c = 0; c < per_word; ++c) {
+        const int e = tid * per_word + c;
+        if (e < E) w |= static_cast<uint32_t>(total[e]) << (32 / per_word * c);
+      }
+      a.counts[static_cast<int64_t>(blockIdx.x) * a.counts_pitch + tid] = w;
+    }
     return;
   }
   const int n = tid < E ? total[tid] : 0;
@@ -332,36 +342,54 @@ __global__ void __launch_bounds__(kThreads) route_scatter_kernel(RouteArgs a) {
   }
   __syncthreads();
   {
-    // thread (q, e): every lanes-th workgroup's counts of experts 2 e, 2 e + 1;
-    // integer sums, so the order of the additions does not matter
-    const int pairs = (E + 1) / 2, lanes = kThreads / pairs;
-    const int q = tid / pairs, e = tid % pairs;
+    // thread (q, e): word e of every lanes-th workgroup's counts, its fields
+    // added two at a time in 16 or all in 32 bits (a thread adds at most 64
+    // words of 8-bit counts: 64 x 192 < 2^16); integer sums, so the order of the
+    // additions does not matter
+    const int words = a.counts_pitch, lanes = kThreads / words;
+    const int q = tid / words, e = tid % words;
     if (q < lanes) {
-      const auto* counts = reinterpret_cast<const uint32_t*>(a.counts);
-      int sum[2] = {0, 0}, mine[2] = {0, 0};
+      uint32_t sum[4] = {0, 0, 0, 0}, mine[4] = {0, 0, 0, 0};
       for (int g0 = q; g0 < a.groups; g0 += 16 * lanes) {
         uint32_t c[16];                                // sixteen loads on their way at once
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const int g = min(g0 + x * lanes, a.groups - 1);
-          c[x] = counts[static_cast<int64_t>(g) * (a.counts_pitch / 2) + e];
+          c[x] = a.counts[static_cast<int64_t>(g) * words + e];
         }
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const int g = g0 + x * lanes;
           if (g >= a.groups) c[x] = 0;
-          sum[0] += c[x] & 0xFFFFu;
-          sum[1] += c[x] >> 16;
-          if (g >= static_cast<int>(blockIdx.x)) c[x] = 0;
-          mine[0] += c[x] & 0xFFFFu;
-          mine[1] += c[x] >> 16;
+          const uint32_t before = g < static_cast<int>(blockIdx.x) ? c[x] : 0u;
+          if (a.narrow) {
+            sum[0] += c[x] & 0x00FF00FFu;
+            sum[1] += c[x] >> 8 & 0x00FF00FFu;
+            mine[0] += before & 0x00FF00FFu;
+            mine[1] += before >> 8 & 0x00FF00FFu;
+          } else {
+            sum[0] += c[x] & 0xFFFFu;
+            sum[1] += c[x] >> 16;
+            mine[0] += before & 0xFFFFu;
+            mine[1] += before >> 16;
+          }
         }
       }
+      if (a.narrow) {                                  // fields 0, 2 and 1, 3 apart
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (2 * e + c < E) {
-          atomicAdd(&base[2 * e + c], mine[c]);
-          atomicAdd(&all[2 * e + c], sum[c]);
+        for (int c = 1; c >= 0; --c) {
+          sum[c + 2] = sum[c] >> 16;
+          sum[c] &= 0xFFFFu;
+          mine[c + 2] = mine[c] >> 16;
+          mine[c] &= 0xFFFFu;
+        }
+      }
+      const int fields = a.narrow ? 4 : 2;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < fields && fields * e + c < E) {
+          atomicAdd(&base[fields * e + c], static_cast<int>(mine[c]));
+          atomicAdd(&all[fields * e + c], static_cast<int>(sum[c]));
         }
     }
   }
@@ -418,7 +446,8 @@ int per_of(int64_t T) {
   return static_cast<int>(per < kMaxPer ? per : kMaxPer);
 }
 int groups_of(int64_t T) { return static_cast<int>((runs_of(T) + per_of(T) - 1) / per_of(T)); }
-int pitch_of(int E) { return (E + 1) / 2 * 2; }
+bool narrow_of(int64_t T) { return per_of(T) <= kNarrowPer; }
+int pitch_of(int64_t T, int E) { return narrow_of(T) ? (E + 3) / 4 : (E + 1) / 2; }
 
 template <int L, int N, int DT>
 hipError_t launch(RouteArgs a, hipStream_t st) {
@@ -447,7 +476,7 @@ hipError_t by_experts(const RouteArgs& a, hipStream_t st) {
 
 size_t route_workspace_bytes(int64_t T, int E) {
   if (runs_of(T) <= 1) return 0;
-  return static_cast<size_t>(groups_of(T)) * pitch_of(E) * 2;
+  return static_cast<size_t>(groups_of(T)) * pitch_of(T, E) * 4;
 }
 
 hipError_t launch_route(const void* logits, lq_dtype dt, int64_t T, int E, int64_t ld,
@@ -469,8 +498,9 @@ hipError_t launch_route(const void* logits, lq_dtype dt, int64_t T, int E, int64
   a.pos = pos;
   a.rows = rows;
   a.offsets = offsets;
-  a.counts = static_cast<uint16_t*>(ws);
-  a.counts_pitch = pitch_of(E);
+  a.counts = static_cast<uint32_t*>(ws);
+  a.counts_pitch = pitch_of(T, E);
+  a.narrow = narrow_of(T);
   if (dt == LQ_F32) return by_experts<LQ_F32>(a, st);
   return dt == LQ_F16 ? by_experts<LQ_F16>(a, st) : by_experts<LQ_BF16>(a, st);
 }

@@ -474,7 +474,8 @@ lq_status lq_gemm_ep(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw
  * workspace: >= lq_route_workspace_size bytes (0 up to 64 tokens, then it may
  *     be NULL), 256-byte aligned, caller-owned, no initialisation needed.
  * Requires 1 <= E <= 1024, 1 <= k <= min(E, 32), T >= 0, T*k < 2^31.  T == 0
- * writes zero offsets.  Float32 arithmetic; deterministic.
+ * writes zero offsets.  Float32 arithmetic; deterministic.  Weights are within
+ * 2^-20 + |l_j - l_max| 2^-24 of their value (the difference is rounded).
  */
 lq_status lq_route_workspace_size(int64_t T, int64_t E, int32_t k, size_t* bytes);
 lq_status lq_route(const void* logits, lq_dtype dtype, int64_t T, int64_t E, int64_t ld,

@@ -125,3 +125,38 @@ def test_route_repeats_and_graph():
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(r, lq.route(logits, 8))), i
+
+
+@pytest.mark.parametrize("T,E,k,crowd", [
+    (16385, 1021, 4, False),      # two runs a workgroup, words of counts not full
+    (49152, 5, 2, True),          # three: every token on one expert, 192 a count
+    (49152, 256, 8, False),
+    (49153, 7, 3, True),          # four: counts of 16 bits, 256 of them
+    (70001, 1024, 1, False),
+])
+def test_route_runs_per_workgroup(T, E, k, crowd):
+    """The oracle of many tokens is a stable sort instead of a loop."""
+    gen = torch.Generator().manual_seed(T + E)
+    logits = torch.randn(T, E, generator=gen).to(torch.bfloat16)
+    if crowd:
+        logits[:, 2] = 50.0
+    r = lq.route(logits.cuda(), k)
+    x = logits.double().numpy()
+    ids = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    flat = ids.reshape(-1)
+    order = np.argsort(flat, kind="stable")
+    pos = np.empty(T * k, np.int64)
+    pos[order] = np.arange(T * k)
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    assert np.array_equal(r.rows.cpu().numpy(), order // k)
+    assert np.array_equal(r.pos.cpu().numpy().reshape(-1), pos)
+    counts = np.bincount(flat, minlength=E)
+    assert np.array_equal(r.offsets.cpu().numpy(), np.concatenate([[0], np.cumsum(counts)]))
+    top = np.take_along_axis(x, ids, 1)
+    share = np.exp(top - top[:, :1])
+    share /= share.sum(1, keepdims=True)
+    # d = l - max is rounded to float32, off by up to |d| 2^-24 (a relative half
+    # step); exp(d + x) = exp(d) (1 + x + ...) makes that a relative error of
+    # |d| 2^-24, beside 2^-20 for exp, the sum and the quotient
+    near = 2.0**-20 + np.abs(top - top[:, :1]) * 2.0**-24
+    assert (np.abs(r.weight.cpu().double().numpy() - share) <= near * share + 1e-38).all()
