@@ -4,20 +4,23 @@
 // independent accumulators, 16-bit operands 2.4).
 //
 // Parts.  Per block of 32 positions of one token, with f the biased exponent
-// of its largest |x| and e = max(f - 2, 14), y = x 2^(127 - e) lies below 8
+// of its largest |x| and e = max(f - 2, 20), y = x 2^(127 - e) lies below 8
 // in magnitude; p0 = fp6(y), p1 = fp6(16 (y - p0)), p2 = fp6(16 (16 (y - p0)
 // - p1)) (E2M3: 4 significant bits up to 7.5, step 1/8 below 2; every
 // remainder is exact in float32), and part p carries the power of two
 // e - part_shift(p) as its hardware scale, which is what the one exponent
 // byte per block holds.  The remainders are at most 1/4, 1/8 and 1/16 of a
 // unit of their part's scale (16-bit values above 7.75 come out exactly), so
-// the fourth part of float32 results, the last, is taken 64 times finer and
-// not 16.  NP = 3 parts keep a value to 2^-14 of its block's largest one (and
-// exactly, when it is a bfloat16 above 2^-6 or a float16 above 2^-3 of it):
-// the rounding of a sum of K of them stays 20 times below that of a 16-bit
-// result (measured 1e-5 of the result for Gaussian bfloat16, 3e-5 for
-// float16, 8e-5 with one value in a hundred 20 times the others).  Float32
-// results take NP = 4 (2^-19; measured 2e-7 and 4e-7).  The products with
+// the fourth part of float32 results is taken 64 times finer and not 16, and
+// the fifth, behind a remainder of 1/8, 32 times.  NP = 3 parts keep a value
+// to 2^-14 of its block's largest one (and exactly, when it is a bfloat16
+// above 2^-6 or a float16 above 2^-3 of it): the rounding of a sum of K of
+// them stays 20 times below that of a 16-bit result (measured 1e-5 of the
+// result for Gaussian bfloat16, 3e-5 for float16, 8e-5 with one value in a
+// hundred 20 times the others).  Float32 results take NP = 5 (2^-24, below
+// the sums' own rounding; four parts, 2^-19, lost 1.3e-6 of a float16 result
+// with such values).  e is at least 20: the last scale, e - 19, stays above 0
+// and subtracting it from four packed bytes borrows nothing.  The products with
 // +-1 are exact and are summed in float32.  A block with an infinity or a NaN
 // has e = 255, which the matrix cores read as NaN: its token's results are
 // all NaN.
@@ -53,7 +56,7 @@ typedef float f32x32 __attribute__((ext_vector_type(32)));
 
 constexpr int kPadPositions = 512;      // images cover whole multiples of this, zero past K
 
-constexpr int part_shift(int p) { return p < 3 ? 4 * p : 14; }
+constexpr int part_shift(int p) { return p < 3 ? 4 * p : 5 * p - 1; }
 
 constexpr int group_steps(int H) { return H == 2 ? 2 : 4; }
 constexpr int group_positions(int H) { return 32 * H * group_steps(H); }
@@ -92,7 +95,7 @@ __device__ __forceinline__ i32x8 expand_signs(uint32_t w, uint32_t two) {
 // Scale byte of a block from the bits of its largest |x|.
 __device__ __forceinline__ uint32_t block_exponent(uint32_t largest) {
   const int f = static_cast<int>(largest >> 23);
-  return f == 255 ? 255u : static_cast<uint32_t>(max(f - 2, 14));
+  return f == 255 ? 255u : static_cast<uint32_t>(max(f - 2, 20));
 }
 
 // Eight 16-bit values of a 16-byte load.

@@ -99,7 +99,7 @@ hipError_t launch_f6_image(const void* a, lq_dtype dt, int64_t rows, bool zero_r
     return hipGetLastError();
   };
   if (NP == 3) return dt == LQ_BF16 ? run(f6_image_kernel<true, 3>) : run(f6_image_kernel<false, 3>);
-  return dt == LQ_BF16 ? run(f6_image_kernel<true, 4>) : run(f6_image_kernel<false, 4>);
+  return dt == LQ_BF16 ? run(f6_image_kernel<true, 5>) : run(f6_image_kernel<false, 5>);
 }
 
 }  // namespace lq

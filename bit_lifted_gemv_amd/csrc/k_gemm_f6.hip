@@ -476,7 +476,7 @@ F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
 }
 
 hipError_t launch_gemm_f6(const F6Product& p, int shape, int NP, hipStream_t st) {
-  return NP == 3 ? by_shape<3>(p, shape, st) : by_shape<4>(p, shape, st);
+  return NP == 3 ? by_shape<3>(p, shape, st) : by_shape<5>(p, shape, st);
 }
 
 }  // namespace lq

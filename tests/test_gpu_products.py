@@ -657,3 +657,19 @@ def test_layer_with_epilogue(dev, B):
     assert ((out.double() - want).abs() <= bar + want.abs() * 2.0**-8).all()
     plain = layer.forward_ep(a, out_dtype=F32)
     assert O.rel_err_colmax(plain.cpu().numpy(), ref.cpu().numpy()) <= 2e-3
+
+
+@pytest.mark.parametrize("m,B", [(64, 1), (300, 5), (256, 16), (200, 40), (1024, 200), (8192, 300)])
+def test_float32_result_keeps_small_values_beside_a_large_one(dev, m, B):
+    """float16 values of 11 bits in the block of one 2048 times theirs: all are
+    multiples of 2^-11 and every partial sum lies below 2048 + 1024 < 2^12, so
+    float32 sums are exact and the result is the exact one."""
+    K = 1024
+    gen = torch.Generator().manual_seed(m + B)
+    w = torch.randint(-2**31, 2**31, (m, K // 32), generator=gen).to(torch.int32)
+    steps = torch.randint(1024, 2048, (B, K), generator=gen) * (2 * torch.randint(0, 2, (B, K), generator=gen) - 1)
+    a = steps.double() * 2.0**-11
+    a[torch.arange(B), torch.randint(0, K, (B,), generator=gen)] = 2048.0
+    z = a @ signs(w, K).T
+    out = lq.gemm_ep(w.to(dev), torch.ones(m, device=dev), a.to(F16).to(dev), out_dtype=F32)
+    assert torch.equal(out.cpu().double(), z)
