@@ -11,15 +11,20 @@
 // e - part_shift(p) as its hardware scale, which is what the one exponent
 // byte per block holds.  The remainders are at most 1/4, 1/8 and 1/16 of a
 // unit of their part's scale (16-bit values above 7.75 come out exactly), so
-// the fourth part of float32 results is taken 64 times finer and not 16, and
-// the fifth, behind a remainder of 1/8, 32 times.  NP = 3 parts keep a value
-// to 2^-14 of its block's largest one (and exactly, when it is a bfloat16
-// above 2^-6 or a float16 above 2^-3 of it): the rounding of a sum of K of
-// them stays 20 times below that of a 16-bit result (measured 1e-5 of the
-// result for Gaussian bfloat16, 3e-5 for float16, 8e-5 with one value in a
-// hundred 20 times the others).  Float32 results take NP = 5 (2^-24, below
-// the sums' own rounding; four parts, 2^-19, lost 1.3e-6 of a float16 result
-// with such values).  e is at least 20: the last scale, e - 19, stays above 0
+// the fourth part is taken 64 times finer and not 16, and the fifth, behind a
+// remainder of 1/8, 32 times.  The parts NP follow from the result's type, so
+// that what they lose stays below its own rounding (shares of the result,
+// root mean squares of sums of 8192, Gaussian values / with one position in a
+// hundred 20 times the others, emulated and as the kernels measure):
+//   bfloat16 results, 1.7e-3: three parts, 2^-14 of the block's largest value
+//     (exact for a bfloat16 above 2^-6 or a float16 above 2^-3 of it); lost
+//     1.1e-5 / 7.8e-5 of bfloat16 values, 3.2e-5 / 1.3e-4 of float16 ones, half
+//     as much again through a gate;
+//   float16 results, 2.1e-4: four parts, 2^-19; lost below 1e-6 (three would
+//     make the error of gated float16 results with such values 2.8e-4);
+//   float32 results: five parts, 2^-24, below the sums' own rounding (four lost
+//     1.3e-6 of a float16 result with such values).
+// The exponent e is at least 20: the last scale, e - 19, stays above 0
 // and subtracting it from four packed bytes borrows nothing.  The products with
 // +-1 are exact and are summed in float32.  A block with an infinity or a NaN
 // has e = 255, which the matrix cores read as NaN: its token's results are

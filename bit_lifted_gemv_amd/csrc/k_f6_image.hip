@@ -3,7 +3,7 @@
 // A wave takes 64 blocks of 32 positions, whose parts are consecutive in the
 // image: it loads them with whole lines, turns each lane's block into parts
 // (LDS between, both ways) and stores whole lines again.  Bound by the bytes
-// read and written (2 and 2.4 per position): 4096 x 8192 in 26 us, 3000 x
+// read and written (2 and, of three parts, 2.4 per position): 4096 x 8192 in 26 us, 3000 x
 // 28672 in 56 (6.6 TB/s), and about 8 us at least.  `zero_row`: one more row of
 // zeros follows the last (what a gathered row with an index out of range
 // reads).
@@ -99,6 +99,7 @@ hipError_t launch_f6_image(const void* a, lq_dtype dt, int64_t rows, bool zero_r
     return hipGetLastError();
   };
   if (NP == 3) return dt == LQ_BF16 ? run(f6_image_kernel<true, 3>) : run(f6_image_kernel<false, 3>);
+  if (NP == 4) return dt == LQ_BF16 ? run(f6_image_kernel<true, 4>) : run(f6_image_kernel<false, 4>);
   return dt == LQ_BF16 ? run(f6_image_kernel<true, 5>) : run(f6_image_kernel<false, 5>);
 }
 

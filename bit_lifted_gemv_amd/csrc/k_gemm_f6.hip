@@ -4,7 +4,7 @@
 // lq_gemm_grouped.
 //
 // Tile.  A workgroup of WR WK waves takes 128 WR rows of the weights and 32 TT
-// tokens; the weights cost 1/8 byte per position and the parts 2.4, so the
+// tokens; the weights cost 1/8 byte per position and the parts 2.4 to 3.9, so the
 // tile is tall.  WK waves share each 128-row strip and split the positions of
 // a stage; every wave holds 128 rows x 32 TT tokens of sums (4 TT tiles of
 // 32 x 32) and uses each operand it reads from LDS four times.  Operands come
@@ -417,7 +417,8 @@ hipError_t by_shape(const F6Product& p, int shape, hipStream_t st) {
   switch (shape) {
     case 4120: if constexpr (NP == 3) return launch<NP, 4, 1, 2, false>(p, st); break;
     case 2421: return launch<NP, 2, 4, 2, true>(p, st);
-    case 4221: if constexpr (NP == 3) return launch<NP, 4, 2, 2, true>(p, st); break;
+    case 2220: if constexpr (NP == 4) return launch<NP, 2, 2, 2, false>(p, st); break;
+    case 4221: if constexpr (NP <= 4) return launch<NP, 4, 2, 2, true>(p, st); break;
     case 4110: return launch<NP, 4, 1, 1, false>(p, st);
     case 2210: return launch<NP, 2, 2, 1, false>(p, st);
     case 2411: return launch<NP, 2, 4, 1, true>(p, st);
@@ -442,6 +443,7 @@ F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
     const int64_t tiles = grouped ? R / tok + (runs + 1) / 2 : (R + tok - 1) / tok;
     return tiles * ((out_m + outs - 1) / outs);
   };
+  auto up = [&](int64_t n) { return (n + cus - 1) / cus * cus; };
   // The tallest tile that fills the compute units, measured on each side:
   // 512 x 64 in two workgroups of four waves per unit (4096 x 8192 -> 28672:
   // 1175 us; 256 x 64 in eight waves 1400), or in one of eight where there is
@@ -451,10 +453,17 @@ F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
   // Where 128 x 32 tiles leave units empty, the positions are split into
   // slices (64 x 10240 -> 4096: 4 slices 20, one 31), down to 512 positions
   // each, or 8192 to put two workgroups on a unit (24 x 68096 -> 8192: 8
-  // slices 46, 4 slices 51).
+  // slices 46, 4 slices 51).  Of four parts a 64-token stage leaves no room for
+  // two workgroups of 512 rows: 512 x 64 in one of eight waves (4096 x 8192 ->
+  // 28672: 1615; 256 x 64 in two of four 1637), or the latter where the last
+  // round of the former would be filled below 9/10 (4096 x 4096 -> 2816: 118
+  // against 135; 1024 x 8192 -> 28672: 430 against 448).  Of runs the last
+  // round is not known here: always the former (3000 rows of 8 experts, 28672
+  // -> 4096: 767 against 839).
   p.slices = 1;
   if (NP == 3 && two && count(4, 2) > cus) p.shape = 4120;
-  else if (NP == 3 && two && count(4, 2) * 5 >= cus * 4) p.shape = 4221;
+  else if (NP == 4 && !grouped && count(4, 2) > cus && count(4, 2) * 10 < up(count(4, 2)) * 9) p.shape = 2220;
+  else if (NP <= 4 && two && count(4, 2) * 5 >= cus * 4) p.shape = 4221;
   else if (two && count(2, 2) * 5 >= cus * 4) p.shape = 2421;
   else if (count(4, 1) >= 2 * cus) p.shape = 4110;
   else if (count(2, 1) > cus) p.shape = 2210;
@@ -476,7 +485,7 @@ F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
 }
 
 hipError_t launch_gemm_f6(const F6Product& p, int shape, int NP, hipStream_t st) {
-  return NP == 3 ? by_shape<3>(p, shape, st) : by_shape<5>(p, shape, st);
+  return NP == 3 ? by_shape<3>(p, shape, st) : NP == 4 ? by_shape<4>(p, shape, st) : by_shape<5>(p, shape, st);
 }
 
 }  // namespace lq

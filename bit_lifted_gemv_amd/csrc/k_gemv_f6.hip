@@ -412,6 +412,9 @@ hipError_t launch_gemv_f6(const F6Few& f, const F6FewPlan& plan, int NP, hipStre
   LQ_FEW(3, 1, 6);
   LQ_FEW(3, 2, 4);
   LQ_FEW(3, 4, 2);
+  LQ_FEW(4, 1, 6);
+  LQ_FEW(4, 2, 4);
+  LQ_FEW(4, 4, 2);
   LQ_FEW(5, 1, 6);
   LQ_FEW(5, 2, 4);
   LQ_FEW(5, 4, 2);

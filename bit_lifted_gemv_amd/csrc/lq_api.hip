@@ -136,7 +136,9 @@ lq_status f6_types(lq_dtype lift_dtype, lq_act act, int32_t gated, int64_t m, lq
   return LQ_OK;
 }
 
-int f6_parts_count(lq_dtype out_dtype) { return out_dtype == LQ_F32 ? 5 : 3; }
+int f6_parts_count(lq_dtype out_dtype) {
+  return out_dtype == LQ_F32 ? 5 : out_dtype == LQ_F16 ? 4 : 3;
+}
 
 // rows: of the activations.  One image of them is addressed with 32-bit offsets.
 lq_status f6_sizes(int64_t E, int64_t m, int64_t K, int64_t rows, lq_dtype out_dtype) {

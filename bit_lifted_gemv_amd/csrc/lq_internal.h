@@ -215,7 +215,7 @@ struct F6Few {
 };
 hipError_t launch_gemv_f6(const F6Few& f, const F6FewPlan& plan, int NP, hipStream_t st);
 
-// 16-bit activations -> parts image (k_f6_image.hip); NP = 3 or 5.
+// 16-bit activations -> parts image (k_f6_image.hip); NP = 3, 4 or 5.
 hipError_t launch_f6_image(const void* a, lq_dtype dt, int64_t rows, bool zero_row, int64_t K,
                            int64_t lda, int NP, void* img, hipStream_t st);
 // Tile shape (its four template digits) and slices of the product for many rows.

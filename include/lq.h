@@ -437,12 +437,13 @@ lq_status lq_gemm(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw,
  *           LQ_BF16, rounded once to nearest even), ldo apart.
  * workspace: >= lq_gemm_ep_workspace_size bytes, 256-byte aligned,
  *           caller-owned, no initialisation needed.
- * Requires B >= 1; B rows of operand image (2.4 bytes per position, 3.9 for
- * float32 outputs) below 4 GiB: split more tokens over several calls.
+ * Requires B >= 1; B rows of operand image (2.4 bytes per position, 3.1 for
+ * float16 outputs, 3.9 for float32 ones) below 4 GiB: split more tokens over several calls.
  * Arithmetic: every value is carried by float6 (E2M3) parts of 4 significant
  * bits with one power of two per 32 positions of a token, three parts for
- * 16-bit outputs (within 2^-14 of the 32 positions' largest value), five for
- * float32 (2^-24); exact products with the signs, float32 sums in a fixed
+ * bfloat16 outputs (within 2^-14 of the 32 positions' largest value), four for
+ * float16 ones (2^-19), five for float32 (2^-24): less than the outputs' own
+ * rounding; exact products with the signs, float32 sums in a fixed
  * order (deterministic); epilogue in float32.  A token that holds an
  * infinity or a NaN gives NaN in all of its outputs.
  */
