@@ -159,6 +159,36 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _on_stream(call):
+    """A wrapper around the calls whose last parameter is `stream`.  A stream
+    other than the current one becomes the current one for the call, so that
+    its workspace and the tensors it makes are that stream's memory, in order
+    with its kernels: a block that the caller's stream has given back may still
+    be in use there.  What is passed in is kept until `stream` is through with
+    it, and what is returned until the caller's stream is; that the one stream
+    waits for the other's results is the caller's business."""
+    last = call.__code__.co_argcount - 1
+
+    @functools.wraps(call)
+    def run(*args, **kwargs):
+        stream = args[last] if len(args) > last else kwargs.get("stream")
+        if stream is None:
+            return call(*args, **kwargs)
+        caller = torch.cuda.current_stream(stream.device)
+        if caller == stream:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            result = call(*args, **kwargs)
+        given = [t for t in (*args, *kwargs.values()) if hasattr(t, "record_stream")]
+        for t in given:
+            t.record_stream(stream)
+        for t in result if isinstance(result, tuple) else (result,):
+            if not any(t is g for g in given):
+                t.record_stream(caller)
+        return result
+    return run
+
+
 # ----------------------------------------------------------------- C ABI wrappers
 def pack_signs(signs: torch.Tensor, ldw: Optional[int] = None, stream=None) -> torch.Tensor:
     """int8 signs [rows][K] -> int32 words [rows][ldw] (LSB-first, bit 1 = positive)."""
@@ -452,6 +482,8 @@ def _handle(device: torch.device, stream) -> int:
     """The HIP stream of a call: `stream`, or the device's current one (its raw
     handle: torch.cuda.current_stream builds a Stream object, 2 us)."""
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device.index)
 
@@ -463,16 +495,12 @@ def _bytes_needed(call: str, *sizes: int) -> int:
     return n.value
 
 
-def _temporary(nbytes: int, device: torch.device, stream) -> Optional[torch.Tensor]:
-    """A workspace from torch's allocator on the call's stream, a new one for
-    every call, so that calls on two streams or captured graphs never share
-    one; returned memory is reused in stream order."""
-    if not nbytes:
-        return None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+def _temporary(nbytes: int, device: torch.device) -> Optional[torch.Tensor]:
+    """A workspace from torch's allocator on the current stream, which is the
+    call's (_on_stream), a new one for every call, so that calls on two streams
+    or captured graphs never share one; returned memory is reused in stream
+    order."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def _same_device(device: torch.device, **tensors: Optional[torch.Tensor]) -> None:
@@ -537,6 +565,7 @@ def _act(act: str) -> int:
     return ACTS[act]
 
 
+@_on_stream
 def gemm_ep(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
             bias: Optional[torch.Tensor] = None, act: str = "none", gated: bool = False,
             residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
@@ -562,13 +591,14 @@ def gemm_ep(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
     odt = _dt(out)
     ldr = 0 if residual is None else _pitch("residual", residual, (B, width), out.dtype)
     nb = _bytes_needed("lq_gemm_ep_workspace_size", m, K, B, odt)
-    ws = _temporary(nb, dev, stream)
+    ws = _temporary(nb, dev)
     check(lib().lq_gemm_ep(_ptr(w_packed), m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift), lda, B,
                            _ptr(bias), code, int(gated), _ptr(residual), ldr, _ptr(out), odt, ldo,
                            _ptr(ws), nb, _handle(dev, stream)))
     return out
 
 
+@_on_stream
 def gemm_grouped(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
                  offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
                  bias: Optional[torch.Tensor] = None, act: str = "none", gated: bool = False,
@@ -595,7 +625,7 @@ def gemm_grouped(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
     out, ldo = _target(out, R, m // 2 if gated else m, out_dtype, a_lift)
     odt = _dt(out)
     nb = _bytes_needed("lq_gemm_grouped_workspace_size", E, m, K, n_rows, R, odt)
-    ws = _temporary(nb, dev, stream)
+    ws = _temporary(nb, dev)
     check(lib().lq_gemm_grouped(_ptr(w_packed), E, m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift),
                                 lda, n_rows, _ptr(rows), _ptr(offsets), R, _ptr(bias), code,
                                 int(gated), _ptr(out), odt, ldo, _ptr(ws), nb,
@@ -603,6 +633,7 @@ def gemm_grouped(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
     return out
 
 
+@_on_stream
 def gemm_join(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
               offsets: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor,
               bias: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
@@ -630,7 +661,7 @@ def gemm_join(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
     odt = _dt(out)
     ldr = 0 if residual is None else _pitch("residual", residual, (T, m), out.dtype)
     nb = _bytes_needed("lq_gemm_join_workspace_size", E, m, K, R, T, k, odt)
-    ws = _temporary(nb, dev, stream)
+    ws = _temporary(nb, dev)
     check(lib().lq_gemm_join(_ptr(w_packed), E, m, K, ldw, _ptr(s), _ptr(a_lift), _dt(a_lift),
                              lda, _ptr(offsets), R, _ptr(bias), _ptr(pos), _ptr(weight), T, k,
                              _ptr(residual), ldr, _ptr(out), odt, ldo, _ptr(ws), nb,
@@ -650,6 +681,7 @@ class Routing(NamedTuple):
     offsets: torch.Tensor
 
 
+@_on_stream
 def route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None, renorm: bool = True,
           stream=None) -> Routing:
     """Each token's k experts, their weights and the pairs sorted by expert
@@ -669,7 +701,7 @@ def route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None, re
     ld = _pitch("logits", logits, (T, E))
     code = _dt(logits)
     nb = _bytes_needed("lq_route_workspace_size", T, E, k)
-    ws = _temporary(nb, dev, stream)
+    ws = _temporary(nb, dev)
     ids, pos, rows = torch.empty((3, T, k), dtype=torch.int32, device=dev).unbind()
     rows = rows.view(-1)
     weight = torch.empty((T, k), dtype=torch.float32, device=dev)

@@ -1,0 +1,67 @@
+"""Calls on a given stream beside calls on the current one, with nothing
+between them: each allocates its own workspace and results, and both have to
+be right."""
+import pytest
+import torch
+
+from bit_lifted_gemv_amd import lq
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def words(gen, *shape):
+    *lead, K = shape
+    return torch.randint(-2**31, 2**31, (*lead, (K // 32 + 3) // 4 * 4), generator=gen).to(torch.int32).cuda()
+
+
+def case(name, gen):
+    """Two inputs of one size, and the call."""
+    if name == "route":
+        return [torch.randn(16384, 256, generator=gen).cuda() for _ in range(2)], lambda x, **k: lq.route(x, 8, **k)
+    if name in ("prompt", "tokens"):
+        m, K, B = (4096, 8192, 600) if name == "prompt" else (8192, 20480, 5)      # an image; slices
+        w, s = words(gen, m, K), torch.rand(m, generator=gen).cuda()
+        return ([torch.randn(B, K, generator=gen).to(BF16).cuda() for _ in range(2)],
+                lambda x, **k: lq.gemm_ep(w, s, x, **k))
+    E, m, K, T, k = 8, 2048, 2048, 300, 2
+    w, s = words(gen, E, m, K), torch.rand(E, m, generator=gen).cuda()
+    r = lq.route(torch.randn(T, E, generator=gen).cuda(), k)
+    if name == "grouped":
+        return ([torch.randn(T, K, generator=gen).to(BF16).cuda() for _ in range(2)],
+                lambda x, **o: lq.gemm_grouped(w, s, x, r.offsets, rows=r.rows, act="silu", gated=True, **o))
+    return ([torch.randn(T * k, K, generator=gen).to(BF16).cuda() for _ in range(2)],
+            lambda x, **o: lq.gemm_join(w, s, x, r.offsets, r.pos, r.weight, **o))
+
+
+@pytest.mark.parametrize("name", ["prompt", "tokens", "grouped", "join", "route"])
+def test_a_call_on_a_stream_beside_one_on_the_current_stream(name):
+    (x, y), call = case(name, torch.Generator().manual_seed(3))
+    flat = lambda r: r if isinstance(r, tuple) else (r,)  # noqa: E731
+    want_x, want_y = flat(call(x)), flat(call(y))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(6):
+        got = [(want_x, flat(call(x))), (want_y, flat(call(y, stream=side))), (want_x, flat(call(x))),
+               (want_y, flat(call(y, stream=side)))]
+        torch.cuda.synchronize()
+        for want, have in got:
+            assert all(torch.equal(p, q) for p, q in zip(want, have))
+
+
+def test_results_of_another_stream_can_be_dropped_early():
+    """The caller's stream waits for the other one, reads the result and lets go of it, and the
+    other stream goes on: what was read is the first result."""
+    (x, y), call = case("prompt", torch.Generator().manual_seed(4))
+    want = call(x).float()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        out = call(x, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        read = sum(out.float() for _ in range(8)) / 8
+        del out
+        call(y, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(read, want)
