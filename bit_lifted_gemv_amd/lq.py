@@ -182,14 +182,18 @@ def _on_stream(call):
         given = [t for t in (*args, *kwargs.values()) if hasattr(t, "record_stream")]
         for t in given:
             t.record_stream(stream)
-        for t in result if isinstance(result, tuple) else (result,):
-            if not any(t is g for g in given):
+        made = []
+        for r in result if isinstance(result, tuple) else (result,):
+            made += r if isinstance(r, list) else [r]
+        for t in made:
+            if t is not None and not any(t is g for g in given):
                 t.record_stream(caller)
         return result
     return run
 
 
 # ----------------------------------------------------------------- C ABI wrappers
+@_on_stream
 def pack_signs(signs: torch.Tensor, ldw: Optional[int] = None, stream=None) -> torch.Tensor:
     """int8 signs [rows][K] -> int32 words [rows][ldw] (LSB-first, bit 1 = positive)."""
     _dev(signs)
@@ -200,6 +204,7 @@ def pack_signs(signs: torch.Tensor, ldw: Optional[int] = None, stream=None) -> t
     return out
 
 
+@_on_stream
 def unpack_signs(packed: torch.Tensor, K: int, stream=None) -> torch.Tensor:
     _dev(packed)
     rows, ldw = packed.shape
@@ -208,6 +213,7 @@ def unpack_signs(packed: torch.Tensor, K: int, stream=None) -> torch.Tensor:
     return out
 
 
+@_on_stream
 def lift(a: torch.Tensor, t_inv: torch.Tensor, M: torch.Tensor, d: int, D: int,
          out_dtype: torch.dtype = torch.float32, t_block: int = 128,
          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -228,6 +234,7 @@ def lift_parts_size(K: int) -> int:
     return n.value
 
 
+@_on_stream
 def lift_parts(a: torch.Tensor, t_inv: torch.Tensor, M: torch.Tensor, d: int, D: int,
                t_block: int = 128, out: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
@@ -244,6 +251,7 @@ def lift_parts(a: torch.Tensor, t_inv: torch.Tensor, M: torch.Tensor, d: int, D:
     return out
 
 
+@_on_stream
 def lift_kron(a: torch.Tensor, s1: torch.Tensor, p1_inv: torch.Tensor, p2_inv: torch.Tensor,
               s2: torch.Tensor, M: torch.Tensor, d: int, D: int,
               out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
@@ -265,6 +273,7 @@ def lift_kron(a: torch.Tensor, s1: torch.Tensor, p1_inv: torch.Tensor, p2_inv: t
     return out
 
 
+@_on_stream
 def encode(w: torch.Tensor, M: torch.Tensor, A: Optional[torch.Tensor] = None,
            codes: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -292,6 +301,7 @@ def encode(w: torch.Tensor, M: torch.Tensor, A: Optional[torch.Tensor] = None,
     return codes, err
 
 
+@_on_stream
 def layer_b1(a: torch.Tensor, t_inv: torch.Tensor, M: torch.Tensor, d: int, D: int,
              w_packed: torch.Tensor, s: torch.Tensor, out: Optional[torch.Tensor] = None,
              stream=None) -> torch.Tensor:
@@ -311,6 +321,7 @@ def layer_b1(a: torch.Tensor, t_inv: torch.Tensor, M: torch.Tensor, d: int, D: i
     return out
 
 
+@_on_stream
 def gemm_decoded(w_packed: torch.Tensor, s: torch.Tensor, M: torch.Tensor, d: int, D: int,
                  u: torch.Tensor, out: Optional[torch.Tensor] = None,
                  stream=None) -> torch.Tensor:
@@ -330,6 +341,7 @@ def gemm_decoded(w_packed: torch.Tensor, s: torch.Tensor, M: torch.Tensor, d: in
     return out
 
 
+@_on_stream
 def softmin_grad(w: torch.Tensor, M: torch.Tensor, T: float = 10.0,
                  loss: Optional[torch.Tensor] = None, grad: Optional[torch.Tensor] = None,
                  stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -350,6 +362,7 @@ def softmin_grad(w: torch.Tensor, M: torch.Tensor, T: float = 10.0,
     return loss, grad
 
 
+@_on_stream
 def adam_update(M: torch.Tensor, grad: torch.Tensor, m1: torch.Tensor, m2: torch.Tensor,
                 step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
                 eps: float = 1e-8, stream=None) -> None:
@@ -360,6 +373,7 @@ def adam_update(M: torch.Tensor, grad: torch.Tensor, m1: torch.Tensor, m2: torch
                                _stream(stream)))
 
 
+@_on_stream
 def learn_m(M0: torch.Tensor, batches, T: float = 10.0, lr: float = 0.01,
             stream=None) -> Tuple[torch.Tensor, list]:
     """Adam on the soft-argmin objective from M0, one step per batch of
@@ -386,7 +400,8 @@ def workspace(nbytes: int, device: torch.device, tag: int = 0, stream=None) -> t
     order, so they may share it; calls on different streams get their own.
     The GEMV uses its row count as tag, the Kronecker lift -1, the encoder -2,
     the soft-argmin objective -3, the decode-weights product -4, the GEMV on
-    the parts image -5."""
+    the parts image -5.  The zeros are written on the current stream, which is
+    the call's (_on_stream)."""
     key = (device.type, device.index, _stream(stream), tag)
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -401,6 +416,7 @@ def gemv_workspace_size(m: int, K: int, B: int) -> int:
     return n.value
 
 
+@_on_stream
 def gemv(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor, K: Optional[int] = None,
          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out [B][m] = s * (sigma @ a_lift^T), float32 lifted activations, 1 <= B <= 16."""
@@ -419,6 +435,7 @@ def gemv(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor, K: Optio
     return out
 
 
+@_on_stream
 def gemv_parts(w_packed: torch.Tensor, s: torch.Tensor, parts: torch.Tensor, K: int, B: int,
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out [B][m] = s * (sigma @ a_hat^T) from the image of lift_parts."""
@@ -435,6 +452,7 @@ def gemv_parts(w_packed: torch.Tensor, s: torch.Tensor, parts: torch.Tensor, K: 
     return out
 
 
+@_on_stream
 def gemv_noalloc(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
                  out: torch.Tensor, stream=None) -> torch.Tensor:
     """lq_gemv without a workspace (the library's per-GPU scratch; calls on
@@ -447,6 +465,7 @@ def gemv_noalloc(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor,
     return out
 
 
+@_on_stream
 def stream_read(buf: torch.Tensor, sink: torch.Tensor, stream=None) -> None:
     """Read every byte of buf once (the HBM read-rate reference); sink: a
     device int32 tensor of at least 4 x compute units."""
@@ -455,6 +474,7 @@ def stream_read(buf: torch.Tensor, sink: torch.Tensor, stream=None) -> None:
                                _stream(stream)))
 
 
+@_on_stream
 def gemm(w_packed: torch.Tensor, s: torch.Tensor, a_lift: torch.Tensor, K: Optional[int] = None,
          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """out [B][m] on the matrix cores; a_lift float16 or bfloat16 [B][K]."""

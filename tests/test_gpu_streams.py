@@ -65,3 +65,28 @@ def test_results_of_another_stream_can_be_dropped_early():
         call(y, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(read, want)
+
+
+def test_the_other_wrappers_on_a_stream_of_their_own():
+    """Lift and GEMV of one and sixteen tokens, the layer on the parts image and M's objective on a
+    side stream that makes every workspace for the first time, beside the same on the current one."""
+    from bit_lifted_gemv_amd import synth
+    gen = torch.Generator().manual_seed(6)
+    L = synth.make_layer(m=4096, n=4096, d=8, D=19, B=16, seed=6, dtype="bf16")
+    layer = lq.DeviceLayer.from_synth(L, device="cuda")
+    a = lq.to_torch_16(L.a, L.dtype).cuda()
+    samples = torch.randn(20000, 8, generator=gen).cuda()
+
+    def run(stream=None):
+        one = lq.lift(a[:1], layer.t_inv, layer.M, layer.d, layer.D, stream=stream)
+        out = [lq.gemv(layer.w, layer.s, one, layer.K, stream=stream)]
+        img = lq.lift_parts(a, layer.t_inv, layer.M, layer.d, layer.D, stream=stream)
+        out.append(lq.gemv_parts(layer.w, layer.s, img, layer.K, 16, stream=stream))
+        return out + list(lq.softmin_grad(samples, layer.M, stream=stream))
+    want = run()
+    for _ in range(3):
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        here, there = run(), run(side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(want, here, there))

@@ -126,6 +126,50 @@ def test_memory_comes_from_the_stream_of_the_call(gpu, name):
     assert gpu.handles == [77, 0] and all(t.owner is gpu.default for t in gpu.made)
 
 
+def older_calls():
+    T = Tensor
+    f32, f16 = torch.float32, torch.float16
+    w, s, M = T((64, 4), torch.int32), T((64,), f32), T((8, 8), f32)
+    a, t_inv = T((8, 128), f16), T((1, 128, 128), f16)
+    return {
+        "pack_signs": lambda **k: lq.pack_signs(T((64, 128), torch.uint8), **k),
+        "unpack_signs": lambda **k: lq.unpack_signs(w, 128, **k),
+        "lift": lambda **k: lq.lift(a, t_inv, M, 8, 8, **k),
+        "lift_parts": lambda **k: lq.lift_parts(a, t_inv, M, 8, 8, **k),
+        "lift_kron": lambda **k: lq.lift_kron(a, T((128,), f32), T((16, 16), f32), T((8, 8), f32),
+                                              T((16,), f32), M, 8, 8, **k),
+        "encode": lambda **k: lq.encode(T((50, 8), f32), M, T((0, 8), f32), **k),
+        "layer_b1": lambda **k: lq.layer_b1(T((1, 128), f16), t_inv, M, 8, 8, w, s, **k),
+        "gemm_decoded": lambda **k: lq.gemm_decoded(w, s, M, 8, 8, a, **k),
+        "softmin_grad": lambda **k: lq.softmin_grad(T((50, 8), f32), M, **k),
+        "gemv": lambda **k: lq.gemv(w, s, T((8, 128), f32), **k),
+        "gemv_parts": lambda **k: lq.gemv_parts(w, s, T((4096,), torch.uint8), 128, 8, **k),
+        "gemm": lambda **k: lq.gemm(w, s, a, **k),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(older_calls()))
+def test_memory_of_the_other_wrappers_comes_from_the_stream_of_the_call(gpu, name):
+    """Their workspaces are kept per stream and filled with zeros when made: on that stream too."""
+    out = older_calls()[name](stream=gpu.other)
+    assert gpu.handles == [77] and gpu.made
+    assert all(t.owner is gpu.other for t in gpu.made)
+    for t in out if isinstance(out, tuple) else (out,):
+        assert gpu.default.cuda_stream in t.used_on
+    older_calls()[name]()
+    assert gpu.handles == [77, 0]
+
+
+def test_wrappers_without_results_take_a_stream(gpu):
+    buf, sink = Tensor((4096,), torch.uint8), Tensor((4096,), torch.int32)
+    assert lq.stream_read(buf, sink, stream=gpu.other) is None and buf.used_on == {77}
+    four = [Tensor((8, 8), torch.float32) for _ in range(4)]
+    assert lq.adam_update(*four, 1, 0.01, stream=gpu.other) is None
+    w, s, a, out = Tensor((64, 4), torch.int32), Tensor((64,), torch.float32), Tensor((8, 128), torch.float32), Tensor((8, 64), torch.float32)
+    assert lq.gemv_noalloc(w, s, a, out, stream=gpu.other) is out and out.used_on == {77}
+    assert gpu.handles == [77, 77, 77]
+
+
 def test_arguments_are_kept_for_the_stream_of_the_call(gpu):
     w, s = Tensor((64, 4), torch.int32), Tensor((64,), torch.float32)
     a, bias = Tensor((40, 128), torch.float16), Tensor((64,), torch.float32)
