@@ -246,6 +246,15 @@ F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtyp
   return p;
 }
 
+// What a plain or a gated call of these sizes needs (an odd m has no gated form).
+size_t f6_bytes(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtype out_dtype,
+                bool grouped) {
+  const size_t plain = f6_plan(E, m, K, rows, R, out_dtype, false, grouped, false).bytes;
+  if (m % 2) return plain;
+  const size_t gated = f6_plan(E, m, K, rows, R, out_dtype, true, grouped, false).bytes;
+  return plain > gated ? plain : gated;
+}
+
 // The product of a checked call: conversion where it is a launch of its own,
 // then the kernel.  p lacks only what the plan decides.
 hipError_t f6_run(lq::F6Product& p, const F6Plan& plan, int64_t K, const void* a, lq_dtype a_dt,
@@ -743,9 +752,7 @@ lq_status lq_gemm_ep_workspace_size(int64_t m, int64_t K, int64_t B, lq_dtype ou
   if (!valid_dtype(out_dtype)) return fail(LQ_ERR_DTYPE, "unknown dtype");
   const lq_status st = f6_sizes(1, m, K, B, out_dtype);
   if (st != LQ_OK) return st;
-  const size_t plain = f6_plan(1, m, K, B, B, out_dtype, false, false, false).bytes;
-  const size_t gated = f6_plan(1, m, K, B, B, out_dtype, true, false, false).bytes;
-  *bytes = plain > gated ? plain : gated;
+  *bytes = f6_bytes(1, m, K, B, B, out_dtype, false);
   return ok();
 }
 
@@ -785,9 +792,7 @@ lq_status lq_gemm_grouped_workspace_size(int64_t E, int64_t m, int64_t K, int64_
   lq_status st = f6_sizes(E, m, K, a_rows, out_dtype);
   if (st == LQ_OK && (R < 0 || R > INT32_MAX)) st = fail(LQ_ERR_SHAPE, "R=%lld", (long long)R);
   if (st != LQ_OK) return st;
-  const size_t plain = f6_plan(E, m, K, a_rows, R, out_dtype, false, true, false).bytes;
-  const size_t gated = f6_plan(E, m, K, a_rows, R, out_dtype, true, true, false).bytes;
-  *bytes = plain > gated ? plain : gated;
+  *bytes = f6_bytes(E, m, K, a_rows, R, out_dtype, true);
   return ok();
 }
 
