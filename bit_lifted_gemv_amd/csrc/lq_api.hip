@@ -187,14 +187,14 @@ lq_status f6_workspace(const void* workspace, size_t have, size_t need) {
 }
 
 lq_status join_sizes(int64_t T, int32_t k) {
-  if (T < 0 || k < 1 || k > 32 || T * k > INT32_MAX)
+  if (T < 0 || T > INT32_MAX || k < 1 || k > 32 || T * k > INT32_MAX)
     return fail(LQ_ERR_SHAPE, "T=%lld k=%d (k in 1..32)", (long long)T, (int)k);
   return LQ_OK;
 }
 
 lq_status route_sizes(int64_t T, int64_t E, int32_t k) {
   if (E < 1 || E > 1024) return fail(LQ_ERR_SHAPE, "E=%lld outside 1..1024", (long long)E);
-  if (T < 0 || k < 1 || k > 32 || k > E || T * k > INT32_MAX)
+  if (T < 0 || T > INT32_MAX || k < 1 || k > 32 || k > E || T * k > INT32_MAX)
     return fail(LQ_ERR_SHAPE, "T=%lld k=%d E=%lld (k in 1..min(E, 32))", (long long)T, (int)k,
                 (long long)E);
   return LQ_OK;

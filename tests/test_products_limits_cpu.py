@@ -31,3 +31,10 @@ def status(name, *sizes):
 def test_one_row_of_weights(name, sizes):
     st, need = status(name, *sizes)
     assert st == OK and need > 0
+
+
+@pytest.mark.parametrize("T,k", [(1 << 62, 4), (1 << 59, 32), ((1 << 63) - 1, 2), (1 << 31, 1), (1 << 30, 2)])
+def test_too_many_choices_are_refused(T, k):
+    """T * k < 2^31, also where the product of the two wraps round to a small number."""
+    assert status("lq_route_workspace_size", T, 64, k)[0] == SHAPE
+    assert status("lq_gemm_join_workspace_size", 4, 64, 128, 10, T, k, BF16)[0] == SHAPE
