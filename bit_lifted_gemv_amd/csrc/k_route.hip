@@ -253,6 +253,8 @@ __global__ void __launch_bounds__(kThreads) route_choose_kernel(RouteArgs a) {
   float weight[2];
   for (int r = 0; r < a.per; ++r) {
     const int run = blockIdx.x * a.per + r;
+    // past the last run: its tokens' numbers may lie past 2^31
+    if (run > 0 && run > (a.T - 1) / kRun) break;
     if (tid < E) mask[tid] = 0;
     __syncthreads();
     for (int q = tid / L; q < kRun; q += kThreads / L) {

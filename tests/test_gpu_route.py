@@ -160,3 +160,19 @@ def test_route_runs_per_workgroup(T, E, k, crowd):
     # |d| 2^-24, beside 2^-20 for exp, the sum and the quotient
     near = 2.0**-20 + np.abs(top - top[:, :1]) * 2.0**-24
     assert (np.abs(r.weight.cpu().double().numpy() - share) <= near * share + 1e-38).all()
+
+
+def test_route_most_tokens():
+    """T = 2^31 - 1: the last workgroup's runs would go on past 2^31.  One expert: every token's
+    choice is 0, and order and positions are the tokens' own."""
+    T = 2**31 - 1
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    r = lq.route(torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda"), 1)
+    assert r.offsets.tolist() == [0, T]
+    assert not r.ids.any() and (r.weight == 1).all()
+    for lo in range(0, T, 1 << 28):
+        own = torch.arange(lo, min(lo + (1 << 28), T), dtype=torch.int32, device="cuda")
+        assert torch.equal(r.pos[lo:lo + (1 << 28), 0], own) and torch.equal(r.rows[lo:lo + (1 << 28)], own)
+    del r, own
+    torch.cuda.empty_cache()
