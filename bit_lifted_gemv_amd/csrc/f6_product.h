@@ -14,7 +14,7 @@ __device__ __forceinline__ int run_tiles(const F6Product& a, int e, int TOK, int
   if (e >= a.E) return 0;
   lo = min(max(a.offsets[e], 0), a.R);
   end = min(max(a.offsets[e + 1], lo), a.R);
-  return (end - lo + TOK - 1) / TOK;
+  return end > lo ? 1 + (end - lo - 1) / TOK : 0;
 }
 
 __device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive

@@ -134,17 +134,22 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   }
   const int total = tiles * RT * a.slices;
   const int chunk = (total + 7) / 8;
-  const int at = static_cast<int>(blockIdx.x & 7) * chunk + static_cast<int>(blockIdx.x >> 3);
-  if (static_cast<int>(blockIdx.x >> 3) >= chunk || at >= total) return;
+  const int block = a.block0 + static_cast<int>(blockIdx.x);
+  if (block >> 3 >= chunk) return;
+  const int at = (block & 7) * chunk + (block >> 3);
+  if (at >= total) return;
   const int slice = a.slices == 1 ? 0 : at / (tiles * RT), here = at - slice * tiles * RT;
   const int pair = here / (2 * RT), in = here - pair * 2 * RT;
   const int wide = min(2, tiles - 2 * pair);
   int tile = 2 * pair + in % wide;
   const int rt = in / wide;
-  int expert = 0, row0 = tile * TOK, row_end = a.R;
+  int expert = 0, row0, row_end = a.R;
   if (a.offsets) {
-    if (a.E <= 64) find_in(runs, 0, tile, TOK, expert, row0, row_end);
-    else find_run(a, tile, TOK, lane, expert, row0, row_end);
+    const bool found = a.E <= 64 ? find_in(runs, 0, tile, TOK, expert, row0, row_end)
+                                 : find_run(a, tile, TOK, lane, expert, row0, row_end);
+    if (!found) return;
+  } else {
+    row0 = tile * TOK;
   }
   const int tokens = min(TOK, row_end - row0);
 
@@ -408,8 +413,15 @@ hipError_t launch(const F6Product& p, hipStream_t st) {
   const hipError_t big = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, P::LDS);
   if (big != hipSuccess) return big;
-  k<<<dim3(static_cast<uint32_t>(grid)), 64 * P::NW, P::LDS, st>>>(a);
-  return hipGetLastError();
+  // a launch has fewer than 2^32 threads: more workgroups go in several
+  constexpr int64_t kMost = (int64_t{1} << 31) / (64 * P::NW);
+  for (int64_t b = 0; b < grid; b += kMost) {
+    a.block0 = static_cast<int>(b);
+    k<<<dim3(static_cast<uint32_t>(grid - b < kMost ? grid - b : kMost)), 64 * P::NW, P::LDS, st>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int NP>

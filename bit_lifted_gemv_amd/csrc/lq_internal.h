@@ -186,6 +186,7 @@ struct F6Product {
   const int* rows;             // image row of each row, or null: its own
   int src_rows;                // rows of the image (with `rows`, one more of zeros follows)
   int row_tiles, token_tiles;  // set by the launcher
+  int block0;                  // its launch's first workgroup
   int slices, slice_units;     // of the positions, in units of 256
   float* sums;                 // [slices][R][ldz] scaled sums of the slices, or null
   int64_t ldz;

@@ -49,3 +49,30 @@ def test_one_row_of_weights_per_expert(dtype):
     own = a[r.rows.long()].contiguous()
     out = lq.gemm_join(w, s, own, r.offsets, r.pos, r.weight, out_dtype=dtype)
     assert torch.equal(out, pick.to(dtype))                                  # k = 1: the weight is 1
+
+
+def test_most_rows_of_experts():
+    """R = 2^31 - 1 gathered rows: more workgroups than one launch takes, runs whose tiles' end lies
+    past 2^31, and rows behind the last run, which stay."""
+    R, E, K, T = 2**31 - 1, 3, 8, 16
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    gen = torch.Generator().manual_seed(12)
+    w, s = words(gen, E, 1, K), torch.ones(E, 1, device="cuda")
+    a = whole(gen, T, K, BF16)
+    rows = torch.randint(0, T, (R,), dtype=torch.int32, device="cuda")
+    ends = [0, 5, 5, R - 2]
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    out = torch.full((R, 1), 300.0, dtype=BF16, device="cuda")
+    lq.gemm_grouped(w, s, a, off, rows=rows, out=out)
+    z = [(a.double() @ signs(w[e], K).T)[:, 0].to(BF16) for e in range(E)]
+    for e in range(E):
+        for lo in range(ends[e], ends[e + 1], 1 << 28):
+            hi = min(lo + (1 << 28), ends[e + 1])
+            assert torch.equal(out[lo:hi, 0], z[e][rows[lo:hi]]), (e, lo)
+    assert (out[R - 2:] == 300).all()
+    off[3] = R                                               # the last run's end is R itself
+    lq.gemm_grouped(w, s, a, off, rows=rows, out=out)
+    assert torch.equal(out[-1000:, 0], z[2][rows[-1000:]])
+    del out, rows
+    torch.cuda.empty_cache()
