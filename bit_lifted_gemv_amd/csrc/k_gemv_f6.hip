@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   // ---- which tokens, slice and row blocks
-  int tile = blockIdx.z, expert = 0, row0 = tile * f.tok, row_end = a.R;
+  int tile = f.tile0 + blockIdx.z, expert = 0, row0 = tile * f.tok, row_end = a.R;
   if (a.offsets && !find_run(a, tile, f.tok, lane, expert, row0, row_end)) return;
   const int tokens = min(f.tok, row_end - row0);
   const int slice = blockIdx.y;
@@ -307,17 +307,24 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
 }
 
 template <int NP, int T, int DEPTH, bool BF16>
-hipError_t launch(const F6Few& f, int tiles, hipStream_t st) {
+hipError_t launch(const F6Few& args, int tiles, hipStream_t st) {
   auto* k = gemv_f6_kernel<NP, T, DEPTH, BF16>;
-  const dim3 grid((f.row_blocks + f.blocks_per - 1) / f.blocks_per, f.p.slices, tiles);
+  F6Few f = args;
   const int lds = f.exchange_at + (f.kv > 1 ? kWaves * T * 1024 : 0);
   if (lds > 64 * 1024) {                   // per call: the attribute belongs to the current device
     const hipError_t big = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (big != hipSuccess) return big;
   }
-  k<<<grid, 64 * kWaves, lds, st>>>(f);
-  return hipGetLastError();
+  // a grid's z ends at 65535: small matrices with more tiles take several launches
+  for (f.tile0 = 0; f.tile0 < tiles; f.tile0 += 65535) {
+    const dim3 grid((f.row_blocks + f.blocks_per - 1) / f.blocks_per, f.p.slices,
+                    tiles - f.tile0 < 65535 ? tiles - f.tile0 : 65535);
+    k<<<grid, 64 * kWaves, lds, st>>>(f);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

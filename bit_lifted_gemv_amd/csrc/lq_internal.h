@@ -213,6 +213,7 @@ struct F6Few {
   int64_t lda;
   int K;
   int tok, kv, slice_groups, row_blocks, blocks_per, exchange_at;
+  int tile0;                   // the launch's first tile
 };
 hipError_t launch_gemv_f6(const F6Few& f, const F6FewPlan& plan, int NP, hipStream_t st);
 

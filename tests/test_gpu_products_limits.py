@@ -76,3 +76,15 @@ def test_most_rows_of_experts():
     assert torch.equal(out[-1000:, 0], z[2][rows[-1000:]])
     del out, rows
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("m,K,B", [(8, 128, 65535 * 16 + 1), (8, 128, 1100000), (1, 512, 2 * 65535 * 16 + 5)])
+def test_more_token_tiles_than_a_grid_is_deep(m, K, B):
+    """So few signs that the kernel for few rows takes any number of tokens, 16 a tile."""
+    gen = torch.Generator().manual_seed(B)
+    w, s = words(gen, m, K), torch.ones(m, device="cuda")
+    a = torch.randint(-8, 9, (B, K), dtype=torch.int8, device="cuda").to(BF16)
+    out = lq.gemm_ep(w, s, a)
+    for lo in range(0, B, 1 << 19):
+        z = a[lo:lo + (1 << 19)].double() @ signs(w, K).T
+        assert torch.equal(out[lo:lo + (1 << 19)], z.to(BF16)), lo
