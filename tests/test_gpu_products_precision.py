@@ -4,7 +4,9 @@ float16 results keep an activation to 2^-19 of the largest one of its 32
 positions: behind three float6 parts the remainder is at most 1/16 of a unit of
 the third part's scale (2^-12 where the largest value is scaled into [4, 8)),
 so 2^14 times it lies below 4, where float6 has steps of at most 1/4, and half
-of one is 2^-17, 2^-19 of a largest value of 4.
+of one is 2^-17, 2^-19 of a largest value of 4.  float32 results keep 2^-24 of it (the
+fourth part leaves 1/8 of a unit at 2^-14, 32 times which lies at 4: half a step
+of 1/4 at 2^-19 is 2^-22, 2^-24 of 4).
 """
 import math
 
@@ -106,3 +108,38 @@ def test_float16_results_with_outliers_round_like_the_exact_ones(dev, B, gated):
     best = rms(y.to(F16).double() - y)
     bound = math.sqrt(best**2 + ((5e-5 if gated else 3e-5) * rms(y))**2)
     assert rms(out.double() - y) <= bound
+
+
+def sparse_beside_large(gen, rows, K):
+    """float16 values of 11 bits below 1 in 2000 positions at most, and 2048 in one: all are multiples
+    of 2^-11, and any partial sum lies below 2000 + 2048 < 2^12, so float32 sums are exact."""
+    a = torch.randint(1024, 2048, (rows, K), generator=gen).double() * 2.0**-11
+    a *= 2 * torch.randint(0, 2, (rows, K), generator=gen) - 1
+    if K > 2000:
+        a *= torch.zeros(K, dtype=torch.float64).index_fill_(0, torch.randperm(K, generator=gen)[:2000], 1.0)
+    a[torch.arange(rows), torch.randint(0, K, (rows,), generator=gen)] = 2048.0
+    return a
+
+
+@pytest.mark.parametrize("m,K,B", [(64, 65536, 1), (512, 16384, 5), (4096, 16384, 16), (300, 32768, 40), (1281, 5128, 777)])
+def test_float32_result_is_exact_over_slices(dev, m, K, B):
+    gen = torch.Generator().manual_seed(m + K + B)
+    w, a = words(gen, m, K), sparse_beside_large(gen, B, K)
+    z = a.to(dev) @ signs(w.to(dev), K).T
+    out = lq.gemm_ep(w.to(dev), torch.ones(m, device=dev), a.to(F16).to(dev), out_dtype=F32)
+    assert torch.equal(out.double(), z)
+
+
+@pytest.mark.parametrize("E,m,K,T", [(4, 256, 1024, 2), (8, 500, 1024, 300), (2, 320, 32768, 20), (3, 64, 65536, 4)])
+def test_float32_expert_results_are_exact(dev, E, m, K, T):
+    """Into the experts, and out of them with weights of 1: sums of two rows, below 2^13."""
+    k = 2
+    gen = torch.Generator().manual_seed(E + m + K + T)
+    w, s = words(gen, E, m, K).to(dev), torch.ones(E, m, device=dev)
+    r = lq.route(torch.randn(T, E, generator=gen).to(dev), k)
+    off, rows = r.offsets.tolist(), r.rows.long()
+    a = sparse_beside_large(gen, T, K).to(dev)
+    z = torch.cat([a[rows[off[e]:off[e + 1]]] @ signs(w[e], K).T for e in range(E)])
+    assert torch.equal(lq.gemm_grouped(w, s, a.to(F16), r.offsets, rows=r.rows, out_dtype=F32).double(), z)
+    out = lq.gemm_join(w, s, a[rows].to(F16).contiguous(), r.offsets, r.pos, torch.ones(T, k, device=dev), out_dtype=F32)
+    assert torch.equal(out.double(), z[r.pos.long()].sum(1))
