@@ -819,7 +819,10 @@ class DeviceExperts:
                 residual: Optional[torch.Tensor] = None, valid: Optional[torch.Tensor] = None,
                 renorm: bool = True) -> torch.Tensor:
         """x [T][n] (float16 or bfloat16), router logits [T][E] -> [T][n]: each token
-        through its k experts, weighted, plus the residual.  valid[t] == 0: none."""
+        through its k experts, weighted, plus the residual.  valid[t] == 0: none.
+        No tokens give no rows."""
+        if x.shape[0] == 0:                        # the lift takes one row at least
+            return torch.empty((0, self.w2.shape[1]), dtype=x.dtype, device=x.device)
         r = route(logits, self.k, valid=valid, renorm=renorm)
         a = lift(x, self.t1, self.M1, self.d, self.D, out_dtype=x.dtype)
         h = gemm_grouped(self.w1, self.s1, a, r.offsets, rows=r.rows, bias=self.bias1,
