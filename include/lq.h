@@ -434,7 +434,8 @@ lq_status lq_gemm(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw,
  * residual: [B] rows, ldr apart, of out_dtype, or NULL; it may be `out`
  *           itself (with ldr == ldo), otherwise it must not overlap it.
  * out:      [B] rows of m (gated: m/2) values of out_dtype (LQ_F32, LQ_F16 or
- *           LQ_BF16, rounded once to nearest even), ldo apart.
+ *           LQ_BF16, rounded once to nearest even), ldo apart; it must not
+ *           overlap a_lift.
  * workspace: >= lq_gemm_ep_workspace_size bytes, 256-byte aligned,
  *           caller-owned, no initialisation needed.
  * Requires B >= 1; B rows of operand image (2.4 bytes per position, 3.1 for
@@ -520,8 +521,9 @@ lq_status lq_gemm_grouped(const uint32_t* w_packed, int64_t E, int64_t m, int64_
  * pos, weight: int32 and float [T][k] (lq_route's).  A position outside
  *           [0, R) adds nothing (one inside, but outside every run, adds an
  *           unspecified value: lq_route gives none).
- * residual: [T] rows of out_dtype, ldr apart, or NULL; it may be `out`.
- * out:      [T] rows of m values of out_dtype, ldo apart.
+ * residual: [T] rows of out_dtype, ldr apart, or NULL; it may be `out`
+ *           (with ldr == ldo).
+ * out:      [T] rows of m values of out_dtype, ldo apart; it may overlap a_lift.
  * Sums over j in float32, in order.  1 <= k <= 32, T*k < 2^31, T == 0 is a
  * no-op; everything else as lq_gemm_grouped.
  */

@@ -90,3 +90,42 @@ def test_the_other_wrappers_on_a_stream_of_their_own():
         here, there = run(), run(side)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) and torch.equal(x, z) for x, y, z in zip(want, here, there))
+
+
+@pytest.mark.parametrize("name", ["prompt", "tokens", "grouped", "join", "route"])
+def test_a_captured_call_on_a_side_stream(name):
+    """Inside one graph: a call on a second stream beside one on the captured stream.  Replayed three
+    times with new inputs and eager calls between."""
+    gen = torch.Generator().manual_seed(8)
+    (x, y), call = case(name, gen)
+    flat = lambda r: r if isinstance(r, tuple) else (r,)  # noqa: E731
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    call(x), call(y, stream=side)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        there, here = flat(call(y, stream=side)), flat(call(x))
+        main.wait_stream(side)
+        both = [p.float() + q.float() for p, q in zip(here, there)]
+    for _ in range(3):
+        for t in (x, y):
+            t.copy_(torch.randn(t.shape, generator=gen).to(t.dtype))
+        g.replay()
+        torch.cuda.synchronize()
+        want_x, want_y = flat(call(x)), flat(call(y))
+        assert all(torch.equal(p, q) for p, q in zip(want_x, here))
+        assert all(torch.equal(p, q) for p, q in zip(want_y, there))
+        assert all(torch.equal(p.float() + q.float(), b) for p, q, b in zip(want_x, want_y, both))
+
+
+def test_join_may_write_over_its_activations():
+    """out in the place of a_lift: the sums over experts come last."""
+    gen = torch.Generator().manual_seed(9)
+    for T in (3, 300):
+        E, m, k = 4, 512, 2
+        w, s = words(gen, E, m, m), torch.rand(E, m, generator=gen).cuda()
+        r = lq.route(torch.randn(T, E, generator=gen).cuda(), k)
+        a = torch.randn(T * k, m, generator=gen).to(BF16).cuda()
+        want = lq.gemm_join(w, s, a, r.offsets, r.pos, r.weight)
+        assert torch.equal(lq.gemm_join(w, s, a, r.offsets, r.pos, r.weight, out=a[:T]), want)

@@ -144,3 +144,14 @@ def test_wrappers_refuse_tensors_on_the_host():
         lq.gemm_ep(w, s, a)
     with pytest.raises(ValueError):
         lq.route(torch.zeros(2, 4), 2)
+
+
+def test_outputs_over_the_activations_are_refused(L):
+    """A workgroup writes outputs while others still read activations; the residual may be the output
+    itself, but then row by row."""
+    Q, W = P + (1 << 28), P + (2 << 28)
+    for B in (1, 300):
+        assert ep(L, m=4096, a=Q, out=Q, ws=W, B=B) == UNSUPPORTED
+    assert grouped(L, a=Q, out=Q, ws=W) == UNSUPPORTED
+    assert ep(L, a=P, out=Q, res=Q, ldr=8192, ws=W) == UNSUPPORTED
+    assert join(L, R=10, a=P, out=Q, res=Q, ldr=128, ws=W) == UNSUPPORTED
