@@ -470,11 +470,14 @@ F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
   // 28672: 1615; 256 x 64 in two of four 1637), or the latter where the last
   // round of the former would be filled below 9/10 (4096 x 4096 -> 2816: 118
   // against 135; 1024 x 8192 -> 28672: 430 against 448).  Of runs the last
-  // round is not known here: always the former (3000 rows of 8 experts, 28672
-  // -> 4096: 767 against 839).
+  // round is not known here, and the latter's second workgroup covers the ends
+  // of a tile: up to 8192 positions the latter (16384 rows of 64 experts, 4096
+  // -> 2 x 1408: 397 against 431; 8192 of 8, 4096 -> 2 x 14336: 1751 against
+  // 1738), past that the former (3000 of 8, 28672 -> 4096: 766 against 829).
   p.slices = 1;
   if (NP == 3 && two && count(4, 2) > cus) p.shape = 4120;
-  else if (NP == 4 && !grouped && count(4, 2) > cus && count(4, 2) * 10 < up(count(4, 2)) * 9) p.shape = 2220;
+  else if (NP == 4 && two && count(4, 2) > cus &&
+           (grouped ? units <= 32 : count(4, 2) * 10 < up(count(4, 2)) * 9)) p.shape = 2220;
   else if (NP <= 4 && two && count(4, 2) * 5 >= cus * 4) p.shape = 4221;
   else if (two && count(2, 2) * 5 >= cus * 4) p.shape = 2421;
   else if (count(4, 1) >= 2 * cus) p.shape = 4110;

@@ -143,3 +143,37 @@ def test_float32_expert_results_are_exact(dev, E, m, K, T):
     assert torch.equal(lq.gemm_grouped(w, s, a.to(F16), r.offsets, rows=r.rows, out_dtype=F32).double(), z)
     out = lq.gemm_join(w, s, a[rows].to(F16).contiguous(), r.offsets, r.pos, torch.ones(T, k, device=dev), out_dtype=F32)
     assert torch.equal(out.double(), z[r.pos.long()].sum(1))
+
+
+# Each tile of the many-row kernel with four parts
+@pytest.mark.parametrize("m,K,B", [
+    (28672, 264, 1024),                    # 256 x 64 in two workgroups of four waves: 896 tiles of 512 rows
+    (28672, 256, 1170),                    # 512 x 64 in eight waves, 19 columns of token tiles
+    (8190, 512, 500),                      # 256 x 64 in eight waves
+    (262200, 256, 17), (38402, 1024, 60), (28672, 1032, 57), (4100, 8200, 40),
+])
+@pytest.mark.parametrize("gated", [False, True])
+def test_float16_results_of_each_tile(dev, m, K, B, gated):
+    """Whole numbers up to 8: sums below 2^17 are exact, and so is the result, rounded once."""
+    gen = torch.Generator().manual_seed(m + K + B)
+    w, s = words(gen, m, K).to(dev), torch.full((m,), 2.0**-4, device=dev)
+    a = torch.randint(-8, 9, (B, K), generator=gen).to(F16).to(dev)
+    pick = torch.randperm(m // 2, generator=gen)[:1000].to(dev)
+    at = torch.cat([pick, pick + m // 2])
+    z = a.double() @ signs(w[at], K).T * 2.0**-4
+    out = lq.gemm_ep(w, s, a, act="relu", gated=gated)
+    y = torch.relu(z[:, :len(pick)]) * z[:, len(pick):] if gated else torch.relu(z[:, :len(pick)])
+    # a gate's product of two exact numbers is rounded to float32 first
+    assert torch.equal(out[:, pick], y.float().to(F16))
+
+
+@pytest.mark.parametrize("E,m,K,T,k", [(64, 1408, 512, 2000, 8), (8, 4096, 8456, 700, 2), (16, 2048, 264, 1500, 4)])
+def test_float16_expert_results_of_the_large_tiles(dev, E, m, K, T, k):
+    gen = torch.Generator().manual_seed(E + m + K)
+    w, s = words(gen, E, m, K).to(dev), torch.full((E, m), 2.0**-4, device=dev)
+    r = lq.route(torch.randn(T, E, generator=gen).to(dev), k)
+    off, rows = r.offsets.tolist(), r.rows.long()
+    a = torch.randint(-8, 9, (T, K), generator=gen).to(F16).to(dev)
+    out = lq.gemm_grouped(w, s, a, r.offsets, rows=r.rows)
+    z = torch.cat([a[rows[off[e]:off[e + 1]]].double() @ signs(w[e], K).T for e in range(E)]) * 2.0**-4
+    assert torch.equal(out, z.to(F16))
