@@ -159,6 +159,13 @@ def _stream(stream=None) -> int:
     return s.cuda_stream
 
 
+def _tensors(x) -> list:
+    """The tensors among arguments or results, also in lists and tuples."""
+    if isinstance(x, (tuple, list)):
+        return [t for v in x for t in _tensors(v)]
+    return [x] if hasattr(x, "record_stream") else []
+
+
 def _on_stream(call):
     """A wrapper around the calls whose last parameter is `stream`.  A stream
     other than the current one becomes the current one for the call, so that
@@ -179,14 +186,11 @@ def _on_stream(call):
             return call(*args, **kwargs)
         with torch.cuda.stream(stream):
             result = call(*args, **kwargs)
-        given = [t for t in (*args, *kwargs.values()) if hasattr(t, "record_stream")]
+        given = _tensors((args, list(kwargs.values())))
         for t in given:
             t.record_stream(stream)
-        made = []
-        for r in result if isinstance(result, tuple) else (result,):
-            made += r if isinstance(r, list) else [r]
-        for t in made:
-            if t is not None and not any(t is g for g in given):
+        for t in _tensors(result):
+            if not any(t is g for g in given):
                 t.record_stream(caller)
         return result
     return run

@@ -129,3 +129,21 @@ def test_join_may_write_over_its_activations():
         a = torch.randn(T * k, m, generator=gen).to(BF16).cuda()
         want = lq.gemm_join(w, s, a, r.offsets, r.pos, r.weight)
         assert torch.equal(lq.gemm_join(w, s, a, r.offsets, r.pos, r.weight, out=a[:T]), want)
+
+
+def test_learning_on_a_side_stream():
+    """Samples made right before the call and dropped with it."""
+    gen = torch.Generator().manual_seed(10)
+    M0 = (torch.randn(8, 16, generator=gen) / 4).cuda()
+    host = [torch.randn(4096, 8, generator=gen) for _ in range(4)]
+    want, losses = lq.learn_m(M0, [x.cuda() for x in host])
+    for _ in range(3):
+        side = torch.cuda.Stream()
+        batches = [x.cuda() for x in host]
+        torch.cuda.synchronize()
+        M, ls = lq.learn_m(M0, batches, stream=side)
+        del batches
+        junk = [torch.full((4096, 8), float("nan"), device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+        assert torch.equal(M, want) and all(torch.equal(p, q) for p, q in zip(ls, losses))
+        del junk

@@ -186,3 +186,17 @@ def test_stream_of_another_device_is_refused(gpu):
     with pytest.raises(ValueError):
         lq.gemm_ep(w, s, a, stream=other)
     assert not gpu.handles
+
+
+def test_tensors_in_lists_are_kept_too(gpu):
+    a, b, c = (Tensor((8, 8), torch.float32) for _ in range(3))
+
+    @lq._on_stream
+    def call(x, several, stream=None):
+        return a, [c, None]
+    assert call(a, [b, (c, 3)], stream=gpu.other)[0] is a
+    assert a.used_on == b.used_on == c.used_on == {77}        # given, so not made by the call
+    d = Tensor((8, 8), torch.float32)
+    call2 = lq._on_stream(lambda x, stream=None: (x, [d]))
+    call2(a, stream=gpu.other)
+    assert d.used_on == {0}
