@@ -15,11 +15,11 @@
 // remainder of 1/8, 32 times.  The parts NP follow from the result's type, so
 // that what they lose stays below its own rounding (shares of the result,
 // root mean squares of sums of 8192, Gaussian values / with one position in a
-// hundred 20 times the others, emulated and as the kernels measure):
+// hundred 20 times the others):
 //   bfloat16 results, 1.7e-3: three parts, 2^-14 of the block's largest value
 //     (exact for a bfloat16 above 2^-6 or a float16 above 2^-3 of it); lost
-//     1.1e-5 / 7.8e-5 of bfloat16 values, 3.2e-5 / 1.3e-4 of float16 ones, half
-//     as much again through a gate;
+//     1.1e-5 / 7.8e-5 of bfloat16 values, 3.2e-5 / 1.3e-4 of float16 ones, 1.4
+//     times that through a gate;
 //   float16 results, 2.1e-4: four parts, 2^-19; lost below 1e-6 (three would
 //     make the error of gated float16 results with such values 2.8e-4);
 //   float32 results: five parts, 2^-24, below the sums' own rounding (four lost

@@ -3,10 +3,10 @@
 // A wave takes 64 blocks of 32 positions, whose parts are consecutive in the
 // image: it loads them with whole lines, turns each lane's block into parts
 // (LDS between, both ways) and stores whole lines again.  Bound by the bytes
-// read and written (2 and, of three parts, 2.4 per position): 4096 x 8192 in 26 us, 3000 x
-// 28672 in 56 (6.6 TB/s), and about 8 us at least.  `zero_row`: one more row of
-// zeros follows the last (what a gathered row with an index out of range
-// reads).
+// read and written (2 and 2.4 per position of three parts, 3.1 of four, 3.9 of
+// five): 4096 x 8192 of three in 26 us, 3000 x 28672 of four in 66 (6.7 TB/s),
+// and about 8 us at least.  `zero_row`: one more row of zeros follows the last
+// (what a gathered row with an index out of range reads).
 #include "f6_parts.h"
 #include "lq_internal.h"
 

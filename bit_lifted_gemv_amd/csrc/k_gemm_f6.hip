@@ -23,11 +23,13 @@
 // them before every read of LDS.  Every wave issues the same number per
 // stage (the last ones repeat a chunk).
 //
-// Measured (MI355X): 4096 x 8192 -> 2 x 14336 gated 1110 us, 1.73 PFLOP/s of
-// lifted product; 512 x 20480 -> 8192 127 us, 1.35; 16384 rows of 64 experts,
-// 4096 -> 2 x 1408, 290 us, 1.30.  Bound by power: the matrix cores are busy
-// 72 % of the cycles at 1.55 GHz; the instruction alone on random operands
-// runs at 1.6 GHz and 2.0.
+// Measured (MI355X, kernel trace, least and median): 4096 x 8192 -> 2 x 14336
+// gated, three parts, 1114 and 1144 us, 1.73 PFLOP/s of lifted product; 16384
+// rows of 64 experts, 4096 -> 2 x 1408, 298 and 317, 1.27; 512 x 20480 -> 8192 to
+// float16, four parts, 157 and 180, 1.09 (three took 127); 3000 rows of 8
+// experts, 28672 -> 4096, four parts, 682 and 709, 1.03.  Bound by power: the
+// matrix cores are busy 72 % of the cycles at 1.5 GHz; the instruction alone on
+// random operands gives 2.0 to 2.1 with three parts.
 //
 // End.  The tiles go through LDS, 32 tokens at a time, where the WK partial
 // sums are added in a fixed order and rows become consecutive, so stores are
@@ -456,7 +458,8 @@ F6ManyPlan many_f6_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
     return tiles * ((out_m + outs - 1) / outs);
   };
   auto up = [&](int64_t n) { return (n + cus - 1) / cus * cus; };
-  // The tallest tile that fills the compute units, measured on each side:
+  // The tallest tile that fills the compute units, measured on each side, with
+  // three parts where nothing else is said:
   // 512 x 64 in two workgroups of four waves per unit (4096 x 8192 -> 28672:
   // 1175 us; 256 x 64 in eight waves 1400), or in one of eight where there is
   // one tile each (1024 x 19456 -> 8192: 231 against 243); 256 x 64 (512 x

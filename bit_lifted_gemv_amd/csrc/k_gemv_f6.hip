@@ -23,10 +23,13 @@
 // many positions needs no second launch: few_f6_plan weighs the two.  Bound
 // by reading the signs once, and by latency for the smallest calls.
 //
-// Measured (MI355X): 1 x 10240 -> 4096 in 6.4 us (activations there after 1 us,
-// split after 2.3, signs done after 4.1, stored after 5.1); 5 x 68096 -> 8192
-// 17 us here (split 4.6 us, then signs at 6.9 TB/s) and 5 in the reduction; 16 x
-// 8192 -> 2 x 14336 gated 11 and 5; one token to 8 experts of 2816 x 4096: 10.2.
+// Measured (MI355X, medians of a kernel trace): 1 x 10240 -> 4096 in 6.2 us (by
+// clocks read in the kernel: activations there after 1 us, split after 2.3,
+// signs done after 4.1, stored after 5.1); 5 x 68096 -> 8192 to float16 25.1 here
+// and 4.8 in the reduction (of three parts 22.8; the 70 MB of signs come from
+// the 256 MB cache where calls on a few matrices repeat, faster than a copy of
+// 5.1 TB/s); 16 x 8192 -> 2 x 14336 gated 13.8 and 4.7; one token to 8 experts
+// of 2816 x 4096: 9.5.
 #include "f6_epilogue.h"
 #include "f6_parts.h"
 #include "f6_product.h"
@@ -335,7 +338,8 @@ hipError_t launch(const F6Few& args, int tiles, hipStream_t st) {
 // (0.7 of it the conversions alone); a compute unit's share of the HBM rate
 // 21 KB per us (16 with T = 1, where reading the operands from LDS is the
 // limit); a second launch 3 us (the join has one anyway) and its sums at
-// about 4 TB/s.
+// about 4 TB/s.  Of one matrix the first 16 tokens are planned, tiles of more
+// tokens run the same.
 static F6FewPlan find_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, int NP,
                            bool grouped, bool join, int64_t cus) {
   F6FewPlan p{};

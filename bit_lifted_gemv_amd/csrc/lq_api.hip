@@ -236,7 +236,9 @@ F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtyp
   // few rows: up to 16 in all, or so few signs that reading them for every 16
   // rows costs less than the other kernel's launches (32 x 10240 -> 4096: 17 us
   // on either; 64 x 4096 -> 2048: 11 against 14; 48 x 10240 -> 4096: 24 against
-  // 19), or about 8 a run on average
+  // 19), or about 8 a run on average (rows of 64 experts, 4096 -> 2 x 1408: 512
+  // spread evenly 46 here, 513 there 58; where all go to one expert, which the
+  // host does not know, 42 here and 27 there)
   p.few = grouped ? R <= kFewRowsPerRun * (E < R ? E : R)
                   : R <= kFewRows || (R + 15) / 16 * m * (K / 8) <= kFewBytes;
   if (p.few) {
