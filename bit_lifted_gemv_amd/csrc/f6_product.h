@@ -1,5 +1,5 @@
-// Arguments of the float4 x float6 products (k_gemm_f6.hip, k_gemv_f6.hip)
-// and the search for the expert run that a token tile belongs to.
+// The search for the expert run that a token tile belongs to, of the products
+// with E matrices (their arguments hold E, R and the offsets).
 #pragma once
 
 #include "lq_internal.h"
@@ -9,7 +9,8 @@ namespace f6 {
 
 // Tiles of TOK rows in expert e's run (0 past the last expert).  Offsets come
 // from the device unchecked: runs are cut to [0, R].
-__device__ __forceinline__ int run_tiles(const F6Product& a, int e, int TOK, int& lo, int& end) {
+template <class Product>
+__device__ __forceinline__ int run_tiles(const Product& a, int e, int TOK, int& lo, int& end) {
   lo = end = 0;
   if (e >= a.E) return 0;
   lo = min(max(a.offsets[e], 0), a.R);
@@ -31,7 +32,8 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive
 struct Runs {
   int lo, end, tiles, upto;
 };
-__device__ __forceinline__ Runs load_runs(const F6Product& a, int e0, int before, int TOK, int lane) {
+template <class Product>
+__device__ __forceinline__ Runs load_runs(const Product& a, int e0, int before, int TOK, int lane) {
   Runs r;
   r.tiles = run_tiles(a, e0 + lane, TOK, r.lo, r.end);
   r.upto = before + wave_scan(r.tiles, lane);
@@ -51,7 +53,8 @@ __device__ __forceinline__ bool find_in(const Runs& r, int e0, int tile, int TOK
   return true;
 }
 // The same over all experts; false past the last tile.
-__device__ __forceinline__ bool find_run(const F6Product& a, int tile, int TOK, int lane,
+template <class Product>
+__device__ __forceinline__ bool find_run(const Product& a, int tile, int TOK, int lane,
                                          int& expert, int& row0, int& row_end) {
   int before = 0;
   for (int e0 = 0; e0 < a.E; e0 += 64) {

@@ -1,43 +1,16 @@
 // C ABI of liblq: host-side validation and dispatch (declarations in include/lq.h).
 // Every entry point checks its arguments before launching anything, returns a
 // status code and records a thread-local message on failure.
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 #include <mutex>
 
 #include "f6_parts.h"
+#include "lq_checks.h"
 #include "lq_internal.h"
 
 namespace {
 
-thread_local char g_err[512] = "";
-
-lq_status fail(lq_status st, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof(g_err), fmt, ap);
-  va_end(ap);
-  return st;
-}
-
-lq_status ok() {
-  g_err[0] = '\0';
-  return LQ_OK;
-}
-
-lq_status hip_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return ok();
-  return fail(LQ_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-bool valid_dtype(lq_dtype dt) { return dt == LQ_F32 || dt == LQ_F16 || dt == LQ_BF16; }
-
-hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
-
-size_t dtype_size(lq_dtype dt) { return dt == LQ_F32 ? 4 : 2; }
+using namespace lq::api;
 
 // lq_gemm addresses a 128-row or 128-token block with 32-bit buffer offsets
 constexpr int64_t kGemmMaxK = int64_t{1} << 22;
@@ -167,25 +140,6 @@ lq_status f6_matrices(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ld
   return LQ_OK;
 }
 
-lq_status f6_rows_out(const void* residual, int64_t ldr, const void* out, lq_dtype out_dtype,
-                      int64_t ldo, int64_t width, int64_t rows) {
-  if (ldo < width && rows > 1)
-    return fail(LQ_ERR_SHAPE, "ldo=%lld < %lld outputs", (long long)ldo, (long long)width);
-  if (residual && ldr < width && rows > 1)
-    return fail(LQ_ERR_SHAPE, "ldr=%lld < %lld outputs", (long long)ldr, (long long)width);
-  if (!aligned(out, dtype_size(out_dtype)) || !aligned(residual, dtype_size(out_dtype)))
-    return fail(LQ_ERR_ALIGN, "misaligned out or residual");
-  return LQ_OK;
-}
-
-lq_status f6_workspace(const void* workspace, size_t have, size_t need) {
-  if (need == 0) return LQ_OK;
-  if (!workspace) return fail(LQ_ERR_WORKSPACE, "workspace of %zu bytes required", need);
-  if (have < need) return fail(LQ_ERR_WORKSPACE, "workspace %zu bytes < %zu required", have, need);
-  if (!aligned(workspace, 256)) return fail(LQ_ERR_ALIGN, "workspace must be 256-byte aligned");
-  return LQ_OK;
-}
-
 // Outputs over what other workgroups still read.  (Rows that interleave with the
 // activations' in one buffer are fine, so only the same start is looked at.)
 lq_status f6_overlap(const void* a_lift, const void* residual, int64_t ldr, const void* out,
@@ -193,12 +147,6 @@ lq_status f6_overlap(const void* a_lift, const void* residual, int64_t ldr, cons
   if (out == a_lift) return fail(LQ_ERR_UNSUPPORTED, "out overlaps a_lift");
   if (out == residual && ldr != ldo && rows > 1)
     return fail(LQ_ERR_UNSUPPORTED, "residual is out with another pitch");
-  return LQ_OK;
-}
-
-lq_status join_sizes(int64_t T, int32_t k) {
-  if (T < 0 || T > INT32_MAX || k < 1 || k > 32 || T * k > INT32_MAX)
-    return fail(LQ_ERR_SHAPE, "T=%lld k=%d (k in 1..32)", (long long)T, (int)k);
   return LQ_OK;
 }
 
@@ -225,8 +173,6 @@ struct F6Plan {
 };
 
 constexpr int64_t kFewRows = 16, kFewRowsPerRun = 8, kFewBytes = 10 << 20;
-
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // rows: of the activations, R: of the product (grouped: in the sorted order).
 F6Plan f6_plan(int64_t E, int64_t m, int64_t K, int64_t rows, int64_t R, lq_dtype out_dtype,
@@ -347,7 +293,7 @@ const char* lq_status_string(lq_status st) {
   }
 }
 
-const char* lq_last_error(void) { return g_err; }
+const char* lq_last_error(void) { return lq::api::g_err; }
 
 const char* lq_version(void) { return "liblq 0.1 gfx950"; }
 
@@ -780,9 +726,9 @@ lq_status lq_gemm_ep(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw
   if (B < 1) return fail(LQ_ERR_SHAPE, "B=%lld", (long long)B);
   const int64_t width = gated ? m / 2 : m;
   st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
-  if (st == LQ_OK) st = f6_rows_out(residual, ldr, out, out_dtype, ldo, width, B);
+  if (st == LQ_OK) st = check_rows_out(residual, ldr, out, out_dtype, ldo, width, B);
   const auto plan = f6_plan(1, m, K, B, B, out_dtype, gated != 0, false, false);
-  if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
+  if (st == LQ_OK) st = check_workspace(workspace, workspace_bytes, plan.bytes);
   if (st == LQ_OK) st = f6_overlap(a_lift, residual, ldr, out, ldo, B);
   if (st != LQ_OK) return st;
   lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, act, gated);
@@ -829,9 +775,9 @@ lq_status lq_gemm_grouped(const uint32_t* w_packed, int64_t E, int64_t m, int64_
     return fail(LQ_ERR_ALIGN, "misaligned rows or offsets");
   const int64_t width = gated ? m / 2 : m;
   st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
-  if (st == LQ_OK) st = f6_rows_out(nullptr, 0, out, out_dtype, ldo, width, R);
+  if (st == LQ_OK) st = check_rows_out(nullptr, 0, out, out_dtype, ldo, width, R);
   const auto plan = f6_plan(E, m, K, a_rows, R, out_dtype, gated != 0, true, false);
-  if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
+  if (st == LQ_OK) st = check_workspace(workspace, workspace_bytes, plan.bytes);
   if (st == LQ_OK) st = f6_overlap(a_lift, nullptr, 0, out, ldo, R);
   if (st != LQ_OK) return st;
   lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, act, gated);
@@ -875,9 +821,9 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
   if (!aligned(offsets, 4) || !aligned(pos, 4) || !aligned(weight, 4))
     return fail(LQ_ERR_ALIGN, "misaligned offsets, pos or weight");
   st = f6_matrices(w_packed, m, K, ldw, s, a_lift, lda, bias);
-  if (st == LQ_OK) st = f6_rows_out(residual, ldr, out, out_dtype, ldo, m, T);
+  if (st == LQ_OK) st = check_rows_out(residual, ldr, out, out_dtype, ldo, m, T);
   const auto plan = f6_plan(E, m, K, R, R, out_dtype, false, true, true);
-  if (st == LQ_OK) st = f6_workspace(workspace, workspace_bytes, plan.bytes);
+  if (st == LQ_OK) st = check_workspace(workspace, workspace_bytes, plan.bytes);
   if (st == LQ_OK) st = f6_overlap(nullptr, residual, ldr, out, ldo, T);  // out is written last
   if (st != LQ_OK) return st;
   const hipStream_t hs = as_stream(stream);
@@ -919,7 +865,7 @@ lq_status lq_route(const void* logits, lq_dtype dtype, int64_t T, int64_t E, int
       !aligned(pos, 4) || !aligned(rows, 4) || !aligned(offsets, 4))
     return fail(LQ_ERR_ALIGN, "misaligned pointer");
   const size_t need = lq::route_workspace_bytes(T, static_cast<int>(E));
-  st = f6_workspace(workspace, workspace_bytes, need);
+  st = check_workspace(workspace, workspace_bytes, need);
   if (st != LQ_OK) return st;
   return hip_status(lq::launch_route(logits, dtype, T, static_cast<int>(E), ld, valid, k, renorm,
                                      ids, weight, pos, rows, offsets, workspace,
