@@ -1,0 +1,73 @@
+// Eight-bit floating point (OCP e4m3, e5m2) with one power of two per 128
+// positions: the exponent of a block and the rounding, shared by the kernels
+// that quantize (k_quant8.hip, k_gemv8.hip).
+#pragma once
+
+#include "lq_internal.h"
+
+namespace lq {
+namespace f8 {
+
+constexpr int kBlock = 128;
+
+template <int T>
+constexpr float top() { return T == LQ_E4M3 ? 448.f : 57344.f; }   // 7/8 2^9, 7/8 2^16
+
+// |x|, 0 for infinities and NaN: a block's scale is that of its finite values.
+__device__ __forceinline__ float finite_magnitude(float x) {
+  const float m = fabsf(x);
+  return m < __builtin_inff() ? m : 0.f;
+}
+
+// e + 127 with e the smallest integer >= -127 such that largest <= top 2^e; 127
+// (scale 1) for a block of zeros.  largest = part 2^x with part in [1/2, 1), and
+// top = 7/8 2^9 (2^16), so e = x - 9 (16), one more where part > 7/8.  At most
+// 128 - 9 + 1 + 127 = 247.
+template <int T>
+__device__ __forceinline__ int block_exponent(float largest) {
+  const int x = __builtin_amdgcn_frexp_expf(largest);
+  const float part = __builtin_amdgcn_frexp_mantf(largest);
+  const int e = x - (T == LQ_E4M3 ? 9 : 16) + (part > 0.875f ? 1 : 0) + 127;
+  return largest > 0.f ? max(e, 0) : 127;
+}
+
+// Four values scaled by 2^(127 - byte) (exact) and rounded once, to nearest
+// even, in one word.  Finite ones lie within the type.  e4m3 has no infinity:
+// one becomes a NaN, as a NaN does.
+template <int T>
+__device__ __forceinline__ uint32_t round4(float x0, float x1, float x2, float x3, int byte) {
+  float x[4] = {x0, x1, x2, x3};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (T == LQ_E4M3) x[i] = fabsf(x[i]) < __builtin_inff() ? x[i] : __builtin_nanf("");
+    x[i] = __builtin_amdgcn_ldexpf(x[i], 127 - byte);
+  }
+  int w = 0;
+  if (T == LQ_E4M3) {
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], w, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], w, true);
+  } else {
+    w = __builtin_amdgcn_cvt_pk_bf8_f32(x[0], x[1], w, false);
+    w = __builtin_amdgcn_cvt_pk_bf8_f32(x[2], x[3], w, true);
+  }
+  return static_cast<uint32_t>(w);
+}
+
+// 2^(byte - 127) for a byte of an exponent; 255 stands for NaN.
+__device__ __forceinline__ float power_of_two(int byte) {
+  return byte == 255 ? __builtin_nanf("") : byte == 0 ? 0x1p-127f : __uint_as_float(byte << 23);
+}
+
+// Two 16-bit values of a word, or a float32.
+template <int DT>
+__device__ __forceinline__ float low16(uint32_t w) {
+  return DT == LQ_F16 ? f16_bits_to_float(static_cast<uint16_t>(w)) : __uint_as_float(w << 16);
+}
+template <int DT>
+__device__ __forceinline__ float high16(uint32_t w) {
+  return DT == LQ_F16 ? f16_bits_to_float(static_cast<uint16_t>(w >> 16))
+                      : __uint_as_float(w & 0xFFFF0000u);
+}
+
+}  // namespace f8
+}  // namespace lq

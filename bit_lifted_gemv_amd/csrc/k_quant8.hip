@@ -1,0 +1,202 @@
+// Quantization to 8-bit floating point with a power of two per 128 positions
+// of a row (lq_quant8) or per 128 x 128 block (lq_quant8_blocks):
+//   byte  = 127 + min { e : largest finite |x| of the block <= top 2^e }
+//   value = round(x 2^(127 - byte)).
+// A power of two costs no accuracy in floating point (only the range below the
+// smallest normal value, at most one binade of it), makes the division exact,
+// so that results do not depend on how it is carried out, and is what the
+// matrix instructions of the product take as a scale.
+//
+// Bound by memory: each value read once, held in registers between the maximum
+// and the rounding.
+#include "f8.h"
+#include "lq_internal.h"
+
+namespace lq {
+namespace {
+
+using namespace f8;
+
+// Eight consecutive values of a row of n from position k; zeros behind it.
+template <int DT, bool WIDE>
+__device__ __forceinline__ void load8(const void* row, int64_t k, int64_t n, float (&v)[8]) {
+  if (WIDE && k + 8 <= n) {
+    if (DT == LQ_F32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + k);
+      const float4 a = p[0], b = p[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k);
+      v[0] = low16<DT>(w.x); v[1] = high16<DT>(w.x);
+      v[2] = low16<DT>(w.y); v[3] = high16<DT>(w.y);
+      v[4] = low16<DT>(w.z); v[5] = high16<DT>(w.z);
+      v[6] = low16<DT>(w.w); v[7] = high16<DT>(w.w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = k + i < n ? load_as_float<DT>(row, k + i) : 0.f;
+}
+
+__device__ __forceinline__ float largest8(const float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_magnitude(v[i]));
+  return m;
+}
+
+template <int T>
+__device__ __forceinline__ uint2 round8(const float (&v)[8], int byte) {
+  return make_uint2(round4<T>(v[0], v[1], v[2], v[3], byte), round4<T>(v[4], v[5], v[6], v[7], byte));
+}
+
+// Rows: 16 lanes per block of 128 positions, so a wave takes 512 positions and
+// writes their four exponents as one word (rows of exponents are whole words).
+// UNITS pieces per wave, their loads on the way together.
+constexpr int kUnits = 2;
+
+template <int DT, int T, bool WIDE>
+__global__ void __launch_bounds__(256) quant8_rows_kernel(const void* __restrict__ x, int64_t units,
+                                                          int64_t K, int64_t ld, int per_row,
+                                                          uint8_t* __restrict__ q, int64_t ldq,
+                                                          uint8_t* __restrict__ exps, int64_t lde) {
+  constexpr int ESZ = DT == LQ_F32 ? 4 : 2;
+  const int lane = threadIdx.x & 63;
+  const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6)) * kUnits;
+  float v[kUnits][8];
+  int64_t row[kUnits];
+  int at[kUnits];
+#pragma unroll
+  for (int c = 0; c < kUnits; ++c) {
+    const int64_t u = min(u0 + c, units - 1);
+    row[c] = u / per_row;
+    at[c] = static_cast<int>(u - row[c] * per_row);
+    load8<DT, WIDE>(static_cast<const uint8_t*>(x) + row[c] * ld * ESZ, at[c] * int64_t{512} + lane * 8,
+                    K, v[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < kUnits; ++c) {
+    if (u0 + c >= units) return;
+    float m = largest8(v[c]);
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+    const int byte = block_exponent<T>(m);
+    const int64_t k = at[c] * int64_t{512} + lane * 8;
+    if (k < (K + 127) / 128 * 128)
+      *reinterpret_cast<uint2*>(q + row[c] * ldq + k) = round8<T>(v[c], byte);
+    uint32_t word = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+      word |= static_cast<uint32_t>(__builtin_amdgcn_readlane(byte, 16 * b)) << (8 * b);
+    if (lane == 0) *reinterpret_cast<uint32_t*>(exps + row[c] * lde + at[c] * 4) = word;
+  }
+}
+
+// Blocks: a workgroup per 128 x 128 block, eight rows of 16 lanes at a time per
+// two waves.
+template <int DT, bool WIDE>
+__global__ void __launch_bounds__(256) quant8_blocks_kernel(const void* __restrict__ w, int m,
+                                                            int64_t K, int64_t ld,
+                                                            uint8_t* __restrict__ q, int64_t ldq,
+                                                            uint8_t* __restrict__ exps, int64_t lde) {
+  constexpr int ESZ = DT == LQ_F32 ? 4 : 2;
+  __shared__ float part[4];
+  const int tid = threadIdx.x, lane = tid & 15, r0 = blockIdx.y * 128 + (tid >> 4);
+  const int64_t first = static_cast<int64_t>(blockIdx.z) * m;
+  const int64_t k = blockIdx.x * int64_t{128} + lane * 8;
+  float v[8][8];
+  float largest = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    load8<DT, WIDE>(static_cast<const uint8_t*>(w) + (first + min(r, m - 1)) * ld * ESZ, k, K, v[i]);
+    largest = fmaxf(largest, largest8(v[i]));
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) largest = fmaxf(largest, __shfl_xor(largest, d));
+  if ((tid & 63) == 0) part[tid >> 6] = largest;
+  __syncthreads();
+  const int byte = block_exponent<LQ_E4M3>(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    if (r < m) *reinterpret_cast<uint2*>(q + (first + r) * ldq + k) = round8<LQ_E4M3>(v[i], byte);
+  }
+  if (tid == 0) {
+    const int64_t strip = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
+    exps[strip * lde + blockIdx.x] = static_cast<uint8_t>(byte);
+  }
+}
+
+template <int DT, int T, bool WIDE>
+hipError_t rows(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, int64_t ldq,
+                uint8_t* exps, int64_t lde, hipStream_t st) {
+  const int per_row = static_cast<int>((K + 511) / 512);
+  constexpr int64_t most = int64_t{1} << 22;                  // workgroups of a launch
+  const int64_t rows_per = most * 4 * kUnits / per_row;
+  for (int64_t r = 0; r < n; r += rows_per) {
+    const int64_t some = n - r < rows_per ? n - r : rows_per;
+    const int64_t groups = (some * per_row + 4 * kUnits - 1) / (4 * kUnits);
+    quant8_rows_kernel<DT, T, WIDE><<<static_cast<uint32_t>(groups), 256, 0, st>>>(
+        static_cast<const uint8_t*>(x) + r * ld * (DT == LQ_F32 ? 4 : 2), some * per_row, K, ld,
+        per_row, q + r * ldq, ldq, exps + r * lde, lde);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int DT, bool WIDE>
+hipError_t by_type(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, lq_dtype type,
+                   int64_t ldq, uint8_t* exps, int64_t lde, hipStream_t st) {
+  return type == LQ_E4M3 ? rows<DT, LQ_E4M3, WIDE>(x, n, K, ld, q, ldq, exps, lde, st)
+                         : rows<DT, LQ_E5M2, WIDE>(x, n, K, ld, q, ldq, exps, lde, st);
+}
+
+// Whether rows of this type can be read in 16-byte pieces.
+bool wide(const void* x, int64_t ld, int size) {
+  return (reinterpret_cast<uintptr_t>(x) | static_cast<uint64_t>(ld) * size) % 16 == 0;
+}
+
+template <int DT>
+hipError_t blocks(const void* w, int64_t E, int64_t m, int64_t K, int64_t ld, uint8_t* q,
+                  int64_t ldq, uint8_t* exps, int64_t lde, hipStream_t st) {
+  const dim3 grid(static_cast<uint32_t>((K + 127) / 128), static_cast<uint32_t>((m + 127) / 128),
+                  static_cast<uint32_t>(E));
+  if (wide(w, ld, DT == LQ_F32 ? 4 : 2))
+    quant8_blocks_kernel<DT, true><<<grid, 256, 0, st>>>(w, static_cast<int>(m), K, ld, q, ldq, exps, lde);
+  else
+    quant8_blocks_kernel<DT, false><<<grid, 256, 0, st>>>(w, static_cast<int>(m), K, ld, q, ldq, exps, lde);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quant8(const void* x, lq_dtype dt, int64_t n, int64_t K, int64_t ld, uint8_t* q,
+                         lq_dtype type, int64_t ldq, uint8_t* exps, int64_t lde, hipStream_t st) {
+  const bool w = wide(x, ld, dt == LQ_F32 ? 4 : 2);
+  switch (dt) {
+    case LQ_F32:
+      return w ? by_type<LQ_F32, true>(x, n, K, ld, q, type, ldq, exps, lde, st)
+               : by_type<LQ_F32, false>(x, n, K, ld, q, type, ldq, exps, lde, st);
+    case LQ_F16:
+      return w ? by_type<LQ_F16, true>(x, n, K, ld, q, type, ldq, exps, lde, st)
+               : by_type<LQ_F16, false>(x, n, K, ld, q, type, ldq, exps, lde, st);
+    default:
+      return w ? by_type<LQ_BF16, true>(x, n, K, ld, q, type, ldq, exps, lde, st)
+               : by_type<LQ_BF16, false>(x, n, K, ld, q, type, ldq, exps, lde, st);
+  }
+}
+
+hipError_t launch_quant8_blocks(const void* w, lq_dtype dt, int64_t E, int64_t m, int64_t K,
+                                int64_t ld, uint8_t* q, int64_t ldq, uint8_t* exps, int64_t lde,
+                                hipStream_t st) {
+  switch (dt) {
+    case LQ_F32: return blocks<LQ_F32>(w, E, m, K, ld, q, ldq, exps, lde, st);
+    case LQ_F16: return blocks<LQ_F16>(w, E, m, K, ld, q, ldq, exps, lde, st);
+    default: return blocks<LQ_BF16>(w, E, m, K, ld, q, ldq, exps, lde, st);
+  }
+}
+
+}  // namespace lq

@@ -140,16 +140,6 @@ lq_status f6_matrices(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ld
   return LQ_OK;
 }
 
-// Outputs over what other workgroups still read.  (Rows that interleave with the
-// activations' in one buffer are fine, so only the same start is looked at.)
-lq_status f6_overlap(const void* a_lift, const void* residual, int64_t ldr, const void* out,
-                     int64_t ldo, int64_t rows) {
-  if (out == a_lift) return fail(LQ_ERR_UNSUPPORTED, "out overlaps a_lift");
-  if (out == residual && ldr != ldo && rows > 1)
-    return fail(LQ_ERR_UNSUPPORTED, "residual is out with another pitch");
-  return LQ_OK;
-}
-
 lq_status route_sizes(int64_t T, int64_t E, int32_t k) {
   if (E < 1 || E > 1024) return fail(LQ_ERR_SHAPE, "E=%lld outside 1..1024", (long long)E);
   if (T < 0 || T > INT32_MAX || k < 1 || k > 32 || k > E || T * k > INT32_MAX)
@@ -729,7 +719,7 @@ lq_status lq_gemm_ep(const uint32_t* w_packed, int64_t m, int64_t K, int64_t ldw
   if (st == LQ_OK) st = check_rows_out(residual, ldr, out, out_dtype, ldo, width, B);
   const auto plan = f6_plan(1, m, K, B, B, out_dtype, gated != 0, false, false);
   if (st == LQ_OK) st = check_workspace(workspace, workspace_bytes, plan.bytes);
-  if (st == LQ_OK) st = f6_overlap(a_lift, residual, ldr, out, ldo, B);
+  if (st == LQ_OK) st = check_overlap(a_lift, residual, ldr, out, ldo, B);
   if (st != LQ_OK) return st;
   lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, act, gated);
   p.residual = residual;
@@ -778,7 +768,7 @@ lq_status lq_gemm_grouped(const uint32_t* w_packed, int64_t E, int64_t m, int64_
   if (st == LQ_OK) st = check_rows_out(nullptr, 0, out, out_dtype, ldo, width, R);
   const auto plan = f6_plan(E, m, K, a_rows, R, out_dtype, gated != 0, true, false);
   if (st == LQ_OK) st = check_workspace(workspace, workspace_bytes, plan.bytes);
-  if (st == LQ_OK) st = f6_overlap(a_lift, nullptr, 0, out, ldo, R);
+  if (st == LQ_OK) st = check_overlap(a_lift, nullptr, 0, out, ldo, R);
   if (st != LQ_OK) return st;
   lq::F6Product p = f6_product(w_packed, m, ldw, s, bias, act, gated);
   p.out = out;
@@ -824,7 +814,7 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
   if (st == LQ_OK) st = check_rows_out(residual, ldr, out, out_dtype, ldo, m, T);
   const auto plan = f6_plan(E, m, K, R, R, out_dtype, false, true, true);
   if (st == LQ_OK) st = check_workspace(workspace, workspace_bytes, plan.bytes);
-  if (st == LQ_OK) st = f6_overlap(nullptr, residual, ldr, out, ldo, T);  // out is written last
+  if (st == LQ_OK) st = check_overlap(nullptr, residual, ldr, out, ldo, T);  // out is written last
   if (st != LQ_OK) return st;
   const hipStream_t hs = as_stream(stream);
   float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.sums_at);

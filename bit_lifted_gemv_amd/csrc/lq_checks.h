@@ -39,13 +39,23 @@ inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 inline size_t dtype_size(lq_dtype dt) { return dt == LQ_F32 ? 4 : 2; }
 
 inline lq_status check_rows_out(const void* residual, int64_t ldr, const void* out, lq_dtype out_dtype,
-                      int64_t ldo, int64_t width, int64_t rows) {
+                                int64_t ldo, int64_t width, int64_t rows) {
   if (ldo < width && rows > 1)
     return fail(LQ_ERR_SHAPE, "ldo=%lld < %lld outputs", (long long)ldo, (long long)width);
   if (residual && ldr < width && rows > 1)
     return fail(LQ_ERR_SHAPE, "ldr=%lld < %lld outputs", (long long)ldr, (long long)width);
   if (!aligned(out, dtype_size(out_dtype)) || !aligned(residual, dtype_size(out_dtype)))
     return fail(LQ_ERR_ALIGN, "misaligned out or residual");
+  return LQ_OK;
+}
+
+// Outputs over what other workgroups still read.  (Rows that interleave with the
+// inputs' in one buffer are fine, so only the same start is looked at.)
+inline lq_status check_overlap(const void* in, const void* residual, int64_t ldr, const void* out,
+                     int64_t ldo, int64_t rows) {
+  if (out == in) return fail(LQ_ERR_UNSUPPORTED, "out overlaps the inputs");
+  if (out == residual && ldr != ldo && rows > 1)
+    return fail(LQ_ERR_UNSUPPORTED, "residual is out with another pitch");
   return LQ_OK;
 }
 

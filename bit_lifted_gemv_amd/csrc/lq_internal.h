@@ -246,4 +246,61 @@ hipError_t launch_route(const void* logits, lq_dtype dt, int64_t T, int E, int64
                         const uint8_t* valid, int k, int renorm, int* ids, float* weight, int* pos,
                         int* rows, int* offsets, void* ws, hipStream_t st);
 
+// ---------------------------------------------------------------- 8-bit floating point
+// Quantization (k_quant8.hip); rows of exps are whole words.
+hipError_t launch_quant8(const void* x, lq_dtype dt, int64_t n, int64_t K, int64_t ld, uint8_t* q,
+                         lq_dtype type, int64_t ldq, uint8_t* exps, int64_t lde, hipStream_t st);
+hipError_t launch_quant8_blocks(const void* w, lq_dtype dt, int64_t E, int64_t m, int64_t K,
+                                int64_t ld, uint8_t* q, int64_t ldq, uint8_t* exps, int64_t lde,
+                                hipStream_t st);
+
+// Arguments of the 8-bit products: lq_gemm8 (one matrix, R tokens) and
+// lq_gemm8_grouped (E matrices, ragged runs of R rows).
+struct F8Product {
+  const uint8_t* w;            // [E][m][ldw], K up to whole 128
+  int64_t ldw, w_matrix;       // bytes of a row and of a matrix
+  int m, K, steps;             // steps: blocks of 128 positions
+  const void* scales;          // [E][strips of 128 rows][lds], exponents or float32
+  int64_t lds, scales_matrix;
+  int float_scales;
+  const void* a;               // [a_rows][lda], 8-bit (K up to whole 128) or 16-bit
+  int64_t lda;
+  const uint8_t* exps;         // [a_rows][lde], of 8-bit activations
+  int64_t lde;
+  int a_rows;
+  const int* rows;             // row of `a` of each row, or null: its own
+  const int* offsets;          // [E + 1], or null: one matrix
+  int E, R;
+  const float* bias;           // [E][m] or null
+  int act, gated;
+  const void* residual;        // [R][ldr] or null
+  int64_t ldr;
+  void* out;                   // [R][ldo]
+  int64_t ldo;
+  int out_dt;
+  float* sums;                 // [slices][R][ldz] sums of the slices, or null: outputs
+  int64_t ldz;
+  int slices, slice_steps;     // of the positions
+  int row_blocks, block0;      // set by the launcher
+};
+// Few rows per matrix (k_gemv8.hip).
+struct F8FewPlan {
+  int tf, wf, waves;           // 16 tf tokens and 16 wf rows per workgroup of `waves`
+  int slices, slice_steps;
+};
+F8FewPlan few_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bool grouped);
+hipError_t launch_gemv8(const F8Product& p, int a_type, const F8FewPlan& plan, hipStream_t st);
+
+// Rows sorted by expert and back (k_rows.hip).
+hipError_t launch_sort_rows(const void* x, int size, int64_t T, int64_t n, int64_t ldx,
+                            const int* rows, int64_t R, void* out, int64_t ldo, hipStream_t st);
+hipError_t launch_join_rows(const void* z, lq_dtype dt, int64_t R, int64_t n, int64_t ldz,
+                            const int* pos, const float* weight, int64_t T, int k,
+                            const void* residual, int64_t ldr, void* out, lq_dtype out_dt,
+                            int64_t ldo, hipStream_t st);
+hipError_t launch_join_rows_grad(const void* dy, lq_dtype dt, int64_t ldy, const void* z, int64_t ldz,
+                                 int64_t R, int64_t n, const int* pos, const float* weight, int64_t T,
+                                 int k, const int* rows, void* dz, int64_t lddz, float* dweight,
+                                 hipStream_t st);
+
 }  // namespace lq

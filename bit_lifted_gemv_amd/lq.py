@@ -20,7 +20,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblq.so")
 
-LQ_F32, LQ_F16, LQ_BF16 = 0, 1, 2
+LQ_F32, LQ_F16, LQ_BF16, LQ_E4M3, LQ_E5M2, LQ_E8M0 = 0, 1, 2, 3, 4, 5
 STATUS = {0: "LQ_OK", 1: "LQ_ERR_NULL", 2: "LQ_ERR_SHAPE", 3: "LQ_ERR_DTYPE", 4: "LQ_ERR_ALIGN",
           5: "LQ_ERR_UNSUPPORTED", 6: "LQ_ERR_HIP", 7: "LQ_ERR_WORKSPACE"}
 
@@ -34,7 +34,9 @@ EXPORTS = ("lq_status_string", "lq_last_error", "lq_version", "lq_pack_signs", "
            "lq_gemv_parts_workspace_size", "lq_gemv_parts",
            "lq_gemm_ep_workspace_size", "lq_gemm_ep", "lq_route_workspace_size", "lq_route",
            "lq_gemm_grouped_workspace_size", "lq_gemm_grouped", "lq_gemm_join_workspace_size",
-           "lq_gemm_join")
+           "lq_gemm_join", "lq_quant8", "lq_quant8_blocks", "lq_gemm8_workspace_size", "lq_gemm8",
+           "lq_gemm8_grouped_workspace_size", "lq_gemm8_grouped", "lq_sort_rows", "lq_join_rows",
+           "lq_join_rows_grad")
 
 # Activations of gemm_ep and gemm_grouped.
 ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -102,6 +104,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                ctypes.POINTER(_sz)]),
         "lq_gemm_join": (_i32, [_vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _i64, _vp, _i64, _vp,
                                 _vp, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
+        "lq_quant8": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _i64, _vp]),
+        "lq_quant8_blocks": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+        "lq_gemm8_workspace_size": (_i32, [_i64, _i64, _i32, _i64, ctypes.POINTER(_sz)]),
+        "lq_gemm8": (_i32, [_vp, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _i32, _i64, _vp, _i64, _i64,
+                            _vp, _i32, _i32, _vp, _i64, _vp, _i32, _i64, _vp, _sz, _vp]),
+        "lq_gemm8_grouped_workspace_size": (_i32, [_i64, _i64, _i64, _i32, _i64, _i64,
+                                                   ctypes.POINTER(_sz)]),
+        "lq_gemm8_grouped": (_i32, [_vp, _i64, _i64, _i64, _i64, _vp, _i32, _i64, _vp, _i32, _i64,
+                                    _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i32, _vp, _i32,
+                                    _i64, _vp, _sz, _vp]),
+        "lq_sort_rows": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
+        "lq_join_rows": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp,
+                                _i32, _i64, _vp]),
+        "lq_join_rows_grad": (_i32, [_vp, _i32, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _i64, _i32,
+                                     _vp, _vp, _i64, _vp, _vp]),
         "lq_adam_update": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, ctypes.c_float,
                                   ctypes.c_float, ctypes.c_float, ctypes.c_float, _vp]),
     }
@@ -734,6 +751,321 @@ def route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None, re
                          _ptr(weight), _ptr(pos), _ptr(rows), _ptr(offsets), _ptr(ws), nb,
                          _handle(dev, stream)))
     return Routing(ids, weight, pos, rows, offsets)
+
+
+# ------------------------------------- 8-bit floating point layers
+#: The 8-bit types of quantize8 and the products.
+TYPES8 = {torch.float8_e4m3fn: LQ_E4M3, torch.float8_e5m2: LQ_E5M2}
+
+
+class Rows8(NamedTuple):
+    """Activations in 8 bits (lq_quant8): values float8_e4m3fn or float8_e5m2
+    [B][K in whole 128] and exps uint8 [B][K / 128], a power of two 2^(exps - 127)
+    for each 128 positions.  Rows of exps lie whole words apart."""
+    values: torch.Tensor
+    exps: torch.Tensor
+
+
+class Blocks8(NamedTuple):
+    """Weights in 8 bits: values float8_e4m3fn [m][K in whole 128] (zeros from K
+    on), or [E][m][..] for E matrices, and a scale for each 128 x 128 block
+    [ceil(m / 128)][K / 128] (or [E][..][..]): float32, or uint8 exponents
+    (2^(scales - 127)) whose rows lie whole words apart."""
+    values: torch.Tensor
+    scales: torch.Tensor
+
+    def transposed(self) -> "Blocks8":
+        """The weights of the gradient: m and K exchanged (laid out anew)."""
+        values = self.values.view(torch.uint8).transpose(-1, -2)
+        m = self.values.shape[-2]
+        values = torch.nn.functional.pad(values, (0, -m % 128)).contiguous().view(torch.float8_e4m3fn)
+        scales = self.scales.transpose(-1, -2)
+        if scales.dtype != torch.uint8:
+            return Blocks8(values, scales.contiguous())
+        held = _exponents(scales.shape, scales.device)
+        held.copy_(scales)
+        return Blocks8(values, held)
+
+
+def _exponents(shape, device) -> torch.Tensor:
+    """Room for exponents whose rows are whole words: a view of it."""
+    blocks = shape[-1]
+    return torch.empty((*shape[:-1], blocks + -blocks % 4), dtype=torch.uint8,
+                       device=device)[..., :blocks]
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _on_gpu(*ts: torch.Tensor) -> None:
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("tensors must live on the GPU")
+
+
+@_on_stream
+def quantize8(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, stream=None) -> Rows8:
+    """Rows x [B][K] (float32, float16 or bfloat16; rows may lie apart) in 8
+    bits with a power of two for each 128 positions (lq_quant8)."""
+    B, K = x.shape
+    dev = x.device
+    _on_gpu(x)
+    if dtype not in TYPES8:
+        raise TypeError(f"unsupported 8-bit type {dtype}")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return quantize8(x, dtype, stream)
+    ld = _pitch("x", x, (B, K))
+    values = torch.empty((B, _blocks(K) * 128), dtype=dtype, device=dev)
+    exps = _exponents((B, _blocks(K)), dev)
+    check(lib().lq_quant8(_ptr(x), _dt(x), B, K, ld, _ptr(values), TYPES8[dtype], values.shape[1],
+                          _ptr(exps), _blocks(K) + -_blocks(K) % 4, _handle(dev, stream)))
+    return Rows8(values, exps)
+
+
+@_on_stream
+def quantize8_blocks(w: torch.Tensor, stream=None) -> Blocks8:
+    """Weights w [m][K] or [E][m][K] (float32, float16 or bfloat16, contiguous) in
+    8 bits with a power of two for each 128 x 128 block (lq_quant8_blocks)."""
+    *lead, m, K = w.shape
+    dev = w.device
+    _on_gpu(w)
+    if len(lead) > 1:
+        raise ValueError(f"w has shape {tuple(w.shape)}, not [m][K] or [E][m][K]")
+    if not w.is_contiguous():
+        raise ValueError("w must be contiguous")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return quantize8_blocks(w, stream)
+    E = lead[0] if lead else 1
+    values = torch.empty((*lead, m, _blocks(K) * 128), dtype=torch.float8_e4m3fn, device=dev)
+    scales = _exponents((*lead, _blocks(m), _blocks(K)), dev)
+    check(lib().lq_quant8_blocks(_ptr(w), _dt(w), E, m, K, K, _ptr(values), values.shape[-1],
+                                 _ptr(scales), _blocks(K) + -_blocks(K) % 4, _handle(dev, stream)))
+    return Blocks8(values, scales)
+
+
+def _exponent_pitch(name: str, t: torch.Tensor) -> int:
+    """Row pitch of exponents [..][rows][blocks], whose rows are whole words (also the
+    last one: the kernels read words)."""
+    *lead, rows, blocks = t.shape
+    held = blocks + -blocks % 4
+    if blocks > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s rows must be dense")
+    # a stride along a single element says nothing
+    pitch = t.stride(-2) if rows > 1 else held
+    if lead and lead[0] > 1:
+        if rows == 1:
+            pitch = t.stride(0)
+        elif t.stride(0) != rows * pitch:
+            raise ValueError(f"{name}'s matrices must follow one another")
+    if t.dtype == torch.uint8 and t.numel():
+        last = t.storage_offset() + (t.numel() // blocks - 1) * pitch + held
+        if pitch % 4 or last > t.untyped_storage().nbytes():
+            raise ValueError(f"{name}'s rows must be whole words (as quantize8 makes them)")
+    return pitch
+
+
+def _weights8(w: Blocks8, lead: tuple) -> Tuple[int, int]:
+    """Checks weights of [lead] matrices; their scales' type and row pitch."""
+    values, scales = w.values, w.scales
+    m, K = values.shape[-2:]
+    _plain("w.values", values, torch.float8_e4m3fn, lead + (m, K))
+    if K % 128:
+        raise ValueError(f"w.values has {K} columns, not whole 128 (zeros behind the last)")
+    shape = lead + (_blocks(m), _blocks(K))
+    if scales.dtype not in (torch.uint8, torch.float32):
+        raise TypeError(f"w.scales must be uint8 exponents or float32, not {scales.dtype}")
+    if scales.shape != shape:
+        raise ValueError(f"w.scales has shape {tuple(scales.shape)}, not {shape}")
+    kind = LQ_F32 if scales.dtype == torch.float32 else LQ_E8M0
+    return kind, _exponent_pitch("w.scales", scales)
+
+
+def _rows8(a, width: int):
+    """(tensor, type code, pitch, exponents, their pitch) of 8- or 16-bit activations for
+    weights of `width` columns; and K."""
+    if isinstance(a, Rows8):
+        values, exps = a
+        if values.dtype not in TYPES8:
+            raise TypeError(f"a.values must be float8_e4m3fn or float8_e5m2, not {values.dtype}")
+        B = values.shape[0]
+        lda = _pitch("a.values", values, (B, width))
+        _pitch("a.exps", exps, (B, width // 128), torch.uint8)
+        return values, TYPES8[values.dtype], lda, exps, _exponent_pitch("a.exps", exps), width
+    if a.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"a must be Rows8, float16 or bfloat16, not {a.dtype}")
+    B, K = a.shape
+    if _blocks(K) * 128 != width:
+        raise ValueError(f"a has {K} columns, the weights {width}")
+    return a, _dt(a), _pitch("a", a, (B, K)), None, 0, K
+
+
+def _target8(out: Optional[torch.Tensor], rows: int, width: int, out_dtype: Optional[torch.dtype],
+             a: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    if out is None and out_dtype is None and a.dtype in TYPES8:
+        out_dtype = torch.bfloat16
+    return _target(out, rows, width, out_dtype, a)
+
+
+@_on_stream
+def gemm8(w: Blocks8, a, bias: Optional[torch.Tensor] = None, act: str = "none",
+          gated: bool = False, residual: Optional[torch.Tensor] = None,
+          out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+          stream=None) -> torch.Tensor:
+    """act(a @ w^T + bias) + residual for any number of tokens (lq_gemm8).  w:
+    8-bit weights [m][K]; a: Rows8, or float16 or bfloat16 [B][K], which the
+    call quantizes (to the same result).  Epilogue as gemm_ep; out_dtype: a's,
+    bfloat16 for Rows8.  The gradient of the activations is
+    gemm8(w.transposed(), quantize8(dz, torch.float8_e5m2))."""
+    m, width = w.values.shape
+    values = a.values if isinstance(a, Rows8) else a
+    dev = values.device
+    _on_gpu(values)
+    kind, lds = _weights8(w, ())
+    _plain("bias", bias, torch.float32, (m,))
+    _same_device(dev, w=w.values, scales=w.scales, exps=a.exps if isinstance(a, Rows8) else None,
+                 bias=bias, residual=residual, out=out)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return gemm8(w, a, bias, act, gated, residual, out_dtype, out, stream)
+    values, code, lda, exps, lde, K = _rows8(a, width)
+    B = values.shape[0]
+    rows_out = m // 2 if gated else m
+    out, ldo = _target8(out, B, rows_out, out_dtype, values)
+    odt = _dt(out)
+    ldr = 0 if residual is None else _pitch("residual", residual, (B, rows_out), out.dtype)
+    nb = _bytes_needed("lq_gemm8_workspace_size", m, K, code, B)
+    ws = _temporary(nb, dev)
+    check(lib().lq_gemm8(_ptr(w.values), m, K, width, _ptr(w.scales), kind, lds, _ptr(values), code,
+                         lda, _ptr(exps), lde, B, _ptr(bias), _act(act), int(gated), _ptr(residual),
+                         ldr, _ptr(out), odt, ldo, _ptr(ws), nb, _handle(dev, stream)))
+    return out
+
+
+@_on_stream
+def gemm8_grouped(w: Blocks8, a, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                  bias: Optional[torch.Tensor] = None, act: str = "none", gated: bool = False,
+                  out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """The experts' products on ragged runs of rows (lq_gemm8_grouped): w 8-bit
+    weights [E][m][K], a as in gemm8, offsets int32 [E + 1], rows int32 [R] (which
+    row of a each sorted row is; None: its own), bias float32 [E][m].  Returns
+    out [R][m], or [R][m/2] when gated; rows outside every run are not written."""
+    E, m, width = w.values.shape
+    values = a.values if isinstance(a, Rows8) else a
+    dev = values.device
+    _on_gpu(values)
+    n_rows = values.shape[0]
+    R = n_rows if rows is None else rows.shape[0]
+    kind, lds = _weights8(w, (E,))
+    _plain("bias", bias, torch.float32, (E, m))
+    _plain("offsets", offsets, torch.int32, (E + 1,))
+    _plain("rows", rows, torch.int32, (R,))
+    _same_device(dev, w=w.values, scales=w.scales, exps=a.exps if isinstance(a, Rows8) else None,
+                 offsets=offsets, rows=rows, bias=bias, out=out)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return gemm8_grouped(w, a, offsets, rows, bias, act, gated, out_dtype, out, stream)
+    values, code, lda, exps, lde, K = _rows8(a, width)
+    out, ldo = _target8(out, R, m // 2 if gated else m, out_dtype, values)
+    odt = _dt(out)
+    nb = _bytes_needed("lq_gemm8_grouped_workspace_size", E, m, K, code, n_rows, R)
+    ws = _temporary(nb, dev)
+    check(lib().lq_gemm8_grouped(_ptr(w.values), E, m, K, width, _ptr(w.scales), kind, lds,
+                                 _ptr(values), code, lda, _ptr(exps), lde, n_rows, _ptr(rows),
+                                 _ptr(offsets), R, _ptr(bias), _act(act), int(gated), _ptr(out), odt,
+                                 ldo, _ptr(ws), nb, _handle(dev, stream)))
+    return out
+
+
+# ------------------------------------- rows sorted by expert and back
+@_on_stream
+def sort_rows(x, rows: torch.Tensor, out=None, stream=None):
+    """x [T][n] in the experts' order (lq_sort_rows): out[r] = x[rows[r]], zeros
+    where rows (int32 [R], route's) is outside [0, T).  x: float32, float16,
+    bfloat16 or an 8-bit type, or Rows8 (values and exponents go along).  The
+    gradient is join_rows(dout, pos)."""
+    if isinstance(x, Rows8):
+        _on_gpu(x.exps)
+        held = Rows8(None, None) if out is None else out
+        exps = held.exps
+        if exps is None:
+            exps = _exponents((rows.shape[0], x.exps.shape[1]), x.exps.device)
+        return Rows8(sort_rows(x.values, rows, held.values), sort_rows(x.exps, rows, exps))
+    T, n = x.shape
+    R, dev = rows.shape[0], x.device
+    _on_gpu(x)
+    size = x.element_size()
+    if size not in (1, 2, 4):
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    _plain("rows", rows, torch.int32, (R,))
+    _same_device(dev, rows=rows, out=out)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return sort_rows(x, rows, out, stream)
+    ldx = _pitch("x", x, (T, n))
+    out, ldo = _target(out, R, n, x.dtype, x)
+    check(lib().lq_sort_rows(_ptr(x), size, T, n, ldx, _ptr(rows), R, _ptr(out), ldo,
+                             _handle(dev, stream)))
+    return out
+
+
+@_on_stream
+def join_rows(z: torch.Tensor, pos: torch.Tensor, weight: Optional[torch.Tensor] = None,
+              residual: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The sorted rows z [R][n] back in the tokens' order, weighted and added
+    (lq_join_rows): out[t] = residual[t] + sum_j weight[t][j] z[pos[t][j]], pos int32
+    and weight float32 [T][k] (None: the plain sum); a position outside [0, R)
+    adds nothing.  out_dtype (default z's), also the residual's: float32, float16
+    or bfloat16; `residual` may be `out`."""
+    R, n = z.shape
+    T, k = pos.shape
+    dev = z.device
+    _on_gpu(z)
+    _plain("pos", pos, torch.int32, (T, k))
+    _plain("weight", weight, torch.float32, (T, k))
+    _same_device(dev, pos=pos, weight=weight, residual=residual, out=out)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return join_rows(z, pos, weight, residual, out_dtype, out, stream)
+    ldz = _pitch("z", z, (R, n))
+    out, ldo = _target(out, T, n, out_dtype, z)
+    ldr = 0 if residual is None else _pitch("residual", residual, (T, n), out.dtype)
+    check(lib().lq_join_rows(_ptr(z), _dt(z), R, n, ldz, _ptr(pos), _ptr(weight), T, k,
+                             _ptr(residual), ldr, _ptr(out), _dt(out), ldo, _handle(dev, stream)))
+    return out
+
+
+@_on_stream
+def join_rows_grad(dy: torch.Tensor, z: torch.Tensor, pos: torch.Tensor, weight: torch.Tensor,
+                   rows: Optional[torch.Tensor] = None, stream=None
+                   ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The gradients of join_rows with weights, from dy [T][n] (lq_join_rows_grad):
+    (dz [R][n] of z's type, dweight float32 [T][k]).  With rows (route's) the
+    rows of dz that no token has are zeros; without, every row must be named
+    in pos, for the others are not written.  The residual's gradient is dy."""
+    R, n = z.shape
+    T, k = pos.shape
+    dev = z.device
+    _on_gpu(z)
+    _plain("pos", pos, torch.int32, (T, k))
+    _plain("weight", weight, torch.float32, (T, k))
+    _plain("rows", rows, torch.int32, (R,))
+    _same_device(dev, dy=dy, pos=pos, weight=weight, rows=rows)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return join_rows_grad(dy, z, pos, weight, rows, stream)
+    ldy = _pitch("dy", dy, (T, n), z.dtype)
+    ldz = _pitch("z", z, (R, n))
+    dz = torch.empty((R, n), dtype=z.dtype, device=dev)
+    dweight = torch.empty((T, k), dtype=torch.float32, device=dev)
+    check(lib().lq_join_rows_grad(_ptr(dy), _dt(z), ldy, _ptr(z), ldz, R, n, _ptr(pos), _ptr(weight),
+                                  T, k, _ptr(rows), _ptr(dz), n, _ptr(dweight),
+                                  _handle(dev, stream)))
+    return dz, dweight
 
 
 # ----------------------------------------------------------------- layer

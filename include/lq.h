@@ -55,6 +55,10 @@ typedef int32_t lq_dtype;
 #define LQ_F32  0
 #define LQ_F16  1
 #define LQ_BF16 2
+/* Types of lq_quant8 and the 8-bit products alone (OCP 8-bit floating point). */
+#define LQ_E4M3 3  /* 4 exponent bits, 3 of fraction, largest 448, no infinity  */
+#define LQ_E5M2 4  /* 5 exponent bits, 2 of fraction, largest 57344             */
+#define LQ_E8M0 5  /* of scales: a byte b, the scale 2^(b - 127)                */
 
 /* Activations of the products with an epilogue (lq_gemm_ep, lq_gemm_grouped). */
 typedef int32_t lq_act;
@@ -535,6 +539,136 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
                        const float* weight, int64_t T, int32_t k, const void* residual,
                        int64_t ldr, void* out, lq_dtype out_dtype, int64_t ldo, void* workspace,
                        size_t workspace_bytes, void* stream);
+
+/*
+ * lq_quant8 -- rows to 8-bit floating point with a power of two for each 128
+ * positions, as the activations of lq_gemm8 are held.  With block q of a row
+ * the positions 128 q .. 128 q + 127 (those from K on are zeros) and top = 448
+ * (LQ_E4M3) or 57344 (LQ_E5M2):
+ *   exps[r][q] = 127 + the smallest e >= -127 with max |x| <= top 2^e, the
+ *                maximum over the block's finite values (127 if all are zero);
+ *   q[r][k]    = x[r][k] 2^(127 - exps[r][q]), rounded once to nearest even.
+ * A NaN stays a NaN; an infinity becomes one in LQ_E4M3 and stays in LQ_E5M2.
+ * x:    [rows] rows of K values of dtype, ld apart (any alignment of whole
+ *       values; 16-byte aligned rows are read fastest).
+ * q:    uint8 [rows][ldq], ldq >= K in whole 128, a multiple of 16, 16-byte aligned;
+ *       positions from K to the whole 128 are written as zeros.
+ * exps: uint8 [rows][lde], lde >= ceil(K / 128), a multiple of 4, 4-byte aligned;
+ *       the bytes behind the last block up to a whole word are written too.
+ * Requires 1 <= K <= 2^22, 0 <= rows < 2^31 (0 is a no-op).
+ */
+lq_status lq_quant8(const void* x, lq_dtype dtype, int64_t rows, int64_t K, int64_t ld, void* q,
+                    lq_dtype q_dtype, int64_t ldq, uint8_t* exps, int64_t lde, void* stream);
+
+/*
+ * lq_quant8_blocks -- E matrices of m rows to LQ_E4M3 with a power of two for
+ * each block of 128 rows x 128 positions, as the weights of lq_gemm8 are
+ * held: as lq_quant8 with the maximum over the block.
+ * w:    [E * m] rows of K values of dtype (LQ_F32, LQ_F16, LQ_BF16), ld apart.
+ * q:    uint8 [E * m][ldq].   exps: uint8 [E][ceil(m / 128)][lde].
+ * Conditions as lq_quant8; 1 <= E <= 1024, 1 <= m <= 2^22.
+ */
+lq_status lq_quant8_blocks(const void* w, lq_dtype dtype, int64_t E, int64_t m, int64_t K,
+                           int64_t ld, void* q, int64_t ldq, uint8_t* exps, int64_t lde,
+                           void* stream);
+
+/*
+ * lq_gemm8 -- the product of 8-bit weights with a scale for each block of 128
+ * rows x 128 positions and 8-bit activations with a power of two for each 128
+ * positions, with the epilogue of lq_gemm_ep, for any number of tokens from one:
+ *   z[b][i]   = sum_q S[i / 128][q] 2^(exps[b][q] - 127) sum_{k in block q} w[i][k] a[b][k] + bias[i]
+ *   out[b][i] = act(z[b][i]) + residual[b][i], or the gated form (lq_gemm_ep).
+ * w:       LQ_E4M3 [m][ldw], ldw >= K in whole 128, a multiple of 16, 16-byte aligned,
+ *          m * ldw < 2^31; positions from K to the whole 128 hold zeros
+ *          (lq_quant8_blocks writes them).
+ * scales:  scale_type LQ_E8M0: uint8 [ceil(m / 128)][lds], lds a multiple of 4, 4-byte
+ *          aligned; LQ_F32: float of any value, [ceil(m / 128)][lds]; lds >= ceil(K / 128).
+ * a:       [B] rows, lda apart, of a_dtype:
+ *          LQ_E4M3 or LQ_E5M2 (gradients): as lq_quant8 writes them, with exps
+ *          [B][lde]; lda a multiple of 16, 16-byte aligned, lde a multiple of 4;
+ *          LQ_F16 or LQ_BF16: K values, any lda >= K; the call quantizes them as
+ *          lq_quant8 to LQ_E4M3 (the same result bit for bit); exps is ignored.
+ * bias, act, gated, residual, out, out_dtype: as lq_gemm_ep.
+ * workspace: >= lq_gemm8_workspace_size bytes (it may be 0), 256-byte aligned,
+ *          caller-owned, no initialisation needed.
+ * Requires 1 <= K <= 2^22, B >= 1, B rows of 8-bit activations below 4 GiB.
+ * Exact products, float32 sums in a fixed order (deterministic); epilogue in
+ * float32.  A NaN in a token gives NaN in its outputs.
+ * The gradient of the activations is the same product with the transposed
+ * weights and scales (128 x 128 blocks transpose onto blocks).
+ */
+lq_status lq_gemm8_workspace_size(int64_t m, int64_t K, lq_dtype a_dtype, int64_t B,
+                                  size_t* bytes);
+lq_status lq_gemm8(const void* w, int64_t m, int64_t K, int64_t ldw, const void* scales,
+                   lq_dtype scale_type, int64_t lds, const void* a, lq_dtype a_dtype, int64_t lda,
+                   const uint8_t* exps, int64_t lde, int64_t B, const float* bias, lq_act act,
+                   int32_t gated, const void* residual, int64_t ldr, void* out,
+                   lq_dtype out_dtype, int64_t ldo, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * lq_gemm8_grouped -- the same product with one matrix per expert on ragged runs
+ * of rows: row r of the sorted order, offsets[e] <= r < offsets[e + 1], is row
+ * rows[r] of a (r itself without rows) through matrix e; an index outside
+ * [0, a_rows) counts as a row of zeros.  Rows outside every run are left as
+ * they were; runs are cut to [0, R] and read on the device.
+ * w: [E][m][ldw];  scales: [E][ceil(m / 128)][lds];  bias: float [E][m] or NULL.
+ * a: [a_rows] rows (a_rows >= R without rows).  rows: int32 [R];  offsets:
+ * int32 [E + 1], ascending;  out: [R] rows.
+ * 1 <= E <= 1024, 0 <= R < 2^31 (0 is a no-op); everything else as lq_gemm8.
+ */
+lq_status lq_gemm8_grouped_workspace_size(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype,
+                                          int64_t a_rows, int64_t R, size_t* bytes);
+lq_status lq_gemm8_grouped(const void* w, int64_t E, int64_t m, int64_t K, int64_t ldw,
+                           const void* scales, lq_dtype scale_type, int64_t lds, const void* a,
+                           lq_dtype a_dtype, int64_t lda, const uint8_t* exps, int64_t lde,
+                           int64_t a_rows, const int32_t* rows, const int32_t* offsets, int64_t R,
+                           const float* bias, lq_act act, int32_t gated, void* out,
+                           lq_dtype out_dtype, int64_t ldo, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/*
+ * lq_sort_rows -- tokens' rows in the experts' order: out[r] = x[rows[r]], zeros
+ * for an index outside [0, T) (lq_route's -1 behind the last run).  Values are
+ * moved as they are, `size` bytes each (1, 2 or 4), n to a row; x: [T] rows,
+ * ldx apart; out: [R] rows, ldo apart; rows: int32 [R].
+ * Requires 1 <= n <= 2^30, T and R < 2^31 (R == 0 is a no-op); out must not
+ * overlap x.  Its gradient is lq_join_rows without weights.
+ */
+lq_status lq_sort_rows(const void* x, int32_t size, int64_t T, int64_t n, int64_t ldx,
+                       const int32_t* rows, int64_t R, void* out, int64_t ldo, void* stream);
+
+/*
+ * lq_join_rows -- the experts' rows back in the tokens' order, weighted and added:
+ *   out[t] = residual[t] + sum_j weight[t][j] z[pos[t][j]],
+ * without weights (NULL) their plain sum.  A position outside [0, R) adds nothing.
+ * z: [R] rows of n values of dtype, ldz apart.  pos: int32 [T][k];  weight:
+ * float [T][k] or NULL.  residual: [T] rows of out_dtype, ldr apart, or NULL;
+ * it may be `out` (with ldr == ldo).  out: [T] rows of out_dtype, ldo
+ * apart; it must not overlap z.  Float32 sums over j in order, residual last.
+ * Requires 1 <= n <= 2^30, 1 <= k <= 32, 0 <= R < 2^31, T*k < 2^31 (T == 0 is a no-op).
+ */
+lq_status lq_join_rows(const void* z, lq_dtype dtype, int64_t R, int64_t n, int64_t ldz,
+                       const int32_t* pos, const float* weight, int64_t T, int32_t k,
+                       const void* residual, int64_t ldr, void* out, lq_dtype out_dtype,
+                       int64_t ldo, void* stream);
+
+/*
+ * lq_join_rows_grad -- the gradients of lq_join_rows with weights, from that of its
+ * output dy [T] rows of n:
+ *   dz[pos[t][j]] = weight[t][j] dy[t]  (rounded once),
+ *   dweight[t][j] = sum_i dy[t][i] z[pos[t][j]][i]  (0 for a position outside [0, R)).
+ * With `rows` (lq_route's, int32 [R]) the rows of dz whose rows[r] is outside
+ * [0, T) are cleared; without, rows that no pair names are left as they were.
+ * Positions of two pairs must differ, as lq_route's do.
+ * dy, z, dz: of dtype, ldy, ldz and lddz apart; dz must not overlap dy or z.
+ * dweight: float [T][k].  Float32 sums in a fixed order.  Limits as lq_join_rows
+ * (T == 0 with rows clears what they say).
+ */
+lq_status lq_join_rows_grad(const void* dy, lq_dtype dtype, int64_t ldy, const void* z, int64_t ldz,
+                            int64_t R, int64_t n, const int32_t* pos, const float* weight,
+                            int64_t T, int32_t k, const int32_t* rows, void* dz, int64_t lddz,
+                            float* dweight, void* stream);
 
 #ifdef __cplusplus
 }
