@@ -36,23 +36,24 @@ __device__ __forceinline__ float gelu(float z) {
   return z * (z < 0.f ? half_erfc : 1.f - half_erfc);
 }
 
-__device__ __forceinline__ void activate4(float (&z)[4], int act) {
+template <int N>
+__device__ __forceinline__ void activate(float (&z)[N], int act) {
   switch (act) {
     case LQ_ACT_RELU:
 #pragma unroll
-      for (int c = 0; c < 4; ++c) z[c] = z[c] < 0.f ? 0.f : z[c];     // a NaN stays one
+      for (int c = 0; c < N; ++c) z[c] = z[c] < 0.f ? 0.f : z[c];     // a NaN stays one
       break;
     case LQ_ACT_SILU:
 #pragma unroll
-      for (int c = 0; c < 4; ++c) z[c] *= sigmoid(z[c]);
+      for (int c = 0; c < N; ++c) z[c] *= sigmoid(z[c]);
       break;
     case LQ_ACT_GELU:
 #pragma unroll
-      for (int c = 0; c < 4; ++c) z[c] = gelu(z[c]);
+      for (int c = 0; c < N; ++c) z[c] = gelu(z[c]);
       break;
     case LQ_ACT_GELU_TANH:                                            // (1 + tanh u) / 2 = sigmoid(2 u)
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < N; ++c)
         z[c] *= sigmoid(1.59576912160573071f * (z[c] + 0.044715f * z[c] * z[c] * z[c]));
       break;
     default: break;

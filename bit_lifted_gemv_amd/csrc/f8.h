@@ -1,6 +1,6 @@
 // Eight-bit floating point (OCP e4m3, e5m2) with one power of two per 128
 // positions: the exponent of a block and the rounding, shared by the kernels
-// that quantize (k_quant8.hip, k_gemv8.hip).
+// that quantize (k_quant8.hip, k_gemv8.hip), and the way to bfloat16.
 #pragma once
 
 #include "lq_internal.h"
@@ -53,9 +53,32 @@ __device__ __forceinline__ uint32_t round4(float x0, float x1, float x2, float x
   return static_cast<uint32_t>(w);
 }
 
-// 2^(byte - 127) for a byte of an exponent; 255 stands for NaN.
-__device__ __forceinline__ float power_of_two(int byte) {
-  return byte == 255 ? __builtin_nanf("") : byte == 0 ? 0x1p-127f : __uint_as_float(byte << 23);
+// 2^(byte - 127) for a byte of an exponent (0: a subnormal); 255 stands for NaN.
+__device__ __forceinline__ float power_of_two(uint32_t byte) {
+  return __uint_as_float(max(byte << 23, 0x00400000u) | (byte + 1) >> 8 << 22);
+}
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Eight 8-bit values times 2^(byte - 127) in bfloat16.
+template <int T>
+__device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  bf16x8 v;
+  const int w[2] = {lo, hi};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    bf16x2 a, b;
+    if (T == LQ_E5M2) {
+      a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w[i], scale, false);
+      b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w[i], scale, true);
+    } else {
+      a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, false);
+      b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, true);
+    }
+    v[4 * i] = a[0]; v[4 * i + 1] = a[1]; v[4 * i + 2] = b[0]; v[4 * i + 3] = b[1];
+  }
+  return v;
 }
 
 // Two 16-bit values of a word, or a float32.

@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(128) f6_reduce_kernel(F6Product a) {
   float y[4] = {}, up[4] = {};
   sum(o, y);
   if (a.gated) sum(out_m + o, up);
-  activate4(y, a.act);
+  activate(y, a.act);
   if (a.gated) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] *= up[j];

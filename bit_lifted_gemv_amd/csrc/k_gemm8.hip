@@ -1,0 +1,486 @@
+// Product of 8-bit weights (e4m3, a scale per 128 x 128 block) with many rows of
+// 8-bit activations (a power of two per 128 positions), on the matrix cores, with
+// the epilogue of lq_gemm8 and the ragged expert runs of lq_gemm8_grouped.
+//
+// Tile.  WT x WW waves, each 16 FT tokens x 16 FW rows of weights in tiles of 16 x 16:
+// v_mfma_scale_f32_16x16x128_f8f6f4 takes a whole block of 128 positions, so a
+// float32 scale of the block costs four multiply-adds per product (a lane's sums
+// are of one row of weights).  Operands come to LDS by loads that write it
+// directly, in stages of 128 positions (a ring of S); 16-byte piece c of row r
+// lies at piece c ^ (r / 2 % 8), so that 16 lanes reading one piece of 16 rows
+// touch every bank once.
+//
+// A wave holds a stage's rows and a ring of four token tiles; each is refilled from
+// LDS as soon as its last product has been issued.  Where the refills pass to the
+// next stage, one barrier says both that it has landed and that this one's place
+// in the ring may be loaded again.
+//
+// The waits are counted by hand (the compiler would drain the loads before every
+// read of LDS): every wave issues the same number of loads per stage.
+#include "f6_epilogue.h"
+#include "f6_product.h"
+#include "f8.h"
+#include "lq_internal.h"
+
+namespace lq {
+namespace {
+
+using namespace f6;
+using namespace f8;
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// 64 lanes x 16 (or 4) bytes from resource r at voff + soff to LDS at `lds` (bytes).
+__device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t voff, const i32x4& r, uint32_t soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+      : "memory");
+}
+__device__ __forceinline__ void load_word_to_lds(uint32_t lds, uint32_t voff, const i32x4& r, uint32_t soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(r), "s"(soff)
+      : "memory");
+}
+
+template <class T>
+__device__ __forceinline__ T lds_read(uint32_t at, int offset) {
+  const auto* base = reinterpret_cast<const __attribute__((address_space(3))) char*>(at);
+  return *reinterpret_cast<const __attribute__((address_space(3))) T*>(base + offset);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_and_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ i32x4 resource(const void* p, int64_t bytes) {
+  const uint64_t u = reinterpret_cast<uint64_t>(p);
+  i32x4 r;
+  r[0] = uniform(static_cast<int>(u));
+  r[1] = uniform(static_cast<int>(u >> 32) & 0xFFFF);
+  r[2] = uniform(static_cast<int>(bytes > 0xFFFFFFFF ? 0xFFFFFFFF : bytes));
+  r[3] = 0x00020000;
+  return r;
+}
+
+// Q: rows of a matrix-core tile, 16 (stages of 128 positions) or 32 (of 64).
+template <int Q, int WT, int WW, int WK, int FT, int FW>
+struct Tile {
+  static constexpr int GROUP = WT * WW, NW = GROUP * WK;        // waves
+  static constexpr int TOK = Q * FT * WT, ROWS = Q * FW * WW;
+  static constexpr int KS = Q == 16 ? 128 : 64, CH = KS / 16;   // a row's bytes and pieces per stage
+  static constexpr int PER = 64 / CH;                           // rows of a 1 KB load
+  static constexpr int IL = TOK / PER / GROUP, WL = ROWS / PER / GROUP;   // loads per wave and stage
+  static constexpr int LOADS = IL + WL + 1;
+  // a stage: tokens, rows and the rows' scales; behind the ring the tokens' exponents, whose words
+  // hold four blocks (two of them, in turn), and a place that nobody reads
+  static constexpr int ROWS_AT = TOK * KS, SCALES_AT = ROWS_AT + ROWS * KS, STAGE = SCALES_AT + ROWS * 4;
+  static constexpr int BEHIND = 2 * TOK * 4 + 256;
+  static constexpr int PER_SIMD = 2;                            // waves, of up to 256 registers
+  static constexpr int MAX_LDS = 163840 / (PER_SIMD * 4 / NW);  // workgroups of a compute unit
+  static constexpr int RING = (MAX_LDS / WK - BEHIND) / STAGE, S = RING > 4 ? 4 : RING;
+  static constexpr int PART = S * STAGE + BEHIND, LDS = WK * PART;   // of a group, of all
+  static constexpr int PITCH = Q * FW + 4, AT_ONCE = Q == 16 ? 2 : 1;   // of the sums on their way out
+  static_assert(NW * AT_ONCE * Q * PITCH * 4 <= LDS);
+  static_assert(WK <= 2 && S >= 2 && TOK >= 64 && ROWS >= 64 && FT >= 4 && S * LOADS < 64);
+  static_assert(TOK / 64 + ROWS / 64 <= GROUP);                 // one wave for each 64 exponents or scales
+  static_assert(WK == 1 || GROUP * FT * FW * Q * Q * 4 <= LDS); // the groups' sums change hands there
+};
+
+template <int AK, bool FS, bool PREC, int Q, int WT, int WW, int WK, int FT, int FW>
+__global__ void __launch_bounds__(64 * WT * WW * WK, (Tile<Q, WT, WW, WK, FT, FW>::PER_SIMD))
+gemm8_kernel(F8Product p) {
+  using P = Tile<Q, WT, WW, WK, FT, FW>;
+  constexpr int TOK = P::TOK, ROWS = P::ROWS, GROUP = P::GROUP, S = P::S, KS = P::KS, NR = Q * Q / 64;
+  static_assert(Q == 16 || !(FS || PREC));
+  typedef float sums __attribute__((ext_vector_type(NR)));
+  extern __shared__ __align__(1024) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63, c = lane % Q, g = lane / Q;
+  const int wave = uniform(tid >> 6), wk = wave / GROUP, wg = wave % GROUP, wt = wg % WT, ww = wg / WT;
+
+  // ---- which tile: token tiles in fours, the rows inside, so that the
+  // workgroups of an XCD (every eighth block) share both operands in its L2
+  int tiles = p.token_tiles;
+  Runs runs{};
+  if (p.offsets) {
+    tiles = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+      runs = load_runs(p, e0, tiles, TOK, lane);
+      tiles = uniform(__shfl(runs.upto, 63));
+    }
+  }
+  const int RT = p.row_blocks, total = tiles * RT * p.slices, chunk = (total + 7) / 8;
+  const int block = p.block0 + static_cast<int>(blockIdx.x);
+  if (block >> 3 >= chunk) return;
+  const int at = (block & 7) * chunk + (block >> 3);
+  if (at >= total) return;
+  const int slice = p.slices == 1 ? 0 : at / (tiles * RT), here = at - slice * tiles * RT;
+  const int four = here / (4 * RT), in = here - four * 4 * RT, wide4 = min(4, tiles - 4 * four);
+  const int tile = 4 * four + in % wide4, rt = in / wide4;
+  int expert = 0, row0 = tile * TOK, row_end = p.R;
+  if (p.offsets) {
+    const bool found = p.E <= 64 ? find_in(runs, 0, tile, TOK, expert, row0, row_end)
+                                 : find_run(p, tile, TOK, lane, expert, row0, row_end);
+    if (!found) return;
+  }
+  const int tokens = min(TOK, row_end - row0);
+  const int half = p.m / 2, out_m = p.gated ? half : p.m;
+  const int out0 = rt * (p.gated ? ROWS / 2 : ROWS);
+
+  // ---- sources of this wave's loads.  Of a wave's FW row tiles the first half are the
+  // gate's and the others the up rows of the same outputs.
+  auto weight_row = [&](int lr) {
+    if (!p.gated) return min(out0 + lr, p.m - 1);
+    const int w = lr / (Q * FW), j = lr / Q % FW;
+    return min(out0 + w * (Q / 2) * FW + j % (FW / 2) * Q + lr % Q, half - 1) + (j < FW / 2 ? 0 : half);
+  };
+  auto token_row = [&](int lt) {
+    int r = row0 + min(lt, tokens - 1);
+    if (p.rows) {
+      r = p.rows[r];
+      r = r < 0 || r >= p.a_rows ? 0 : r;                // its sums are dropped below
+    }
+    return r;
+  };
+  const int64_t strips = (p.m + 127) / 128;
+  const i32x4 ares = resource(p.a, p.a_rows * p.lda), eres = resource(p.exps, p.a_rows * p.lde);
+  const i32x4 wres = resource(p.w + expert * p.w_matrix, p.w_matrix);
+  const i32x4 sres = resource(static_cast<const uint8_t*>(p.scales) + expert * p.scales_matrix * (FS ? 4 : 1),
+                              strips * p.lds * (FS ? 4 : 1));
+  uint32_t a_src[P::IL], w_src[P::WL];
+  // where piece x of row r of a tile lies, 16 lanes reading one piece of 16 rows apart
+  auto place = [](int r, int x) { return x ^ (Q == 16 ? r >> 1 & 7 : r >> 2 & 3); };
+#pragma unroll
+  for (int i = 0; i < P::IL; ++i) {
+    const int lt = P::PER * (wg + GROUP * i) + lane / P::CH;
+    a_src[i] = static_cast<uint32_t>(token_row(lt)) * static_cast<uint32_t>(p.lda) + 16 * place(lt, lane % P::CH);
+  }
+#pragma unroll
+  for (int i = 0; i < P::WL; ++i) {
+    const int lr = P::PER * (wg + GROUP * i) + lane / P::CH;
+    w_src[i] = static_cast<uint32_t>(weight_row(lr)) * static_cast<uint32_t>(p.ldw) + 16 * place(lr, lane % P::CH);
+  }
+  // wave w of a group loads the exponents of 64 tokens, the scales of 64 rows, or nothing
+  constexpr int EW = TOK / 64, SW = ROWS / 64;
+  const uint32_t small_src =
+      wg < EW ? static_cast<uint32_t>(token_row(64 * wg + lane)) * static_cast<uint32_t>(p.lde)
+      : wg < EW + SW ? static_cast<uint32_t>(weight_row(64 * (wg - EW) + lane) / 128) *
+                           static_cast<uint32_t>(p.lds) * (FS ? 4u : 1u)
+                     : 0u;
+  // this group's stages: every WK-th from wk of the slice's
+  constexpr int PER_BLOCK = 128 / KS;
+  const int step0 = slice * p.slice_steps * PER_BLOCK;
+  const int steps = min(p.slice_steps, p.steps - slice * p.slice_steps) * PER_BLOCK;
+  const int most = (steps + WK - 1) / WK, mine = (steps + WK - 1 - wk) / WK;
+  const uint32_t lds0 = lds_address(lds) + wk * P::PART;
+  auto step_of = [&](int n) { return step0 + min(n * WK + wk, steps - 1); };
+  // past the end: the last one again, into a place that nobody reads
+  auto issue = [&](int n, int slot) {
+    const int st = step_of(n), q = st / PER_BLOCK;
+    const uint32_t base = lds0 + slot * P::STAGE;
+#pragma unroll
+    for (int i = 0; i < P::IL; ++i)
+      load_to_lds(base + (wg + GROUP * i) * 1024, a_src[i], ares, st * KS);
+#pragma unroll
+    for (int i = 0; i < P::WL; ++i)
+      load_to_lds(base + P::ROWS_AT + (wg + GROUP * i) * 1024, w_src[i], wres, st * KS);
+    // every lane of an exponent load touches a line of its own: only when a new word begins
+    const bool scales = wg >= EW && wg < EW + SW;
+    const bool fresh = n == 0 || q >> 2 != (st - WK) / PER_BLOCK >> 2;
+    const uint32_t to = scales ? base + P::SCALES_AT + (wg - EW) * 256
+                        : wg < EW && fresh ? lds0 + S * P::STAGE + (q >> 2 & 1) * TOK * 4 + wg * 256
+                                           : lds0 + S * P::STAGE + 2 * TOK * 4;
+    if (scales) load_word_to_lds(to, small_src, sres, FS ? q * 4 : q & ~3);
+    else load_word_to_lds(to, wg < EW && fresh ? small_src : 0u, eres, q & ~3);
+  };
+
+  // ---- operands: all row tiles, and a ring of four token tiles
+  sums acc[FT][FW] = {};
+  i32x8 a[4], b[FW];
+  uint32_t ea[4], sb[FW];                                // exponents, still in words
+  f32x4 sf[FS ? FW : 1];                                 // float32 scales of a lane's four rows
+  // A lane's places in LDS; those of the ring move on with the stage that is read,
+  // tiles are immediate offsets from them.
+  uint32_t a_at[2], b_at[2], s_at, e_at;
+  {
+    const uint32_t at = c * KS + 16 * place(c, g);
+    a_at[0] = lds0 + wt * Q * FT * KS + at;
+    b_at[0] = lds0 + P::ROWS_AT + ww * Q * FW * KS + at;
+    a_at[1] = a_at[0] ^ KS / 2;                          // (every other part is a multiple of KS)
+    b_at[1] = b_at[0] ^ KS / 2;
+    s_at = lds0 + P::SCALES_AT + (ww * Q * FW + (FS ? 4 * g : c)) * 4;
+  }
+  const uint32_t e0_at = lds0 + S * P::STAGE + (wt * Q * FT + c) * 4;
+  auto exponents_of = [&](int n) { e_at = e0_at + (step_of(n) / PER_BLOCK >> 2 & 1) * TOK * 4; };
+  auto a_moves = [&](uint32_t by) { a_at[0] += by; a_at[1] += by; };
+  auto b_moves = [&](uint32_t by) { b_at[0] += by; b_at[1] += by; s_at += by; };
+  auto read_tile = [&](const uint32_t (&at)[2], int offset, i32x8& v) {
+    const i32x4 lo = lds_read<i32x4>(at[0], offset), hi = lds_read<i32x4>(at[1], offset);
+    v[0] = lo[0]; v[1] = lo[1]; v[2] = lo[2]; v[3] = lo[3];
+    v[4] = hi[0]; v[5] = hi[1]; v[6] = hi[2]; v[7] = hi[3];
+  };
+  auto read_a = [&](int f) {
+    read_tile(a_at, f * Q * KS, a[f % 4]);
+    ea[f % 4] = lds_read<uint32_t>(e_at, f * Q * 4);
+  };
+  auto read_b = [&](int f) {
+    read_tile(b_at, f * Q * KS, b[f]);
+    if constexpr (FS) sf[f] = lds_read<f32x4>(s_at, f * Q * 4);
+    else sb[f] = lds_read<uint32_t>(s_at, f * Q * 4);
+  };
+  bf16x8 wb[PREC ? FW : 1][4];
+  // a stage's exponents of the rows out of their words, and its rows in bfloat16
+  auto begin = [&](int shift) {
+    if constexpr (!FS) {
+#pragma unroll
+      for (int j = 0; j < FW; ++j) sb[j] >>= shift;
+    }
+    if constexpr (PREC) {
+#pragma unroll
+      for (int j = 0; j < FW; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          wb[j][i] = widen8<LQ_E4M3>(b[j][2 * i], b[j][2 * i + 1],
+                                     FS ? 1.f : power_of_two(sb[j] & 255));
+    }
+  };
+  // The products of token tile t; `after(j)` follows that with row tile j.
+  auto products = [&](int t, int shift, auto&& after) {
+    const uint32_t e = ea[t % 4] >> shift;
+    bf16x8 wa[4];
+    if constexpr (PREC) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        wa[i] = widen8<AK>(a[t % 4][2 * i], a[t % 4][2 * i + 1], power_of_two(e & 255));
+    }
+#pragma unroll
+    for (int j = 0; j < FW; ++j) {
+      sums& to = acc[t][j];
+      constexpr int B = AK == LQ_E5M2 ? 1 : 0;
+      if constexpr (PREC) {
+        f32x4 z = FS ? f32x4{} : to;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][i], wa[i], z, 0, 0, 0);
+        to = FS ? to + z * sf[j] : z;
+      } else if constexpr (FS) {
+        const f32x4 z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[t % 4], f32x4{}, 0, B, 0, 127, 0, e);
+        to += z * sf[j];
+      } else if constexpr (Q == 32) {
+        to = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[j], a[t % 4], to, 0, B, 0, sb[j], 0, e);
+      } else {
+        to = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[t % 4], to, 0, B, 0, sb[j], 0, e);
+      }
+      after(j);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+#pragma unroll
+  for (int i = 0; i < S; ++i) issue(i, i);
+  wait_and_barrier<(S - 1) * P::LOADS>();
+  exponents_of(0);
+#pragma unroll
+  for (int i = 0; i < FW; ++i) read_b(i);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) read_a(i);
+  // The scheduling barriers keep the order: a token tile's products, then the reads
+  // that refill its place, four tiles ahead of their use.  The last stage refills
+  // nothing; a group without one skips it.
+  int slot = 0;
+  for (int n = 0; n + 1 < most; ++n) {
+    const int next = slot + 1 == S ? 0 : slot + 1, shift = 8 * (step_of(n) / PER_BLOCK & 3);
+    const uint32_t on = static_cast<uint32_t>((next - slot) * P::STAGE);
+    begin(shift);
+#pragma unroll
+    for (int t = 0; t < FT; ++t) {
+      products(t, shift, [&](int j) {
+        if (t == FT - 1) {
+          __builtin_amdgcn_sched_barrier(0);
+          read_b(j);
+        }
+      });
+      if (t == FT - 4) {
+        // the next stage has landed and nobody reads this one's place any more
+        wait_and_barrier<(S - 2) * P::LOADS>();
+        issue(n + S, slot);
+        a_moves(on);
+        b_moves(on);
+        exponents_of(n + 1);
+      }
+      read_a((t + 4) % FT);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    slot = next;
+  }
+  if (WK == 1 || mine == most) {
+    const int shift = 8 * (step_of(most - 1) / PER_BLOCK & 3);
+    begin(shift);
+#pragma unroll
+    for (int t = 0; t < FT; ++t) {
+      products(t, shift, [](int) {});
+      if (t + 4 < FT) read_a(t + 4);
+    }
+  }
+
+  // ---- the groups' halves change hands: each finishes half of the token tiles
+  constexpr int LAST = WK == 1 ? FT : FT / 2;
+  if constexpr (WK == 2) {
+    wait_and_barrier<0>();
+    sums* ex = reinterpret_cast<sums*>(lds) + lane;
+    auto slot_of = [&](int group, int t, int j) { return ((group * GROUP + wg) * LAST + t) * FW + j; };
+#pragma unroll
+    for (int t = 0; t < LAST; ++t)
+#pragma unroll
+      for (int j = 0; j < FW; ++j)
+        ex[slot_of(1 - wk, t, j) * 64] = wk ? acc[t][j] : acc[LAST + t][j];
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < LAST; ++t)
+#pragma unroll
+      for (int j = 0; j < FW; ++j) {
+        const sums other = ex[slot_of(wk, t, j) * 64];
+        acc[t][j] = wk ? other + acc[LAST + t][j] : acc[t][j] + other;
+      }
+  }
+
+  // ---- the end: two token tiles at a time through the wave's own part of LDS, [token][row],
+  // so that its loop over them is short (unrolled over the sums' registers it would be 100 KB of
+  // code, fetched once per tile: 15 us of each instead of 5) and its stores are whole runs
+  constexpr int PITCH = P::PITCH, AT_ONCE = P::AT_ONCE;
+  if constexpr (WK == 1) wait_and_barrier<0>();
+  else __syncthreads();
+  float* ex = reinterpret_cast<float*>(lds) + wave * AT_ONCE * Q * PITCH;
+  const int rows_out = p.gated ? Q * FW / 2 : Q * FW, quads = rows_out / 4;
+  const int o_wave = out0 + ww * rows_out;
+  const OutputTypes types = output_types(p.out, p.ldo, p.residual, p.ldr, p.out_dt);
+  const float* bias = p.bias && slice == 0 ? p.bias + static_cast<int64_t>(expert) * p.m : nullptr;
+  const int wave_token = wt * Q * FT + (WK == 2 && wk ? Q * LAST : 0);
+#pragma unroll
+  for (int f0 = 0; f0 < LAST; f0 += AT_ONCE) {
+#pragma unroll
+    for (int t = 0; t < AT_ONCE; ++t)
+#pragma unroll
+      for (int j = 0; j < FW; ++j)
+#pragma unroll
+        for (int x = 0; x < NR / 4; ++x)
+          *reinterpret_cast<f32x4*>(ex + (Q * t + c) * PITCH + Q * j + 8 * x + 4 * g) =
+              f32x4{acc[f0 + t][j][4 * x], acc[f0 + t][j][4 * x + 1], acc[f0 + t][j][4 * x + 2], acc[f0 + t][j][4 * x + 3]};
+#pragma unroll 1
+    for (int x = lane; x < AT_ONCE * Q * quads; x += 64) {
+      const int at_token = x / quads, o_in = x % quads * 4, o = o_wave + o_in, n = min(4, out_m - o);
+      const int token = wave_token + Q * f0 + at_token;
+      if (token >= tokens || n <= 0) continue;
+      const int64_t row = row0 + token, out_row = row + static_cast<int64_t>(slice) * p.R;
+      const Residual res = load_residual(n, types, p.residual, row * p.ldr + o);
+      bool live = true;
+      if (p.rows) {
+        const int r = p.rows[row];
+        live = r >= 0 && r < p.a_rows;
+      }
+      const float* from = ex + at_token * PITCH + o_in;
+      auto finished = [&](const float* z4, int o_bias, float (&y)[4]) {
+        const f32x4 z = *reinterpret_cast<const f32x4*>(z4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = live ? z[i] : 0.f;
+        if (bias) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < n) y[i] += bias[o_bias + i];
+        }
+      };
+      float y[4], up[4];
+      finished(from, o, y);
+      activate(y, p.act);
+      if (p.gated) {
+        finished(from + Q * FW / 2, half + o, up);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] *= up[i];
+      }
+      store4(y, n, types, res, p.residual != nullptr, p.out, out_row * p.ldo + o);
+    }
+  }
+}
+
+template <int AK, bool FS, bool PREC, int Q, int WT, int WW, int WK, int FT, int FW>
+hipError_t launch(const F8Product& in, hipStream_t st) {
+  using P = Tile<Q, WT, WW, WK, FT, FW>;
+  F8Product p = in;
+  const int64_t outs = p.gated ? P::ROWS / 2 : P::ROWS, out_m = p.gated ? p.m / 2 : p.m;
+  p.row_blocks = static_cast<int>((out_m + outs - 1) / outs);
+  int64_t tiles = (p.R + P::TOK - 1) / P::TOK;
+  if (p.offsets) tiles = p.R / P::TOK + (p.E < p.R ? p.E : p.R);
+  p.token_tiles = static_cast<int>(tiles);
+  const int64_t grid = (tiles * p.row_blocks * p.slices + 7) / 8 * 8;
+  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  auto* k = gemm8_kernel<AK, FS, PREC, Q, WT, WW, WK, FT, FW>;
+  // per call: the attribute belongs to the current device
+  const hipError_t big = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, P::LDS);
+  if (big != hipSuccess) return big;
+  // a launch has fewer than 2^32 threads
+  constexpr int64_t kMost = (int64_t{1} << 31) / (64 * P::NW);
+  for (int64_t b = 0; b < grid; b += kMost) {
+    p.block0 = static_cast<int>(b);
+    k<<<static_cast<uint32_t>(grid - b < kMost ? grid - b : kMost), 64 * P::NW, P::LDS, st>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int AK, bool FS>
+hipError_t by_shape(const F8Product& p, const F8ManyPlan& plan, bool precise, hipStream_t st) {
+  if (precise) return plan.big ? launch<AK, FS, true, 16, 4, 2, 1, 4, 4>(p, st) : launch<AK, FS, true, 16, 2, 2, 2, 4, 4>(p, st);
+  if (!plan.big) return launch<AK, FS, false, 16, 2, 2, 2, 4, 4>(p, st);
+  if constexpr (FS) return launch<AK, FS, false, 16, 4, 2, 1, 4, 4>(p, st);
+  else return launch<AK, FS, false, 16, 2, 4, 1, 8, 4>(p, st);
+}
+
+template <int AK>
+hipError_t by_scales(const F8Product& p, const F8ManyPlan& plan, bool precise, hipStream_t st) {
+  return p.float_scales ? by_shape<AK, true>(p, plan, precise, st) : by_shape<AK, false>(p, plan, precise, st);
+}
+
+}  // namespace
+
+F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bool grouped,
+                        bool float_scales, bool precise) {
+  F8ManyPlan p{};
+  const int64_t cus = num_cus(), steps = (K + 127) / 128;
+  const int64_t runs = grouped ? (E < R ? E : R) : 1, out_m = gated ? m / 2 : m;
+  auto count = [&](int tok, int rows) {
+    const int64_t outs = gated ? rows / 2 : rows;
+    const int64_t tiles = grouped ? R / tok + (runs + 1) / 2 : (R + tok - 1) / tok;
+    return tiles * ((out_m + outs - 1) / outs);
+  };
+  p.big = count(256, precise ? 128 : 256) >= cus;
+  p.slices = 1;
+  const int64_t tiles = count(128, 128);
+  if (!p.big && tiles < cus) {
+    p.slices = static_cast<int>(cus / tiles);
+    if (p.slices > steps / 8) p.slices = static_cast<int>(steps / 8);
+    if (p.slices > 16) p.slices = 16;
+    if (p.slices < 1) p.slices = 1;
+  }
+  p.slice_steps = static_cast<int>((steps + p.slices - 1) / p.slices);
+  p.slices = static_cast<int>((steps + p.slice_steps - 1) / p.slice_steps);
+  return p;
+}
+
+hipError_t launch_gemm8(const F8Product& p, int a_type, const F8ManyPlan& plan, bool precise, hipStream_t st) {
+  return a_type == LQ_E5M2 ? by_scales<LQ_E5M2>(p, plan, precise, st) : by_scales<LQ_E4M3>(p, plan, precise, st);
+}
+
+}  // namespace lq

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
         };
         float y[4];
         scaled(sum(z), rs, y);
-        activate4(y, a.act);
+        activate(y, a.act);
         if (a.gated) {
           float g[4];
           scaled(sum(z + 64), up, g);

@@ -32,29 +32,6 @@ using namespace f8;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// Eight 8-bit values times 2^(byte - 127) in bfloat16.
-template <int T>
-__device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  bf16x8 v;
-  const int w[2] = {lo, hi};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    bf16x2 a, b;
-    if (T == LQ_E5M2) {
-      a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w[i], scale, false);
-      b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w[i], scale, true);
-    } else {
-      a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, false);
-      b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], scale, true);
-    }
-    v[4 * i] = a[0]; v[4 * i + 1] = a[1]; v[4 * i + 2] = b[0]; v[4 * i + 3] = b[1];
-  }
-  return v;
-}
-
 template <int AK, bool PREC, int TF, int WF>
 __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
   constexpr bool WIDE = AK == LQ_F16 || AK == LQ_BF16;   // 16-bit activations
@@ -270,7 +247,7 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
       }
       continue;
     }
-    activate4(y, p.act);
+    activate(y, p.act);
     if (p.gated) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] *= up[i];
@@ -318,8 +295,8 @@ hipError_t by_shape(const F8Product& p, const F8FewPlan& plan, hipStream_t st) {
 }
 
 template <int AK>
-hipError_t by_precision(const F8Product& p, const F8FewPlan& plan, hipStream_t st) {
-  return p.out_dt == LQ_F32 ? by_shape<AK, true>(p, plan, st) : by_shape<AK, false>(p, plan, st);
+hipError_t by_precision(const F8Product& p, const F8FewPlan& plan, bool precise, hipStream_t st) {
+  return precise ? by_shape<AK, true>(p, plan, st) : by_shape<AK, false>(p, plan, st);
 }
 
 }  // namespace
@@ -350,12 +327,13 @@ F8FewPlan few_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bo
   return p;
 }
 
-hipError_t launch_gemv8(const F8Product& p, int a_type, const F8FewPlan& plan, hipStream_t st) {
+hipError_t launch_gemv8(const F8Product& p, int a_type, const F8FewPlan& plan, bool precise,
+                        hipStream_t st) {
   switch (a_type) {
-    case LQ_E4M3: return by_precision<LQ_E4M3>(p, plan, st);
-    case LQ_E5M2: return by_precision<LQ_E5M2>(p, plan, st);
-    case LQ_F16: return by_precision<LQ_F16>(p, plan, st);
-    default: return by_precision<LQ_BF16>(p, plan, st);
+    case LQ_E4M3: return by_precision<LQ_E4M3>(p, plan, precise, st);
+    case LQ_E5M2: return by_precision<LQ_E5M2>(p, plan, precise, st);
+    case LQ_F16: return by_precision<LQ_F16>(p, plan, precise, st);
+    default: return by_precision<LQ_BF16>(p, plan, precise, st);
   }
 }
 

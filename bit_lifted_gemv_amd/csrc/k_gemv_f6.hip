@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
       const int o = column(rb, t), left = min(4, out_m - o);
       if (left <= 0) continue;
       float y[4] = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
-      activate4(y, a.act);
+      activate(y, a.act);
       if (a.gated) {
         const f32x4& up = acc[t + T / 2 < T ? t + T / 2 : t];
 #pragma unroll

@@ -33,8 +33,10 @@ lq_status check_quant(const void* x, lq_dtype dtype, int64_t K, int64_t ld) {
 
 // ---- the products
 struct Plan8 {
-  bool quantize;               // 16-bit activations through lq_quant8 first
+  bool few;                    // on the few-row kernel, which can quantize 16-bit activations itself
+  bool inside;                 // whether it does, where their alignment allows it
   lq::F8FewPlan fp;
+  lq::F8ManyPlan mp;
   int slices;
   int64_t ldq, lde, ldz;       // of the quantized rows, of the slices' sums
   size_t exps_at, sums_at, bytes;
@@ -54,15 +56,20 @@ lq_status check_sizes8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_
   return LQ_OK;
 }
 
+constexpr int64_t kFewRowsPerRun = 64, kInside = 16;
+
 Plan8 plan8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_t a_rows, int64_t R, bool gated,
-            bool grouped) {
+            bool grouped, bool float_scales, bool precise) {
   Plan8 p{};
-  p.quantize = is16(a_dtype);
+  const int64_t runs = grouped ? (E < R ? E : R < 1 ? 1 : R) : 1;
+  p.few = R <= kFewRowsPerRun * runs;
+  p.inside = p.few && R <= kInside * runs;
   p.fp = lq::few_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped);
-  p.slices = p.fp.slices;
+  p.mp = lq::many_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped, float_scales, precise);
+  p.slices = p.few ? p.fp.slices : p.mp.slices;
   p.ldq = whole(K);
   p.lde = (blocks(K) + 3) / 4 * 4;
-  if (p.quantize) {
+  if (is16(a_dtype)) {
     p.exps_at = round256(static_cast<size_t>(a_rows * p.ldq));
     p.bytes = p.exps_at + round256(static_cast<size_t>(a_rows * p.lde));
   }
@@ -72,11 +79,16 @@ Plan8 plan8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_t a_rows, i
   return p;
 }
 
+// What any call of these sizes needs: gated or not (an odd m has no gated form), scales
+// and outputs of either kind.
 size_t bytes8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_t a_rows, int64_t R, bool grouped) {
-  const size_t plain = plan8(E, m, K, a_dtype, a_rows, R, false, grouped).bytes;
-  if (m % 2) return plain;
-  const size_t gated = plan8(E, m, K, a_dtype, a_rows, R, true, grouped).bytes;
-  return plain > gated ? plain : gated;
+  size_t most = 0;
+  for (int kind = 0; kind < 8; ++kind) {
+    if ((kind & 1) && m % 2) continue;
+    const size_t n = plan8(E, m, K, a_dtype, a_rows, R, kind & 1, grouped, kind & 2, kind & 4).bytes;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 lq_status check_product8(const void* w, int64_t m, int64_t K, int64_t ldw, const void* scales,
@@ -93,6 +105,8 @@ lq_status check_product8(const void* w, int64_t m, int64_t K, int64_t ldw, const
   if (ldw > INT32_MAX || m * ldw > INT32_MAX)
     return fail(LQ_ERR_SHAPE, "weights of one matrix exceed the 2 GiB per-call limit");
   if (lds < blocks(K)) return fail(LQ_ERR_SHAPE, "lds=%lld < %lld", (long long)lds, (long long)blocks(K));
+  if (lds > INT32_MAX || blocks(m) * lds > (int64_t{1} << 29))
+    return fail(LQ_ERR_SHAPE, "scales of one matrix exceed the 2^29 per-call limit");
   if (ldw % 16 || !aligned(w, 16)) return fail(LQ_ERR_ALIGN, "w and ldw must be 16-byte aligned");
   if (!aligned(scales, 4) || (scale_type == LQ_E8M0 && lds % 4))
     return fail(LQ_ERR_ALIGN, "scales must be 4-byte aligned, LQ_E8M0 rows whole words");
@@ -101,8 +115,8 @@ lq_status check_product8(const void* w, int64_t m, int64_t K, int64_t ldw, const
     if (!exps) return fail(LQ_ERR_NULL, "exps is null");
     const lq_status st = check_rows8("activations", a, K, lda, exps, lde);
     if (st != LQ_OK) return st;
-    if (lda > INT64_C(0xFFFFFFFF) || a_rows * lda > INT64_C(0xFFFFFFFF))
-      return fail(LQ_ERR_SHAPE, "8-bit activations exceed the 4 GiB per-call limit");
+    if (lda > INT64_C(0xFFFFFFFF) || a_rows * lda > INT64_C(0xFFFFFFFF) || lde > lda)
+      return fail(LQ_ERR_SHAPE, "8-bit activations exceed the 4 GiB per-call limit (or lde > lda)");
   } else {
     if (lda < K) return fail(LQ_ERR_SHAPE, "lda=%lld < K=%lld", (long long)lda, (long long)K);
     if (!aligned(a, 2)) return fail(LQ_ERR_ALIGN, "misaligned activations");
@@ -120,7 +134,10 @@ hipError_t run8(lq::F8Product& p, const Plan8& plan, const void* a, lq_dtype a_d
   p.exps = exps;
   p.lde = lde;
   p.a_rows = static_cast<int>(a_rows);
-  if (plan.quantize) {
+  const bool wide = is16(a_dtype), precise = p.out_dt == LQ_F32;
+  // in the kernel where rows are whole 16-byte pieces
+  const bool inside = plan.inside && p.K % 8 == 0 && lda % 8 == 0 && aligned(a, 16);
+  if (wide && !inside) {
     const hipError_t e = lq::launch_quant8(a, a_dtype, a_rows, p.K, lda, ws, LQ_E4M3, plan.ldq,
                                            ws + plan.exps_at, plan.lde, st);
     if (e != hipSuccess) return e;
@@ -131,10 +148,24 @@ hipError_t run8(lq::F8Product& p, const Plan8& plan, const void* a, lq_dtype a_d
     type = LQ_E4M3;
   }
   p.slices = plan.slices;
-  p.slice_steps = plan.fp.slice_steps;
+  p.slice_steps = plan.few ? plan.fp.slice_steps : plan.mp.slice_steps;
   p.ldz = plan.ldz;
   p.sums = plan.slices > 1 ? reinterpret_cast<float*>(ws + plan.sums_at) : nullptr;
-  hipError_t e = lq::launch_gemv8(p, type, plan.fp, st);
+  hipError_t e;
+  if (plan.few) {
+    e = lq::launch_gemv8(p, type, plan.fp, precise, st);
+  } else {
+    lq::F8Product q = p;
+    if (p.sums) {                          // plain rows, in their own order
+      q.act = LQ_ACT_NONE;
+      q.gated = 0;
+      q.residual = nullptr;
+      q.out = p.sums;
+      q.ldo = p.ldz;
+      q.out_dt = LQ_F32;
+    }
+    e = lq::launch_gemm8(q, type, plan.mp, precise, st);
+  }
   if (e == hipSuccess && p.sums) {
     lq::F6Product q{};                     // what the reduction reads of it
     q.m = p.m;
@@ -237,7 +268,8 @@ lq_status lq_gemm8(const void* w, int64_t m, int64_t K, int64_t ldw, const void*
                       gated, out_dtype);
   if (st == LQ_OK) st = check_rows_out(residual, ldr, out, out_dtype, ldo, gated ? m / 2 : m, B);
   if (st != LQ_OK) return st;
-  const Plan8 plan = plan8(1, m, K, a_dtype, B, B, gated != 0, false);
+  const Plan8 plan = plan8(1, m, K, a_dtype, B, B, gated != 0, false, scale_type == LQ_F32,
+                           out_dtype == LQ_F32);
   st = check_workspace(workspace, workspace_bytes, plan.bytes);
   if (st == LQ_OK) st = check_overlap(a, residual, ldr, out, ldo, B);
   if (st != LQ_OK) return st;
@@ -278,7 +310,8 @@ lq_status lq_gemm8_grouped(const void* w, int64_t E, int64_t m, int64_t K, int64
                       act, gated, out_dtype);
   if (st == LQ_OK) st = check_rows_out(nullptr, 0, out, out_dtype, ldo, gated ? m / 2 : m, R);
   if (st != LQ_OK) return st;
-  const Plan8 plan = plan8(E, m, K, a_dtype, a_rows, R, gated != 0, true);
+  const Plan8 plan = plan8(E, m, K, a_dtype, a_rows, R, gated != 0, true, scale_type == LQ_F32,
+                           out_dtype == LQ_F32);
   st = check_workspace(workspace, workspace_bytes, plan.bytes);
   if (st == LQ_OK) st = check_overlap(a, nullptr, 0, out, ldo, R);
   if (st != LQ_OK) return st;

@@ -281,7 +281,7 @@ struct F8Product {
   float* sums;                 // [slices][R][ldz] sums of the slices, or null: outputs
   int64_t ldz;
   int slices, slice_steps;     // of the positions
-  int row_blocks, block0;      // set by the launcher
+  int row_blocks, token_tiles, block0;      // set by the launcher
 };
 // Few rows per matrix (k_gemv8.hip).
 struct F8FewPlan {
@@ -289,7 +289,17 @@ struct F8FewPlan {
   int slices, slice_steps;
 };
 F8FewPlan few_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bool grouped);
-hipError_t launch_gemv8(const F8Product& p, int a_type, const F8FewPlan& plan, hipStream_t st);
+hipError_t launch_gemv8(const F8Product& p, int a_type, const F8FewPlan& plan, bool precise,
+                        hipStream_t st);
+// Many (k_gemm8.hip), 8-bit activations.  precise: float32 results.
+struct F8ManyPlan {
+  int big;                     // the large tile of the variant, or 128 x 128
+  int slices, slice_steps;
+};
+F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bool grouped,
+                        bool float_scales, bool precise);
+hipError_t launch_gemm8(const F8Product& p, int a_type, const F8ManyPlan& plan, bool precise,
+                        hipStream_t st);
 
 // Rows sorted by expert and back (k_rows.hip).
 hipError_t launch_sort_rows(const void* x, int size, int64_t T, int64_t n, int64_t ldx,
