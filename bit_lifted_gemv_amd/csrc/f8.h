@@ -81,7 +81,47 @@ __device__ __forceinline__ bf16x8 widen8(int lo, int hi, float scale) {
   return v;
 }
 
-// Two 16-bit values of a word, or a float32.
+// 2 N 16-bit values of a lane, lanes FIRST .. LAST apart (doubling) sharing a block, to
+// e4m3: the same as above by packed maxima and the scaled conversion, which divides
+// by a power of two and rounds once.
+template <int DT, int N, int FIRST, int LAST>
+__device__ __forceinline__ int block16(const uint32_t (&w)[N]) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  constexpr int kInf = DT == LQ_F16 ? 0x7C00 : 0x7F80;
+  u16x2 most = {0, 0};
+#pragma unroll
+  for (int i = 0; i < N; ++i) most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, w[i] & 0x7FFF7FFFu));
+  int m = max(static_cast<int>(most[0]), static_cast<int>(most[1]));
+  if (m >= kInf) {                                         // infinities and NaN do not count
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int lo = w[i] & 0x7FFF, hi = w[i] >> 16 & 0x7FFF;
+      m = max(m, max(lo < kInf ? lo : 0, hi < kInf ? hi : 0));
+    }
+  }
+#pragma unroll
+  for (int d = FIRST; d <= LAST; d *= 2) m = max(m, __shfl_xor(m, d));
+  return block_exponent<LQ_E4M3>(DT == LQ_F16 ? f16_bits_to_float(static_cast<uint16_t>(m))
+                                              : __uint_as_float(static_cast<uint32_t>(m) << 16));
+}
+template <int DT>
+__device__ __forceinline__ int round16(uint32_t lo, uint32_t hi, float scale) {
+  typedef short i16x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  i16x2 v = {0, 0};
+  if (DT == LQ_F16) {
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(v, __builtin_bit_cast(f16x2, lo), scale, false);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(v, __builtin_bit_cast(f16x2, hi), scale, true);
+  } else {
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v, __builtin_bit_cast(bf16x2, lo), scale, false);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(v, __builtin_bit_cast(bf16x2, hi), scale, true);
+  }
+  return __builtin_bit_cast(int, v);
+}
+
+// Two 16-bit values of a word
 template <int DT>
 __device__ __forceinline__ float low16(uint32_t w) {
   return DT == LQ_F16 ? f16_bits_to_float(static_cast<uint16_t>(w)) : __uint_as_float(w << 16);

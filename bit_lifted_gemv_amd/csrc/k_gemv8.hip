@@ -12,12 +12,16 @@
 // v_mfma_f32_16x16x32_bf16 keeps 24 bits.
 //
 // Bound by reading the weights: nothing of them passes through LDS.  A wave
-// takes WF x 16 rows and TF x 16 tokens, each lane loads two 16-byte pieces of
+// takes WF x 16 rows and up to 16 tokens, each lane loads two 16-byte pieces of
 // its row's block (the two halves of 64 bytes, so that a load covers whole
 // 64-byte runs of 16 rows; activations are read in the same order), and U blocks
 // are on their way at once.  The waves of a workgroup share the rows and split
-// the positions; their sums meet in LDS.  16-bit activations are quantized
-// in registers on the way (lq_quant8's result bit for bit).
+// the positions; their sums meet in LDS.
+//
+// HELD: 16-bit activations of few tokens are quantized on the way to LDS (lq_quant8's
+// result bit for bit), behind the first loads of weights, which saves the launch that
+// does it (about 4.7 us): 4096 x 4096, one token, 9.5 us (8-bit ones straight from memory
+// 8.8), four tokens 12.9 (9.2); 28672 positions of one token would cost 51 (42).
 #include "f6_epilogue.h"
 #include "f6_product.h"
 #include "f8.h"
@@ -32,12 +36,18 @@ using namespace f8;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-template <int AK, bool PREC, int TF, int WF>
+constexpr int kFewTokens = 16;
+
+__device__ __forceinline__ void wait_lds_and_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+}
+
+template <int AK, bool PREC, int WF>
 __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
-  constexpr bool WIDE = AK == LQ_F16 || AK == LQ_BF16;   // 16-bit activations
-  constexpr int TOK = 16 * TF, ROWS = 16 * WF, PITCH = ROWS + 4;
-  constexpr int U = TF * (WIDE ? 2 : 1) + WF <= 4 ? 4 : 2;
-  constexpr int AP = WIDE ? 4 : 2;                       // 16-byte pieces of a lane's activations
+  constexpr bool HELD = AK == LQ_F16 || AK == LQ_BF16;   // 16-bit activations
+  constexpr int AT = HELD ? LQ_E4M3 : AK;                // of the operand
+  constexpr int TOK = kFewTokens, ROWS = 16 * WF, PITCH = ROWS + 4;
+  constexpr int U = WF == 1 ? (HELD ? 8 : 4) : WF == 2 || HELD ? 4 : 2;   // blocks of positions on their way
   extern __shared__ __align__(16) float lds[];
   const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
@@ -68,18 +78,20 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
     srow[f] = static_cast<const uint8_t*>(p.scales) +
               (expert * p.scales_matrix + row / 128 * p.lds) * (p.float_scales ? 4 : 1);
   }
-  const uint8_t* arow[TF];
-  const uint8_t* erow[TF];
-#pragma unroll
-  for (int f = 0; f < TF; ++f) {
-    int r = row0 + min(16 * f + c16, tokens - 1);
+  auto source_row = [&](int token) {
+    int r = row0 + min(token, tokens - 1);
     if (p.rows) {
       r = p.rows[r];
       r = r < 0 || r >= p.a_rows ? 0 : r;                // its sums are dropped below
     }
-    arow[f] = static_cast<const uint8_t*>(p.a) + static_cast<int64_t>(r) * p.lda * (WIDE ? 2 : 1) +
-              (WIDE ? 32 : 16) * g;
-    erow[f] = WIDE ? nullptr : p.exps + r * p.lde;
+    return static_cast<int64_t>(r);
+  };
+  const uint8_t* arow = nullptr;
+  const uint8_t* erow = nullptr;
+  if constexpr (!HELD) {
+    const int64_t r = source_row(c16);
+    arow = static_cast<const uint8_t*>(p.a) + r * p.lda + 16 * g;
+    erow = p.exps + r * p.lde;
   }
 
   // ---- this wave's blocks of 128 positions
@@ -87,8 +99,8 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
   const int per = (s_end - s_begin + waves - 1) / waves;
   const int begin = s_begin + wave * per, end = min(begin + per, s_end);
 
-  uint4 wv[U][WF][2], av[U][TF][AP];
-  uint32_t sv[U][WF], ev[U][TF];
+  uint4 wv[U][WF][2], av[HELD ? 1 : U][2];
+  uint32_t sv[U][WF], ev[HELD ? 1 : U];
   auto load = [&](int u, int step) {
     const int64_t at = min(step, end - 1);
 #pragma unroll
@@ -98,23 +110,11 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
       wv[u][f][1] = from[4];
       sv[u][f] = p.float_scales ? reinterpret_cast<const uint32_t*>(srow[f])[at] : srow[f][at];
     }
-#pragma unroll
-    for (int f = 0; f < TF; ++f) {
-      const uint4* from = reinterpret_cast<const uint4*>(arow[f] + at * (WIDE ? 256 : 128));
-      if (WIDE) {
-        // rows hold whole 16-byte pieces: those past the end are zeros
-        const int k = static_cast<int>(at) * 128 + 16 * g;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        av[u][f][0] = k < p.K ? from[0] : zero;
-        av[u][f][1] = k + 8 < p.K ? from[1] : zero;
-        av[u][f][AP - 2] = k + 64 < p.K ? from[8] : zero;
-        av[u][f][AP - 1] = k + 72 < p.K ? from[9] : zero;
-        ev[u][f] = 0;
-      } else {
-        av[u][f][0] = from[0];
-        av[u][f][1] = from[4];
-        ev[u][f] = erow[f][at];
-      }
+    if constexpr (!HELD) {
+      const uint4* from = reinterpret_cast<const uint4*>(arow + at * 128);
+      av[u][0] = from[0];
+      av[u][1] = from[4];
+      ev[u] = erow[at];
     }
   };
   auto words = [](const uint4& lo, const uint4& hi) {
@@ -123,92 +123,92 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
     v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
     return v;
   };
+  if (begin < end) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, begin + u);
+  }
 
-  f32x4 acc[TF][WF] = {};
-  auto step = [&](int u) {
-    i32x8 a[TF];
-    int ea[TF];
-#pragma unroll
-    for (int f = 0; f < TF; ++f) {
-      if (WIDE) {
-        float v[32], largest = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 x = av[u][f][i % AP];
-          const uint32_t w4[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            v[8 * i + 2 * j] = low16<AK>(w4[j]);
-            v[8 * i + 2 * j + 1] = high16<AK>(w4[j]);
-          }
+  // ---- HELD: [token][positions of the slice], then their exponents in words
+  const int blocks = s_end - s_begin, held_pitch = blocks * 128 + 32;
+  uint8_t* held = reinterpret_cast<uint8_t*>(lds);
+  uint32_t* held_exps = reinterpret_cast<uint32_t*>(held + tokens * held_pitch);
+  if constexpr (HELD) {
+    const int l16 = tid & 15;                            // 16 lanes a block, eight values each
+    for (int x = tid >> 4; x < tokens * blocks; x += blockDim.x >> 4) {
+      const int token = x / blocks, block = x - token * blocks;
+      const int k = (s_begin + block) * 128 + l16 * 8;
+      const uint16_t* from = static_cast<const uint16_t*>(p.a) + source_row(token) * p.lda + k;
+      uint32_t w[4] = {0, 0, 0, 0};
+      if (p.pieces) {                                    // rows are whole 16-byte pieces
+        if (k < p.K) {
+          const uint4 v = *reinterpret_cast<const uint4*>(from);
+          w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) largest = fmaxf(largest, finite_magnitude(v[i]));
-        largest = fmaxf(largest, __shfl_xor(largest, 16));
-        largest = fmaxf(largest, __shfl_xor(largest, 32));
-        ea[f] = block_exponent<LQ_E4M3>(largest);
+      } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          a[f][i] = static_cast<int>(round4<LQ_E4M3>(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], ea[f]));
-      } else {
-        a[f] = words(av[u][f][0], av[u][f][1]);
-        ea[f] = static_cast<int>(ev[u][f]);
+          if (k + i < p.K) w[i / 2] |= static_cast<uint32_t>(from[i]) << (16 * (i % 2));
       }
+      const int byte = block16<AK, 4, 1, 8>(w);
+      const float scale = power_of_two(byte);
+      *reinterpret_cast<int2*>(held + token * held_pitch + block * 128 + l16 * 8) =
+          make_int2(round16<AK>(w[0], w[1], scale), round16<AK>(w[2], w[3], scale));
+      if (l16 == 0) held_exps[token * blocks + block] = byte;
     }
-    bf16x8 wide[PREC ? TF : 1][4];
-    if (PREC) {
+    wait_lds_and_barrier();
+  }
+  const int my_token = min(c16, tokens - 1);
+  const uint8_t* my_held = held + my_token * held_pitch + 16 * g;
+
+  f32x4 acc[WF] = {};
+  auto step = [&](int u, int s) {
+    i32x8 a;
+    int e;
+    if constexpr (HELD) {
+      const uint4* from = reinterpret_cast<const uint4*>(my_held + (s - s_begin) * 128);
+      a = words(from[0], from[4]);
+      e = static_cast<int>(held_exps[my_token * blocks + s - s_begin]);
+    } else {
+      a = words(av[u][0], av[u][1]);
+      e = static_cast<int>(ev[u]);
+    }
+    bf16x8 wide[4];
+    if constexpr (PREC) {
 #pragma unroll
-      for (int t = 0; t < TF; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          wide[t][i] = widen8<AK>(a[t][2 * i], a[t][2 * i + 1], power_of_two(ea[t]));
+      for (int i = 0; i < 4; ++i) wide[i] = widen8<AT>(a[2 * i], a[2 * i + 1], power_of_two(e));
     }
 #pragma unroll
     for (int f = 0; f < WF; ++f) {
       const i32x8 b = words(wv[u][f][0], wv[u][f][1]);
       const float scale = p.float_scales ? __uint_as_float(sv[u][f]) : power_of_two(sv[u][f]);
-      bf16x8 wb[4];
-      if (PREC) {
+      f32x4 z = {};
+      if constexpr (PREC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) wb[i] = widen8<LQ_E4M3>(b[2 * i], b[2 * i + 1], 1.f);
+        for (int i = 0; i < 4; ++i)
+          z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              wide[i], widen8<LQ_E4M3>(b[2 * i], b[2 * i + 1], 1.f), z, 0, 0, 0);
+      } else {
+        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, AT == LQ_E5M2 ? 1 : 0, 0, 0, e, 0, 127);
       }
-#pragma unroll
-      for (int t = 0; t < TF; ++t) {
-        f32x4 z = {};
-        if (PREC) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wide[t][i], wb[i], z, 0, 0, 0);
-        } else {
-          constexpr int A = AK == LQ_E5M2 ? 1 : 0;
-          z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[t], b, z, A, 0, 0, ea[t], 0, 127);
-        }
-        acc[t][f] += z * scale;
-      }
+      acc[f] += z * scale;
     }
   };
-  if (begin < end) {
+  for (int s = begin; s < end; s += U) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) load(u, begin + u);
-    for (int s = begin; s < end; s += U) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (s + u < end) {
-          step(u);
-          load(u, s + u + U);
-        }
+    for (int u = 0; u < U; ++u) {
+      if (s + u < end) {
+        step(u, s + u);
+        load(u, s + u + U);
       }
     }
   }
 
   // ---- the waves' sums, [wave][token][row], added in order
+  if constexpr (HELD) wait_lds_and_barrier();            // nobody reads the activations any more
 #pragma unroll
-  for (int t = 0; t < TF; ++t)
+  for (int f = 0; f < WF; ++f)
 #pragma unroll
-    for (int f = 0; f < WF; ++f)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        lds[(wave * TOK + 16 * t + 4 * g + i) * PITCH + 16 * f + c16] = acc[t][f][i];
+    for (int i = 0; i < 4; ++i) lds[(wave * TOK + 4 * g + i) * PITCH + 16 * f + c16] = acc[f][i];
   __syncthreads();
   const int quads = outs / 4;
   const OutputTypes types = output_types(p.out, p.ldo, p.residual, p.ldr, p.out_dt);
@@ -256,28 +256,29 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
   }
 }
 
-template <int AK, bool PREC, int TF, int WF>
+template <int AK, bool PREC, int WF>
 hipError_t launch(const F8Product& in, const F8FewPlan& plan, hipStream_t st) {
   F8Product p = in;
-  const int64_t tok = 16 * TF, outs = p.gated ? 8 * WF : 16 * WF, out_m = p.gated ? p.m / 2 : p.m;
+  const int64_t tok = kFewTokens, outs = p.gated ? 8 * WF : 16 * WF, out_m = p.gated ? p.m / 2 : p.m;
   p.row_blocks = static_cast<int>((out_m + outs - 1) / outs);
   int64_t tiles = (p.R + tok - 1) / tok;
   if (p.offsets) tiles = p.R / tok + (p.E < p.R ? p.E : p.R);
   const int64_t blocks = tiles * p.row_blocks * p.slices;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const int threads = 64 * plan.waves;
-  const int bytes = static_cast<int>(plan.waves * tok * (16 * WF + 4) * 4);
-  auto* k = gemv8_kernel<AK, PREC, TF, WF>;
+  int64_t bytes = plan.waves * tok * (16 * WF + 4) * 4;
+  if (plan.held && plan.held_bytes > bytes) bytes = plan.held_bytes;
+  auto* k = gemv8_kernel<AK, PREC, WF>;
   if (bytes > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
     if (e != hipSuccess) return e;
   }
   // a launch has fewer than 2^32 threads
   const int64_t most = (int64_t{1} << 31) / threads;
   for (int64_t b = 0; b < blocks; b += most) {
     p.block0 = static_cast<int>(b);
-    k<<<static_cast<uint32_t>(blocks - b < most ? blocks - b : most), threads, bytes, st>>>(p);
+    k<<<static_cast<uint32_t>(blocks - b < most ? blocks - b : most), threads, static_cast<uint32_t>(bytes), st>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -286,12 +287,9 @@ hipError_t launch(const F8Product& in, const F8FewPlan& plan, hipStream_t st) {
 
 template <int AK, bool PREC>
 hipError_t by_shape(const F8Product& p, const F8FewPlan& plan, hipStream_t st) {
-  if (plan.wf == 1) return launch<AK, PREC, 1, 1>(p, plan, st);
-  switch (plan.tf) {
-    case 1: return launch<AK, PREC, 1, 2>(p, plan, st);
-    case 2: return launch<AK, PREC, 2, 2>(p, plan, st);
-    default: return launch<AK, PREC, 4, 2>(p, plan, st);
-  }
+  return plan.wf == 1   ? launch<AK, PREC, 1>(p, plan, st)
+         : plan.wf == 2 ? launch<AK, PREC, 2>(p, plan, st)
+                        : launch<AK, PREC, 4>(p, plan, st);
 }
 
 template <int AK>
@@ -304,26 +302,33 @@ hipError_t by_precision(const F8Product& p, const F8FewPlan& plan, bool precise,
 F8FewPlan few_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bool grouped) {
   F8FewPlan p{};
   const int64_t cus = num_cus(), steps = (K + 127) / 128;
-  const int64_t runs = grouped ? (E < R ? E : R) : 1, rows = (R + runs - 1) / runs;
-  p.tf = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const int64_t runs = grouped ? (E < R ? E : R) : 1;
   const int64_t out_m = gated ? m / 2 : m;
   auto blocks = [&](int wf) {
     const int64_t outs = gated ? 8 * wf : 16 * wf;
     return (out_m + outs - 1) / outs * runs;
   };
-  p.wf = p.tf > 1 || gated || blocks(2) >= 2 * cus ? 2 : 1;
-  p.waves = static_cast<int>(steps >= 32 ? 8 : steps >= 8 ? 4 : steps >= 2 ? 2 : 1);
+  // The tallest block that leaves no compute unit without one (16 tokens x 4096 ->
+  // 2 x 14336: 64 rows 28 us, 32 rows 36; one token x 4096 -> 4096: 16 rows 8.8 us,
+  // 32 rows 10.1), and waves of 8 blocks of positions or more (the same: 4 waves 8.8 us,
+  // 8 waves 9.7; 28672 -> 8192: 8 waves 46, 4 waves 55), 16 where there are
+  // workgroups enough (16 tokens: 2 waves 28 us, 4 waves 32).
+  p.wf = blocks(4) >= cus ? 4 : gated || blocks(2) >= cus ? 2 : 1;
+  const int64_t have = blocks(p.wf), each = have * 2 >= cus * 3 ? 16 : 8;
+  p.waves = static_cast<int>(steps >= 8 * each ? 8 : steps < each ? 1 : steps / each);
   p.slices = 1;
   p.slice_steps = static_cast<int>(steps);
-  const int64_t have = blocks(p.wf);
   if (have < cus) {
-    int64_t s = (cus + have - 1) / have;
-    const int64_t most = steps / (4 * p.waves) > 1 ? steps / (4 * p.waves) : 1;
-    if (s > most) s = most;
+    int64_t s = cus / have;
+    if (s > steps / 64) s = steps / 64;
     if (s > 16) s = 16;
+    if (s < 1) s = 1;
     p.slice_steps = static_cast<int>((steps + s - 1) / s);
     p.slices = static_cast<int>((steps + p.slice_steps - 1) / p.slice_steps);
   }
+  // of runs the host knows only that none is longer than R
+  p.held = R <= 4 && R * p.slice_steps <= 128;
+  p.held_bytes = R * (p.slice_steps * 132 + 32);
   return p;
 }
 

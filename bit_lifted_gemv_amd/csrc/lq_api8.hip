@@ -33,8 +33,8 @@ lq_status check_quant(const void* x, lq_dtype dtype, int64_t K, int64_t ld) {
 
 // ---- the products
 struct Plan8 {
-  bool few;                    // on the few-row kernel, which can quantize 16-bit activations itself
-  bool inside;                 // whether it does, where their alignment allows it
+  bool few;                    // on the few-row kernel
+  bool quantize;               // 16-bit activations by a launch of its own
   lq::F8FewPlan fp;
   lq::F8ManyPlan mp;
   int slices;
@@ -56,20 +56,23 @@ lq_status check_sizes8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_
   return LQ_OK;
 }
 
-constexpr int64_t kFewRowsPerRun = 64, kInside = 16;
+// Up to 16 rows of one matrix, or of a run on average, go to the few-row kernel: 16 x 4096
+// -> 4096 12 us there and 15 on tiles, -> 2 x 14336 32 and 33, 24 rows 44 and 33;
+// 64 experts (2048 -> 2 x 1408), 1024 rows 96 and 107, 2048 rows 150 and 114.
+constexpr int64_t kFewRowsPerRun = 16;
 
 Plan8 plan8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_t a_rows, int64_t R, bool gated,
             bool grouped, bool float_scales, bool precise) {
   Plan8 p{};
   const int64_t runs = grouped ? (E < R ? E : R < 1 ? 1 : R) : 1;
   p.few = R <= kFewRowsPerRun * runs;
-  p.inside = p.few && R <= kInside * runs;
-  p.fp = lq::few_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped);
+    p.fp = lq::few_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped);
   p.mp = lq::many_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped, float_scales, precise);
   p.slices = p.few ? p.fp.slices : p.mp.slices;
   p.ldq = whole(K);
   p.lde = (blocks(K) + 3) / 4 * 4;
-  if (is16(a_dtype)) {
+  p.quantize = is16(a_dtype) && !(p.few && p.fp.held);
+  if (p.quantize) {
     p.exps_at = round256(static_cast<size_t>(a_rows * p.ldq));
     p.bytes = p.exps_at + round256(static_cast<size_t>(a_rows * p.lde));
   }
@@ -134,10 +137,9 @@ hipError_t run8(lq::F8Product& p, const Plan8& plan, const void* a, lq_dtype a_d
   p.exps = exps;
   p.lde = lde;
   p.a_rows = static_cast<int>(a_rows);
-  const bool wide = is16(a_dtype), precise = p.out_dt == LQ_F32;
-  // in the kernel where rows are whole 16-byte pieces
-  const bool inside = plan.inside && p.K % 8 == 0 && lda % 8 == 0 && aligned(a, 16);
-  if (wide && !inside) {
+  const bool precise = p.out_dt == LQ_F32;
+  p.pieces = p.K % 8 == 0 && lda % 8 == 0 && aligned(a, 16);
+  if (plan.quantize) {
     const hipError_t e = lq::launch_quant8(a, a_dtype, a_rows, p.K, lda, ws, LQ_E4M3, plan.ldq,
                                            ws + plan.exps_at, plan.lde, st);
     if (e != hipSuccess) return e;

@@ -265,6 +265,7 @@ struct F8Product {
   int float_scales;
   const void* a;               // [a_rows][lda], 8-bit (K up to whole 128) or 16-bit
   int64_t lda;
+  int pieces;                  // 16-bit rows are whole 16-byte pieces
   const uint8_t* exps;         // [a_rows][lde], of 8-bit activations
   int64_t lde;
   int a_rows;
@@ -285,8 +286,10 @@ struct F8Product {
 };
 // Few rows per matrix (k_gemv8.hip).
 struct F8FewPlan {
-  int tf, wf, waves;           // 16 tf tokens and 16 wf rows per workgroup of `waves`
+  int wf, waves;               // 16 wf rows and 16 tokens per workgroup of `waves`
   int slices, slice_steps;
+  int held;                    // activations in LDS, 16-bit ones quantized on the way
+  int64_t held_bytes;
 };
 F8FewPlan few_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bool grouped);
 hipError_t launch_gemv8(const F8Product& p, int a_type, const F8FewPlan& plan, bool precise,

@@ -790,8 +790,8 @@ class Blocks8(NamedTuple):
 def _exponents(shape, device) -> torch.Tensor:
     """Room for exponents whose rows are whole words: a view of it."""
     blocks = shape[-1]
-    return torch.empty((*shape[:-1], blocks + -blocks % 4), dtype=torch.uint8,
-                       device=device)[..., :blocks]
+    held = torch.empty((*shape[:-1], blocks + -blocks % 4), dtype=torch.uint8, device=device)
+    return held[..., :blocks] if blocks % 4 else held
 
 
 def _blocks(n: int) -> int:
@@ -846,41 +846,41 @@ def quantize8_blocks(w: torch.Tensor, stream=None) -> Blocks8:
     return Blocks8(values, scales)
 
 
-def _exponent_pitch(name: str, t: torch.Tensor) -> int:
-    """Row pitch of exponents [..][rows][blocks], whose rows are whole words (also the
-    last one: the kernels read words)."""
-    *lead, rows, blocks = t.shape
+def _exponent_pitch(name: str, t: torch.Tensor, dtype: torch.dtype) -> int:
+    """Row pitch of scales [..][rows][blocks]; rows of uint8 exponents are whole words
+    (also the last one: the kernels read words)."""
+    shape, stride = t.shape, t.stride()
+    rows, blocks = shape[-2:]
     held = blocks + -blocks % 4
-    if blocks > 1 and t.stride(-1) != 1:
+    if blocks > 1 and stride[-1] != 1:
         raise ValueError(f"{name}'s rows must be dense")
     # a stride along a single element says nothing
-    pitch = t.stride(-2) if rows > 1 else held
-    if lead and lead[0] > 1:
+    pitch = stride[-2] if rows > 1 else held
+    if len(shape) > 2 and shape[0] > 1:
         if rows == 1:
-            pitch = t.stride(0)
-        elif t.stride(0) != rows * pitch:
+            pitch = stride[0]
+        elif stride[0] != rows * pitch:
             raise ValueError(f"{name}'s matrices must follow one another")
-    if t.dtype == torch.uint8 and t.numel():
-        last = t.storage_offset() + (t.numel() // blocks - 1) * pitch + held
-        if pitch % 4 or last > t.untyped_storage().nbytes():
+    if dtype is torch.uint8 and t.numel():
+        if pitch % 4 or (held != blocks and t.storage_offset() + (t.numel() // blocks - 1) * pitch + held
+                         > t.untyped_storage().nbytes()):
             raise ValueError(f"{name}'s rows must be whole words (as quantize8 makes them)")
     return pitch
 
 
 def _weights8(w: Blocks8, lead: tuple) -> Tuple[int, int]:
     """Checks weights of [lead] matrices; their scales' type and row pitch."""
-    values, scales = w.values, w.scales
+    values, scales = w
     m, K = values.shape[-2:]
     _plain("w.values", values, torch.float8_e4m3fn, lead + (m, K))
     if K % 128:
         raise ValueError(f"w.values has {K} columns, not whole 128 (zeros behind the last)")
-    shape = lead + (_blocks(m), _blocks(K))
-    if scales.dtype not in (torch.uint8, torch.float32):
-        raise TypeError(f"w.scales must be uint8 exponents or float32, not {scales.dtype}")
+    shape, dtype = lead + (-(-m // 128), K // 128), scales.dtype
+    if dtype is not torch.uint8 and dtype is not torch.float32:
+        raise TypeError(f"w.scales must be uint8 exponents or float32, not {dtype}")
     if scales.shape != shape:
         raise ValueError(f"w.scales has shape {tuple(scales.shape)}, not {shape}")
-    kind = LQ_F32 if scales.dtype == torch.float32 else LQ_E8M0
-    return kind, _exponent_pitch("w.scales", scales)
+    return LQ_E8M0 if dtype is torch.uint8 else LQ_F32, _exponent_pitch("w.scales", scales, dtype)
 
 
 def _rows8(a, width: int):
@@ -893,7 +893,8 @@ def _rows8(a, width: int):
         B = values.shape[0]
         lda = _pitch("a.values", values, (B, width))
         _pitch("a.exps", exps, (B, width // 128), torch.uint8)
-        return values, TYPES8[values.dtype], lda, exps, _exponent_pitch("a.exps", exps), width
+        return (values, TYPES8[values.dtype], lda, exps, _exponent_pitch("a.exps", exps, torch.uint8),
+                width)
     if a.dtype not in (torch.float16, torch.bfloat16):
         raise TypeError(f"a must be Rows8, float16 or bfloat16, not {a.dtype}")
     B, K = a.shape
