@@ -17,26 +17,43 @@ namespace {
 
 using namespace f8;
 
-// Eight consecutive values of a row of n from position k; zeros behind it.
-template <int DT, bool WIDE>
-__device__ __forceinline__ void load8(const void* row, int64_t k, int64_t n, float (&v)[8]) {
-  if (WIDE && k + 8 <= n) {
-    if (DT == LQ_F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + k);
-      const float4 a = p[0], b = p[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + k);
-      v[0] = low16<DT>(w.x); v[1] = high16<DT>(w.x);
-      v[2] = low16<DT>(w.y); v[3] = high16<DT>(w.y);
-      v[4] = low16<DT>(w.z); v[5] = high16<DT>(w.z);
-      v[6] = low16<DT>(w.w); v[7] = high16<DT>(w.w);
-    }
-    return;
-  }
+// Eight consecutive values of a row of n from position k, zeros behind it, as they
+// lie in memory (16 bytes at any address: global memory takes them).
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef i32x4 i32x4_any __attribute__((aligned(1)));
+
+template <int DT>
+struct Eight {
+  static constexpr int WORDS = DT == LQ_F32 ? 8 : 4;
+  uint32_t w[WORDS] = {};
+};
+template <int DT>
+__device__ __forceinline__ Eight<DT> load8(const void* row, int64_t k, int64_t n) {
+  Eight<DT> v;
+  const uint8_t* p = static_cast<const uint8_t*>(row) + k * (DT == LQ_F32 ? 4 : 2);
+  if (k + 8 <= n) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = k + i < n ? load_as_float<DT>(row, k + i) : 0.f;
+    for (int x = 0; x < v.WORDS / 4; ++x) {
+      const i32x4 y = *reinterpret_cast<const i32x4_any*>(p + 16 * x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.w[4 * x + i] = y[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (k + i >= n) break;
+      if (DT == LQ_F32) v.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+      else v.w[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[i]) << (16 * (i % 2));
+    }
+  }
+  return v;
+}
+template <int DT>
+__device__ __forceinline__ void values(const Eight<DT>& e, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = DT == LQ_F32 ? __uint_as_float(e.w[i % Eight<DT>::WORDS])
+                        : i % 2 ? high16<DT>(e.w[i / 2]) : low16<DT>(e.w[i / 2]);
 }
 
 __device__ __forceinline__ float largest8(const float (&v)[8]) {
@@ -56,7 +73,7 @@ __device__ __forceinline__ uint2 round8(const float (&v)[8], int byte) {
 // UNITS pieces per wave, their loads on the way together.
 constexpr int kUnits = 2;
 
-template <int DT, int T, bool WIDE>
+template <int DT, int T>
 __global__ void __launch_bounds__(256) quant8_rows_kernel(const void* __restrict__ x, int64_t units,
                                                           int64_t K, int64_t ld, int per_row,
                                                           uint8_t* __restrict__ q, int64_t ldq,
@@ -64,7 +81,7 @@ __global__ void __launch_bounds__(256) quant8_rows_kernel(const void* __restrict
   constexpr int ESZ = DT == LQ_F32 ? 4 : 2;
   const int lane = threadIdx.x & 63;
   const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6)) * kUnits;
-  float v[kUnits][8];
+  Eight<DT> raw[kUnits];
   int64_t row[kUnits];
   int at[kUnits];
 #pragma unroll
@@ -72,19 +89,20 @@ __global__ void __launch_bounds__(256) quant8_rows_kernel(const void* __restrict
     const int64_t u = min(u0 + c, units - 1);
     row[c] = u / per_row;
     at[c] = static_cast<int>(u - row[c] * per_row);
-    load8<DT, WIDE>(static_cast<const uint8_t*>(x) + row[c] * ld * ESZ, at[c] * int64_t{512} + lane * 8,
-                    K, v[c]);
+    raw[c] = load8<DT>(static_cast<const uint8_t*>(x) + row[c] * ld * ESZ, at[c] * int64_t{512} + lane * 8, K);
   }
 #pragma unroll
   for (int c = 0; c < kUnits; ++c) {
     if (u0 + c >= units) return;
-    float m = largest8(v[c]);
+    float v[8];
+    values(raw[c], v);
+    float m = largest8(v);
 #pragma unroll
     for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
     const int byte = block_exponent<T>(m);
     const int64_t k = at[c] * int64_t{512} + lane * 8;
     if (k < (K + 127) / 128 * 128)
-      *reinterpret_cast<uint2*>(q + row[c] * ldq + k) = round8<T>(v[c], byte);
+      *reinterpret_cast<uint2*>(q + row[c] * ldq + k) = round8<T>(v, byte);
     uint32_t word = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -95,7 +113,7 @@ __global__ void __launch_bounds__(256) quant8_rows_kernel(const void* __restrict
 
 // Blocks: a workgroup per 128 x 128 block, eight rows of 16 lanes at a time per
 // two waves.
-template <int DT, bool WIDE>
+template <int DT>
 __global__ void __launch_bounds__(256) quant8_blocks_kernel(const void* __restrict__ w, int m,
                                                             int64_t K, int64_t ld,
                                                             uint8_t* __restrict__ q, int64_t ldq,
@@ -105,13 +123,17 @@ __global__ void __launch_bounds__(256) quant8_blocks_kernel(const void* __restri
   const int tid = threadIdx.x, lane = tid & 15, r0 = blockIdx.y * 128 + (tid >> 4);
   const int64_t first = static_cast<int64_t>(blockIdx.z) * m;
   const int64_t k = blockIdx.x * int64_t{128} + lane * 8;
-  float v[8][8];
-  float largest = 0.f;
+  Eight<DT> raw[8];
+  float v[8], largest = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 16 * i;
-    load8<DT, WIDE>(static_cast<const uint8_t*>(w) + (first + min(r, m - 1)) * ld * ESZ, k, K, v[i]);
-    largest = fmaxf(largest, largest8(v[i]));
+    raw[i] = load8<DT>(static_cast<const uint8_t*>(w) + (first + min(r, m - 1)) * ld * ESZ, k, K);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    values(raw[i], v);
+    largest = fmaxf(largest, largest8(v));
   }
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) largest = fmaxf(largest, __shfl_xor(largest, d));
@@ -121,7 +143,8 @@ __global__ void __launch_bounds__(256) quant8_blocks_kernel(const void* __restri
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 16 * i;
-    if (r < m) *reinterpret_cast<uint2*>(q + (first + r) * ldq + k) = round8<LQ_E4M3>(v[i], byte);
+    values(raw[i], v);
+    if (r < m) *reinterpret_cast<uint2*>(q + (first + r) * ldq + k) = round8<LQ_E4M3>(v, byte);
   }
   if (tid == 0) {
     const int64_t strip = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y;
@@ -129,7 +152,7 @@ __global__ void __launch_bounds__(256) quant8_blocks_kernel(const void* __restri
   }
 }
 
-template <int DT, int T, bool WIDE>
+template <int DT, int T>
 hipError_t rows(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, int64_t ldq,
                 uint8_t* exps, int64_t lde, hipStream_t st) {
   const int per_row = static_cast<int>((K + 511) / 512);
@@ -138,7 +161,7 @@ hipError_t rows(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, int
   for (int64_t r = 0; r < n; r += rows_per) {
     const int64_t some = n - r < rows_per ? n - r : rows_per;
     const int64_t groups = (some * per_row + 4 * kUnits - 1) / (4 * kUnits);
-    quant8_rows_kernel<DT, T, WIDE><<<static_cast<uint32_t>(groups), 256, 0, st>>>(
+    quant8_rows_kernel<DT, T><<<static_cast<uint32_t>(groups), 256, 0, st>>>(
         static_cast<const uint8_t*>(x) + r * ld * (DT == LQ_F32 ? 4 : 2), some * per_row, K, ld,
         per_row, q + r * ldq, ldq, exps + r * lde, lde);
     const hipError_t e = hipGetLastError();
@@ -147,16 +170,11 @@ hipError_t rows(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, int
   return hipSuccess;
 }
 
-template <int DT, bool WIDE>
+template <int DT>
 hipError_t by_type(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, lq_dtype type,
                    int64_t ldq, uint8_t* exps, int64_t lde, hipStream_t st) {
-  return type == LQ_E4M3 ? rows<DT, LQ_E4M3, WIDE>(x, n, K, ld, q, ldq, exps, lde, st)
-                         : rows<DT, LQ_E5M2, WIDE>(x, n, K, ld, q, ldq, exps, lde, st);
-}
-
-// Whether rows of this type can be read in 16-byte pieces.
-bool wide(const void* x, int64_t ld, int size) {
-  return (reinterpret_cast<uintptr_t>(x) | static_cast<uint64_t>(ld) * size) % 16 == 0;
+  return type == LQ_E4M3 ? rows<DT, LQ_E4M3>(x, n, K, ld, q, ldq, exps, lde, st)
+                         : rows<DT, LQ_E5M2>(x, n, K, ld, q, ldq, exps, lde, st);
 }
 
 template <int DT>
@@ -164,10 +182,7 @@ hipError_t blocks(const void* w, int64_t E, int64_t m, int64_t K, int64_t ld, ui
                   int64_t ldq, uint8_t* exps, int64_t lde, hipStream_t st) {
   const dim3 grid(static_cast<uint32_t>((K + 127) / 128), static_cast<uint32_t>((m + 127) / 128),
                   static_cast<uint32_t>(E));
-  if (wide(w, ld, DT == LQ_F32 ? 4 : 2))
-    quant8_blocks_kernel<DT, true><<<grid, 256, 0, st>>>(w, static_cast<int>(m), K, ld, q, ldq, exps, lde);
-  else
-    quant8_blocks_kernel<DT, false><<<grid, 256, 0, st>>>(w, static_cast<int>(m), K, ld, q, ldq, exps, lde);
+  quant8_blocks_kernel<DT><<<grid, 256, 0, st>>>(w, static_cast<int>(m), K, ld, q, ldq, exps, lde);
   return hipGetLastError();
 }
 
@@ -175,17 +190,10 @@ hipError_t blocks(const void* w, int64_t E, int64_t m, int64_t K, int64_t ld, ui
 
 hipError_t launch_quant8(const void* x, lq_dtype dt, int64_t n, int64_t K, int64_t ld, uint8_t* q,
                          lq_dtype type, int64_t ldq, uint8_t* exps, int64_t lde, hipStream_t st) {
-  const bool w = wide(x, ld, dt == LQ_F32 ? 4 : 2);
   switch (dt) {
-    case LQ_F32:
-      return w ? by_type<LQ_F32, true>(x, n, K, ld, q, type, ldq, exps, lde, st)
-               : by_type<LQ_F32, false>(x, n, K, ld, q, type, ldq, exps, lde, st);
-    case LQ_F16:
-      return w ? by_type<LQ_F16, true>(x, n, K, ld, q, type, ldq, exps, lde, st)
-               : by_type<LQ_F16, false>(x, n, K, ld, q, type, ldq, exps, lde, st);
-    default:
-      return w ? by_type<LQ_BF16, true>(x, n, K, ld, q, type, ldq, exps, lde, st)
-               : by_type<LQ_BF16, false>(x, n, K, ld, q, type, ldq, exps, lde, st);
+    case LQ_F32: return by_type<LQ_F32>(x, n, K, ld, q, type, ldq, exps, lde, st);
+    case LQ_F16: return by_type<LQ_F16>(x, n, K, ld, q, type, ldq, exps, lde, st);
+    default: return by_type<LQ_BF16>(x, n, K, ld, q, type, ldq, exps, lde, st);
   }
 }
 
