@@ -75,39 +75,34 @@ __device__ __forceinline__ i32x4 resource(const void* p, int64_t bytes) {
   return r;
 }
 
-// Q: rows of a matrix-core tile, 16 (stages of 128 positions) or 32 (of 64).
-template <int Q, int WT, int WW, int WK, int FT, int FW>
+template <int WT, int WW, int WK, int FT, int FW>
 struct Tile {
   static constexpr int GROUP = WT * WW, NW = GROUP * WK;        // waves
-  static constexpr int TOK = Q * FT * WT, ROWS = Q * FW * WW;
-  static constexpr int KS = Q == 16 ? 128 : 64, CH = KS / 16;   // a row's bytes and pieces per stage
-  static constexpr int PER = 64 / CH;                           // rows of a 1 KB load
-  static constexpr int IL = TOK / PER / GROUP, WL = ROWS / PER / GROUP;   // loads per wave and stage
+  static constexpr int TOK = 16 * FT * WT, ROWS = 16 * FW * WW;
+  static constexpr int IL = TOK / 8 / GROUP, WL = ROWS / 8 / GROUP;   // 1 KB loads per wave and stage
   static constexpr int LOADS = IL + WL + 1;
   // a stage: tokens, rows and the rows' scales; behind the ring the tokens' exponents, whose words
   // hold four blocks (two of them, in turn), and a place that nobody reads
-  static constexpr int ROWS_AT = TOK * KS, SCALES_AT = ROWS_AT + ROWS * KS, STAGE = SCALES_AT + ROWS * 4;
+  static constexpr int ROWS_AT = TOK * 128, SCALES_AT = ROWS_AT + ROWS * 128, STAGE = SCALES_AT + ROWS * 4;
   static constexpr int BEHIND = 2 * TOK * 4 + 256;
   static constexpr int PER_SIMD = 2;                            // waves, of up to 256 registers
   static constexpr int MAX_LDS = 163840 / (PER_SIMD * 4 / NW);  // workgroups of a compute unit
   static constexpr int RING = (MAX_LDS / WK - BEHIND) / STAGE, S = RING > 4 ? 4 : RING;
   static constexpr int PART = S * STAGE + BEHIND, LDS = WK * PART;   // of a group, of all
-  static constexpr int PITCH = Q * FW + 4, AT_ONCE = Q == 16 ? 2 : 1;   // of the sums on their way out
-  static_assert(NW * AT_ONCE * Q * PITCH * 4 <= LDS);
+  static constexpr int PITCH = 16 * FW + 4, AT_ONCE = 2;   // of the sums on their way out
+  static_assert(NW * AT_ONCE * 16 * PITCH * 4 <= LDS);
   static_assert(WK <= 2 && S >= 2 && TOK >= 64 && ROWS >= 64 && FT >= 4 && S * LOADS < 64);
   static_assert(TOK / 64 + ROWS / 64 <= GROUP);                 // one wave for each 64 exponents or scales
-  static_assert(WK == 1 || GROUP * FT * FW * Q * Q * 4 <= LDS); // the groups' sums change hands there
+  static_assert(WK == 1 || GROUP * FT * FW * 1024 <= LDS);           // the groups' sums change hands there
 };
 
-template <int AK, bool FS, bool PREC, int Q, int WT, int WW, int WK, int FT, int FW>
-__global__ void __launch_bounds__(64 * WT * WW * WK, (Tile<Q, WT, WW, WK, FT, FW>::PER_SIMD))
+template <int AK, bool FS, bool PREC, int WT, int WW, int WK, int FT, int FW>
+__global__ void __launch_bounds__(64 * WT * WW * WK, (Tile<WT, WW, WK, FT, FW>::PER_SIMD))
 gemm8_kernel(F8Product p) {
-  using P = Tile<Q, WT, WW, WK, FT, FW>;
-  constexpr int TOK = P::TOK, ROWS = P::ROWS, GROUP = P::GROUP, S = P::S, KS = P::KS, NR = Q * Q / 64;
-  static_assert(Q == 16 || !(FS || PREC));
-  typedef float sums __attribute__((ext_vector_type(NR)));
+  using P = Tile<WT, WW, WK, FT, FW>;
+  constexpr int TOK = P::TOK, ROWS = P::ROWS, GROUP = P::GROUP, S = P::S;
   extern __shared__ __align__(1024) uint8_t lds[];
-  const int tid = threadIdx.x, lane = tid & 63, c = lane % Q, g = lane / Q;
+  const int tid = threadIdx.x, lane = tid & 63, c = lane & 15, g = lane >> 4;
   const int wave = uniform(tid >> 6), wk = wave / GROUP, wg = wave % GROUP, wt = wg % WT, ww = wg / WT;
 
   // ---- which tile: token tiles in fours, the rows inside, so that the
@@ -143,8 +138,8 @@ gemm8_kernel(F8Product p) {
   // gate's and the others the up rows of the same outputs.
   auto weight_row = [&](int lr) {
     if (!p.gated) return min(out0 + lr, p.m - 1);
-    const int w = lr / (Q * FW), j = lr / Q % FW;
-    return min(out0 + w * (Q / 2) * FW + j % (FW / 2) * Q + lr % Q, half - 1) + (j < FW / 2 ? 0 : half);
+    const int w = lr / (16 * FW), j = lr / 16 % FW;
+    return min(out0 + w * (16 / 2) * FW + j % (FW / 2) * 16 + lr % 16, half - 1) + (j < FW / 2 ? 0 : half);
   };
   auto token_row = [&](int lt) {
     int r = row0 + min(lt, tokens - 1);
@@ -161,16 +156,16 @@ gemm8_kernel(F8Product p) {
                               strips * p.lds * (FS ? 4 : 1));
   uint32_t a_src[P::IL], w_src[P::WL];
   // where piece x of row r of a tile lies, 16 lanes reading one piece of 16 rows apart
-  auto place = [](int r, int x) { return x ^ (Q == 16 ? r >> 1 & 7 : r >> 2 & 3); };
+  auto place = [](int r, int x) { return x ^ (r >> 1 & 7); };
 #pragma unroll
   for (int i = 0; i < P::IL; ++i) {
-    const int lt = P::PER * (wg + GROUP * i) + lane / P::CH;
-    a_src[i] = static_cast<uint32_t>(token_row(lt)) * static_cast<uint32_t>(p.lda) + 16 * place(lt, lane % P::CH);
+    const int lt = 8 * (wg + GROUP * i) + lane / 8;
+    a_src[i] = static_cast<uint32_t>(token_row(lt)) * static_cast<uint32_t>(p.lda) + 16 * place(lt, lane % 8);
   }
 #pragma unroll
   for (int i = 0; i < P::WL; ++i) {
-    const int lr = P::PER * (wg + GROUP * i) + lane / P::CH;
-    w_src[i] = static_cast<uint32_t>(weight_row(lr)) * static_cast<uint32_t>(p.ldw) + 16 * place(lr, lane % P::CH);
+    const int lr = 8 * (wg + GROUP * i) + lane / 8;
+    w_src[i] = static_cast<uint32_t>(weight_row(lr)) * static_cast<uint32_t>(p.ldw) + 16 * place(lr, lane % 8);
   }
   // wave w of a group loads the exponents of 64 tokens, the scales of 64 rows, or nothing
   constexpr int EW = TOK / 64, SW = ROWS / 64;
@@ -180,25 +175,23 @@ gemm8_kernel(F8Product p) {
                            static_cast<uint32_t>(p.lds) * (FS ? 4u : 1u)
                      : 0u;
   // this group's stages: every WK-th from wk of the slice's
-  constexpr int PER_BLOCK = 128 / KS;
-  const int step0 = slice * p.slice_steps * PER_BLOCK;
-  const int steps = min(p.slice_steps, p.steps - slice * p.slice_steps) * PER_BLOCK;
+  const int step0 = slice * p.slice_steps, steps = min(p.slice_steps, p.steps - step0);
   const int most = (steps + WK - 1) / WK, mine = (steps + WK - 1 - wk) / WK;
   const uint32_t lds0 = lds_address(lds) + wk * P::PART;
   auto step_of = [&](int n) { return step0 + min(n * WK + wk, steps - 1); };
   // past the end: the last one again, into a place that nobody reads
   auto issue = [&](int n, int slot) {
-    const int st = step_of(n), q = st / PER_BLOCK;
+    const int q = step_of(n);
     const uint32_t base = lds0 + slot * P::STAGE;
 #pragma unroll
     for (int i = 0; i < P::IL; ++i)
-      load_to_lds(base + (wg + GROUP * i) * 1024, a_src[i], ares, st * KS);
+      load_to_lds(base + (wg + GROUP * i) * 1024, a_src[i], ares, q * 128);
 #pragma unroll
     for (int i = 0; i < P::WL; ++i)
-      load_to_lds(base + P::ROWS_AT + (wg + GROUP * i) * 1024, w_src[i], wres, st * KS);
+      load_to_lds(base + P::ROWS_AT + (wg + GROUP * i) * 1024, w_src[i], wres, q * 128);
     // every lane of an exponent load touches a line of its own: only when a new word begins
     const bool scales = wg >= EW && wg < EW + SW;
-    const bool fresh = n == 0 || q >> 2 != (st - WK) / PER_BLOCK >> 2;
+    const bool fresh = n == 0 || q >> 2 != (q - WK) >> 2;
     const uint32_t to = scales ? base + P::SCALES_AT + (wg - EW) * 256
                         : wg < EW && fresh ? lds0 + S * P::STAGE + (q >> 2 & 1) * TOK * 4 + wg * 256
                                            : lds0 + S * P::STAGE + 2 * TOK * 4;
@@ -207,7 +200,7 @@ gemm8_kernel(F8Product p) {
   };
 
   // ---- operands: all row tiles, and a ring of four token tiles
-  sums acc[FT][FW] = {};
+  f32x4 acc[FT][FW] = {};
   i32x8 a[4], b[FW];
   uint32_t ea[4], sb[FW];                                // exponents, still in words
   f32x4 sf[FS ? FW : 1];                                 // float32 scales of a lane's four rows
@@ -215,15 +208,15 @@ gemm8_kernel(F8Product p) {
   // tiles are immediate offsets from them.
   uint32_t a_at[2], b_at[2], s_at, e_at;
   {
-    const uint32_t at = c * KS + 16 * place(c, g);
-    a_at[0] = lds0 + wt * Q * FT * KS + at;
-    b_at[0] = lds0 + P::ROWS_AT + ww * Q * FW * KS + at;
-    a_at[1] = a_at[0] ^ KS / 2;                          // (every other part is a multiple of KS)
-    b_at[1] = b_at[0] ^ KS / 2;
-    s_at = lds0 + P::SCALES_AT + (ww * Q * FW + (FS ? 4 * g : c)) * 4;
+    const uint32_t at = c * 128 + 16 * place(c, g);
+    a_at[0] = lds0 + wt * 16 * FT * 128 + at;
+    b_at[0] = lds0 + P::ROWS_AT + ww * 16 * FW * 128 + at;
+    a_at[1] = a_at[0] ^ 64;                               // (every other part is a multiple of 128)
+    b_at[1] = b_at[0] ^ 64;
+    s_at = lds0 + P::SCALES_AT + (ww * 16 * FW + (FS ? 4 * g : c)) * 4;
   }
-  const uint32_t e0_at = lds0 + S * P::STAGE + (wt * Q * FT + c) * 4;
-  auto exponents_of = [&](int n) { e_at = e0_at + (step_of(n) / PER_BLOCK >> 2 & 1) * TOK * 4; };
+  const uint32_t e0_at = lds0 + S * P::STAGE + (wt * 16 * FT + c) * 4;
+  auto exponents_of = [&](int n) { e_at = e0_at + (step_of(n) >> 2 & 1) * TOK * 4; };
   auto a_moves = [&](uint32_t by) { a_at[0] += by; a_at[1] += by; };
   auto b_moves = [&](uint32_t by) { b_at[0] += by; b_at[1] += by; s_at += by; };
   auto read_tile = [&](const uint32_t (&at)[2], int offset, i32x8& v) {
@@ -232,13 +225,13 @@ gemm8_kernel(F8Product p) {
     v[4] = hi[0]; v[5] = hi[1]; v[6] = hi[2]; v[7] = hi[3];
   };
   auto read_a = [&](int f) {
-    read_tile(a_at, f * Q * KS, a[f % 4]);
-    ea[f % 4] = lds_read<uint32_t>(e_at, f * Q * 4);
+    read_tile(a_at, f * 16 * 128, a[f % 4]);
+    ea[f % 4] = lds_read<uint32_t>(e_at, f * 16 * 4);
   };
   auto read_b = [&](int f) {
-    read_tile(b_at, f * Q * KS, b[f]);
-    if constexpr (FS) sf[f] = lds_read<f32x4>(s_at, f * Q * 4);
-    else sb[f] = lds_read<uint32_t>(s_at, f * Q * 4);
+    read_tile(b_at, f * 16 * 128, b[f]);
+    if constexpr (FS) sf[f] = lds_read<f32x4>(s_at, f * 16 * 4);
+    else sb[f] = lds_read<uint32_t>(s_at, f * 16 * 4);
   };
   bf16x8 wb[PREC ? FW : 1][4];
   // a stage's exponents of the rows out of their words, and its rows in bfloat16
@@ -267,7 +260,7 @@ gemm8_kernel(F8Product p) {
     }
 #pragma unroll
     for (int j = 0; j < FW; ++j) {
-      sums& to = acc[t][j];
+      f32x4& to = acc[t][j];
       constexpr int B = AK == LQ_E5M2 ? 1 : 0;
       if constexpr (PREC) {
         f32x4 z = FS ? f32x4{} : to;
@@ -277,8 +270,6 @@ gemm8_kernel(F8Product p) {
       } else if constexpr (FS) {
         const f32x4 z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[t % 4], f32x4{}, 0, B, 0, 127, 0, e);
         to += z * sf[j];
-      } else if constexpr (Q == 32) {
-        to = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[j], a[t % 4], to, 0, B, 0, sb[j], 0, e);
       } else {
         to = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a[t % 4], to, 0, B, 0, sb[j], 0, e);
       }
@@ -300,7 +291,7 @@ gemm8_kernel(F8Product p) {
   // nothing; a group without one skips it.
   int slot = 0;
   for (int n = 0; n + 1 < most; ++n) {
-    const int next = slot + 1 == S ? 0 : slot + 1, shift = 8 * (step_of(n) / PER_BLOCK & 3);
+    const int next = slot + 1 == S ? 0 : slot + 1, shift = 8 * (step_of(n) & 3);
     const uint32_t on = static_cast<uint32_t>((next - slot) * P::STAGE);
     begin(shift);
 #pragma unroll
@@ -325,7 +316,7 @@ gemm8_kernel(F8Product p) {
     slot = next;
   }
   if (WK == 1 || mine == most) {
-    const int shift = 8 * (step_of(most - 1) / PER_BLOCK & 3);
+    const int shift = 8 * (step_of(most - 1) & 3);
     begin(shift);
 #pragma unroll
     for (int t = 0; t < FT; ++t) {
@@ -338,7 +329,7 @@ gemm8_kernel(F8Product p) {
   constexpr int LAST = WK == 1 ? FT : FT / 2;
   if constexpr (WK == 2) {
     wait_and_barrier<0>();
-    sums* ex = reinterpret_cast<sums*>(lds) + lane;
+    f32x4* ex = reinterpret_cast<f32x4*>(lds) + lane;
     auto slot_of = [&](int group, int t, int j) { return ((group * GROUP + wg) * LAST + t) * FW + j; };
 #pragma unroll
     for (int t = 0; t < LAST; ++t)
@@ -350,7 +341,7 @@ gemm8_kernel(F8Product p) {
     for (int t = 0; t < LAST; ++t)
 #pragma unroll
       for (int j = 0; j < FW; ++j) {
-        const sums other = ex[slot_of(wk, t, j) * 64];
+        const f32x4 other = ex[slot_of(wk, t, j) * 64];
         acc[t][j] = wk ? other + acc[LAST + t][j] : acc[t][j] + other;
       }
   }
@@ -361,26 +352,23 @@ gemm8_kernel(F8Product p) {
   constexpr int PITCH = P::PITCH, AT_ONCE = P::AT_ONCE;
   if constexpr (WK == 1) wait_and_barrier<0>();
   else __syncthreads();
-  float* ex = reinterpret_cast<float*>(lds) + wave * AT_ONCE * Q * PITCH;
-  const int rows_out = p.gated ? Q * FW / 2 : Q * FW, quads = rows_out / 4;
+  float* ex = reinterpret_cast<float*>(lds) + wave * AT_ONCE * 16 * PITCH;
+  const int rows_out = p.gated ? 16 * FW / 2 : 16 * FW, quads = rows_out / 4;
   const int o_wave = out0 + ww * rows_out;
   const OutputTypes types = output_types(p.out, p.ldo, p.residual, p.ldr, p.out_dt);
   const float* bias = p.bias && slice == 0 ? p.bias + static_cast<int64_t>(expert) * p.m : nullptr;
-  const int wave_token = wt * Q * FT + (WK == 2 && wk ? Q * LAST : 0);
+  const int wave_token = wt * 16 * FT + (WK == 2 && wk ? 16 * LAST : 0);
 #pragma unroll
   for (int f0 = 0; f0 < LAST; f0 += AT_ONCE) {
 #pragma unroll
     for (int t = 0; t < AT_ONCE; ++t)
 #pragma unroll
       for (int j = 0; j < FW; ++j)
-#pragma unroll
-        for (int x = 0; x < NR / 4; ++x)
-          *reinterpret_cast<f32x4*>(ex + (Q * t + c) * PITCH + Q * j + 8 * x + 4 * g) =
-              f32x4{acc[f0 + t][j][4 * x], acc[f0 + t][j][4 * x + 1], acc[f0 + t][j][4 * x + 2], acc[f0 + t][j][4 * x + 3]};
+        *reinterpret_cast<f32x4*>(ex + (16 * t + c) * PITCH + 16 * j + 4 * g) = acc[f0 + t][j];
 #pragma unroll 1
-    for (int x = lane; x < AT_ONCE * Q * quads; x += 64) {
+    for (int x = lane; x < AT_ONCE * 16 * quads; x += 64) {
       const int at_token = x / quads, o_in = x % quads * 4, o = o_wave + o_in, n = min(4, out_m - o);
-      const int token = wave_token + Q * f0 + at_token;
+      const int token = wave_token + 16 * f0 + at_token;
       if (token >= tokens || n <= 0) continue;
       const int64_t row = row0 + token, out_row = row + static_cast<int64_t>(slice) * p.R;
       const Residual res = load_residual(n, types, p.residual, row * p.ldr + o);
@@ -404,7 +392,7 @@ gemm8_kernel(F8Product p) {
       finished(from, o, y);
       activate(y, p.act);
       if (p.gated) {
-        finished(from + Q * FW / 2, half + o, up);
+        finished(from + 16 * FW / 2, half + o, up);
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] *= up[i];
       }
@@ -413,9 +401,9 @@ gemm8_kernel(F8Product p) {
   }
 }
 
-template <int AK, bool FS, bool PREC, int Q, int WT, int WW, int WK, int FT, int FW>
+template <int AK, bool FS, bool PREC, int WT, int WW, int WK, int FT, int FW>
 hipError_t launch(const F8Product& in, hipStream_t st) {
-  using P = Tile<Q, WT, WW, WK, FT, FW>;
+  using P = Tile<WT, WW, WK, FT, FW>;
   F8Product p = in;
   const int64_t outs = p.gated ? P::ROWS / 2 : P::ROWS, out_m = p.gated ? p.m / 2 : p.m;
   p.row_blocks = static_cast<int>((out_m + outs - 1) / outs);
@@ -424,7 +412,7 @@ hipError_t launch(const F8Product& in, hipStream_t st) {
   p.token_tiles = static_cast<int>(tiles);
   const int64_t grid = (tiles * p.row_blocks * p.slices + 7) / 8 * 8;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  auto* k = gemm8_kernel<AK, FS, PREC, Q, WT, WW, WK, FT, FW>;
+  auto* k = gemm8_kernel<AK, FS, PREC, WT, WW, WK, FT, FW>;
   // per call: the attribute belongs to the current device
   const hipError_t big = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, P::LDS);
@@ -440,17 +428,19 @@ hipError_t launch(const F8Product& in, hipStream_t st) {
   return hipSuccess;
 }
 
-template <int AK, bool FS>
-hipError_t by_shape(const F8Product& p, const F8ManyPlan& plan, bool precise, hipStream_t st) {
-  if (precise) return plan.big ? launch<AK, FS, true, 16, 4, 2, 1, 4, 4>(p, st) : launch<AK, FS, true, 16, 2, 2, 2, 4, 4>(p, st);
-  if (!plan.big) return launch<AK, FS, false, 16, 2, 2, 2, 4, 4>(p, st);
-  if constexpr (FS) return launch<AK, FS, false, 16, 4, 2, 1, 4, 4>(p, st);
-  else return launch<AK, FS, false, 16, 2, 4, 1, 8, 4>(p, st);
+template <int AK, bool FS, bool PREC>
+hipError_t by_shape(const F8Product& p, int shape, hipStream_t st) {
+  if constexpr (!FS && !PREC) {
+    if (shape == kSquare) return launch<AK, FS, PREC, 2, 4, 1, 8, 4>(p, st);
+    if (shape == kTall) return launch<AK, FS, PREC, 2, 4, 1, 4, 4>(p, st);
+  }
+  return shape == kPair ? launch<AK, FS, PREC, 2, 2, 1, 4, 4>(p, st) : launch<AK, FS, PREC, 2, 2, 2, 4, 4>(p, st);
 }
 
 template <int AK>
-hipError_t by_scales(const F8Product& p, const F8ManyPlan& plan, bool precise, hipStream_t st) {
-  return p.float_scales ? by_shape<AK, true>(p, plan, precise, st) : by_shape<AK, false>(p, plan, precise, st);
+hipError_t by_scales(const F8Product& p, int shape, bool precise, hipStream_t st) {
+  if (precise) return p.float_scales ? by_shape<AK, true, true>(p, shape, st) : by_shape<AK, false, true>(p, shape, st);
+  return p.float_scales ? by_shape<AK, true, false>(p, shape, st) : by_shape<AK, false, false>(p, shape, st);
 }
 
 }  // namespace
@@ -465,10 +455,25 @@ F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
     const int64_t tiles = grouped ? R / tok + (runs + 1) / 2 : (R + tok - 1) / tok;
     return tiles * ((out_m + outs - 1) / outs);
   };
-  p.big = count(256, precise ? 128 : 256) >= cus;
+  // Tiles of tokens x rows, measured on each side.  Where exponents alone are applied by
+  // the matrix instruction: 256 x 256 in eight waves where every unit has one (4096 x 4096 ->
+  // 2 x 14336: 428 us; 128 x 256 533, 128 x 128 521; 2048 x 8192 -> 8192: 117; 140; 149), of
+  // runs only of long ones (16384 rows of 64 experts, 2048 -> 2 x 1408: 200; 128 x 256
+  // 192); then 128 x 256.  Float32 scales or results: 128 x 128 in four waves, two
+  // workgroups on a unit (4096 x 4096 -> 2 x 14336 with float32 scales 552, 128 x 256 588;
+  // to float32 803, 869).  Where there is about one such tile per unit or less, eight waves
+  // share it and split its positions (512 x 8192 -> 8192: 55; four waves 63; 1024 x
+  // 4096 -> 4096: 25; 31).
+  const bool quick = !float_scales && !precise;
+  if (quick && count(256, 256) >= cus && R >= 1024 * (grouped ? runs : 0)) p.shape = kSquare;
+  else if (quick && count(128, 256) * 5 >= cus * 4) p.shape = kTall;
+  else if (count(128, 128) * 4 > cus * 5) p.shape = kPair;
+  else p.shape = kOne;
+  // Where tiles leave units without one, the positions are split, down to 1024 a
+  // slice (777 x 5125 -> 1281: one 28, three 22; 64 x 14336 -> 4096: one 67, eight 22).
   p.slices = 1;
   const int64_t tiles = count(128, 128);
-  if (!p.big && tiles < cus) {
+  if (p.shape == kOne && tiles < cus) {
     p.slices = static_cast<int>(cus / tiles);
     if (p.slices > steps / 8) p.slices = static_cast<int>(steps / 8);
     if (p.slices > 16) p.slices = 16;
@@ -480,7 +485,8 @@ F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
 }
 
 hipError_t launch_gemm8(const F8Product& p, int a_type, const F8ManyPlan& plan, bool precise, hipStream_t st) {
-  return a_type == LQ_E5M2 ? by_scales<LQ_E5M2>(p, plan, precise, st) : by_scales<LQ_E4M3>(p, plan, precise, st);
+  return a_type == LQ_E5M2 ? by_scales<LQ_E5M2>(p, plan.shape, precise, st)
+                           : by_scales<LQ_E4M3>(p, plan.shape, precise, st);
 }
 
 }  // namespace lq

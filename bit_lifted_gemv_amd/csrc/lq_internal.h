@@ -295,8 +295,9 @@ F8FewPlan few_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bo
 hipError_t launch_gemv8(const F8Product& p, int a_type, const F8FewPlan& plan, bool precise,
                         hipStream_t st);
 // Many (k_gemm8.hip), 8-bit activations.  precise: float32 results.
+enum F8Shape { kSquare, kTall, kPair, kOne };   // tiles, see many_f8_plan
 struct F8ManyPlan {
-  int big;                     // the large tile of the variant, or 128 x 128
+  int shape;
   int slices, slice_steps;
 };
 F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bool grouped,
