@@ -99,34 +99,26 @@ __device__ __forceinline__ float value16(uint32_t bits, int dt) {
   return dt == LQ_F16 ? f16_bits_to_float(b) : bf16_bits_to_float(b);
 }
 
-// `wide`: four consecutive outputs go in one access of 8 or 16 bytes.
-struct OutputTypes {
-  int dt;
-  bool wide;
-};
-__host__ __device__ __forceinline__ OutputTypes output_types(const void* out, int64_t ldo,
-                                                             const void* residual, int64_t ldr,
-                                                             int dt) {
-  const uint64_t esz = dt == LQ_F32 ? 4 : 2;
-  uint64_t bits = reinterpret_cast<uint64_t>(out) | static_cast<uint64_t>(ldo) * esz;
-  if (residual) bits |= reinterpret_cast<uint64_t>(residual) | static_cast<uint64_t>(ldr) * esz;
-  return {dt, bits % (4 * esz) == 0};
-}
+// Four outputs in one access of 8 or 16 bytes, at any address (global memory takes them).
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 // The residual of four columns of one token, the first n of them inside, as
 // it lies in memory (its conversion waits for its arrival).
 struct Residual {
   uint32_t w[4];
 };
-__device__ __forceinline__ Residual load_residual(int n, const OutputTypes& types,
+__device__ __forceinline__ Residual load_residual(int n, int dt,
                                                   const void* residual, int64_t at) {
   Residual r{};
   if (!residual || n <= 0) return r;
-  if (types.dt == LQ_F32) {
+  if (dt == LQ_F32) {
     const auto* p = static_cast<const uint32_t*>(residual) + at;
-    if (types.wide && n == 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    if (n == 4) {
+      const u32x4 v = *reinterpret_cast<const u32x4_any*>(p);
+      r.w[0] = v[0]; r.w[1] = v[1]; r.w[2] = v[2]; r.w[3] = v[3];
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -134,9 +126,9 @@ __device__ __forceinline__ Residual load_residual(int n, const OutputTypes& type
     }
   } else {
     const auto* p = static_cast<const uint16_t*>(residual) + at;
-    if (types.wide && n == 4) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      r.w[0] = v.x; r.w[1] = v.y;
+    if (n == 4) {
+      const u32x2 v = *reinterpret_cast<const u32x2_any*>(p);
+      r.w[0] = v[0]; r.w[1] = v[1];
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -147,16 +139,17 @@ __device__ __forceinline__ Residual load_residual(int n, const OutputTypes& type
 }
 
 // Adds the residual to y and stores the first n of four outputs.
-__device__ __forceinline__ void store4(float (&y)[4], int n, const OutputTypes& types,
+__device__ __forceinline__ void store4(float (&y)[4], int n, int dt,
                                        const Residual& r, bool add, void* out, int64_t at) {
-  if (types.dt == LQ_F32) {
+  if (dt == LQ_F32) {
     if (add) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) y[c] += __uint_as_float(r.w[c]);
     }
     float* to = static_cast<float*>(out) + at;
-    if (types.wide && n == 4) {
-      *reinterpret_cast<float4*>(to) = make_float4(y[0], y[1], y[2], y[3]);
+    if (n == 4) {
+      *reinterpret_cast<u32x4_any*>(to) = u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]),
+                                                __float_as_uint(y[2]), __float_as_uint(y[3])};
     } else {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -166,24 +159,23 @@ __device__ __forceinline__ void store4(float (&y)[4], int n, const OutputTypes& 
   }
   if (add) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] += value16(r.w[c / 2] >> (16 * (c % 2)), types.dt);
+    for (int c = 0; c < 4; ++c) y[c] += value16(r.w[c / 2] >> (16 * (c % 2)), dt);
   }
-  const uint2 v = make_uint2(round16x2(y[0], y[1], types.dt), round16x2(y[2], y[3], types.dt));
+  const u32x2 v = {round16x2(y[0], y[1], dt), round16x2(y[2], y[3], dt)};
   uint16_t* to = static_cast<uint16_t*>(out) + at;
-  if (types.wide && n == 4) {
-    *reinterpret_cast<uint2*>(to) = v;
+  if (n == 4) {
+    *reinterpret_cast<u32x2_any*>(to) = v;
   } else {
-    const uint32_t w[2] = {v.x, v.y};
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (c < n) to[c] = static_cast<uint16_t>(w[c / 2] >> (16 * (c % 2)));
+      if (c < n) to[c] = static_cast<uint16_t>(v[c / 2] >> (16 * (c % 2)));
   }
 }
 
-__device__ __forceinline__ void finish4(float (&y)[4], int n, const OutputTypes& types,
+__device__ __forceinline__ void finish4(float (&y)[4], int n, int dt,
                                         const void* residual, int64_t at_residual, void* out,
                                         int64_t at) {
-  store4(y, n, types, load_residual(n, types, residual, at_residual), residual != nullptr, out, at);
+  store4(y, n, dt, load_residual(n, dt, residual, at_residual), residual != nullptr, out, at);
 }
 
 }  // namespace f6

@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(128) f6_reduce_kernel(F6Product a) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] *= up[j];
   }
-  finish4(y, n, output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt), a.residual,
+  finish4(y, n, a.out_dt, a.residual,
           row * a.ldr + o, a.out, row * a.ldo + o);
 }
 

@@ -355,7 +355,6 @@ gemm8_kernel(F8Product p) {
   float* ex = reinterpret_cast<float*>(lds) + wave * AT_ONCE * 16 * PITCH;
   const int rows_out = p.gated ? 16 * FW / 2 : 16 * FW, quads = rows_out / 4;
   const int o_wave = out0 + ww * rows_out;
-  const OutputTypes types = output_types(p.out, p.ldo, p.residual, p.ldr, p.out_dt);
   const float* bias = p.bias && slice == 0 ? p.bias + static_cast<int64_t>(expert) * p.m : nullptr;
   const int wave_token = wt * 16 * FT + (WK == 2 && wk ? 16 * LAST : 0);
 #pragma unroll
@@ -371,7 +370,7 @@ gemm8_kernel(F8Product p) {
       const int token = wave_token + 16 * f0 + at_token;
       if (token >= tokens || n <= 0) continue;
       const int64_t row = row0 + token, out_row = row + static_cast<int64_t>(slice) * p.R;
-      const Residual res = load_residual(n, types, p.residual, row * p.ldr + o);
+      const Residual res = load_residual(n, p.out_dt, p.residual, row * p.ldr + o);
       bool live = true;
       if (p.rows) {
         const int r = p.rows[row];
@@ -396,7 +395,7 @@ gemm8_kernel(F8Product p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] *= up[i];
       }
-      store4(y, n, types, res, p.residual != nullptr, p.out, out_row * p.ldo + o);
+      store4(y, n, p.out_dt, res, p.residual != nullptr, p.out, out_row * p.ldo + o);
     }
   }
 }
@@ -434,7 +433,10 @@ hipError_t by_shape(const F8Product& p, int shape, hipStream_t st) {
     if (shape == kSquare) return launch<AK, FS, PREC, 2, 4, 1, 8, 4>(p, st);
     if (shape == kTall) return launch<AK, FS, PREC, 2, 4, 1, 4, 4>(p, st);
   }
-  return shape == kPair ? launch<AK, FS, PREC, 2, 2, 1, 4, 4>(p, st) : launch<AK, FS, PREC, 2, 2, 2, 4, 4>(p, st);
+  if (shape == kPair) return launch<AK, FS, PREC, 2, 2, 1, 4, 4>(p, st);
+  // float32 results convert each operand in every wave that reads it: larger pieces of the tile
+  if constexpr (PREC) return launch<AK, FS, PREC, 2, 2, 2, 4, 4>(p, st);
+  else return launch<AK, FS, PREC, 2, 4, 1, 4, 2>(p, st);
 }
 
 template <int AK>
@@ -462,8 +464,9 @@ F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
   // 192); then 128 x 256.  Float32 scales or results: 128 x 128 in four waves, two
   // workgroups on a unit (4096 x 4096 -> 2 x 14336 with float32 scales 552, 128 x 256 588;
   // to float32 803, 869).  Where there is about one such tile per unit or less, eight waves
-  // share it and split its positions (512 x 8192 -> 8192: 55; four waves 63; 1024 x
-  // 4096 -> 4096: 25; 31).
+  // share it, 64 x 32 each (512 x 8192 -> 8192: 46; four waves 63); for float32 results four
+  // waves for every other block of positions, so that each operand is converted half as
+  // often (71; 64 x 32 each 80; four waves 80).
   const bool quick = !float_scales && !precise;
   if (quick && count(256, 256) >= cus && R >= 1024 * (grouped ? runs : 0)) p.shape = kSquare;
   else if (quick && count(128, 256) * 5 >= cus * 4) p.shape = kTall;

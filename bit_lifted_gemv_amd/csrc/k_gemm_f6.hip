@@ -334,7 +334,6 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
   const int n = min(4, out_m - (out0 + o));
   const int strip = a.gated ? o / 64 : o / 128;
   const float* z0 = ex32 + strip * 32 * P::PITCH + (a.gated ? o % 64 : o % 128);
-  const OutputTypes types = output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt);
   const RowScales rs = row_scales(s, bias, out0 + o, a.m);
   RowScales up = rs;
   if (a.gated) up = row_scales(s, bias, half_m + out0 + o, a.m);
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
     for (int c = 0; c < CHUNK; ++c) {
       const int token = 32 * t + tk + c * tk_step;
       const bool live = tk + c * tk_step < 32 && token < tokens;
-      r[c] = load_residual(live ? n : 0, types, a.residual, (slice_row + token) * a.ldr + out0 + o);
+      r[c] = load_residual(live ? n : 0, a.out_dt, a.residual, (slice_row + token) * a.ldr + out0 + o);
     }
   };
 #pragma unroll
@@ -389,7 +388,7 @@ __global__ void __launch_bounds__(64 * WR * WK, 2) gemm_f6_kernel(F6Product a) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) y[j] *= g[j];
         }
-        store4(y, n, types, r[c], a.residual != nullptr, a.out,
+        store4(y, n, a.out_dt, r[c], a.residual != nullptr, a.out,
                (slice_row + 32 * t + token) * a.ldo + out0 + o);
       }
 #pragma unroll

@@ -211,7 +211,6 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
     for (int i = 0; i < 4; ++i) lds[(wave * TOK + 4 * g + i) * PITCH + 16 * f + c16] = acc[f][i];
   __syncthreads();
   const int quads = outs / 4;
-  const OutputTypes types = output_types(p.out, p.ldo, p.residual, p.ldr, p.out_dt);
   const float* bias = p.bias && slice == 0 ? p.bias + static_cast<int64_t>(expert) * p.m : nullptr;
   for (int x = tid; x < quads * tokens; x += blockDim.x) {
     const int token = x / quads, o = (x - token * quads) * 4, n = min(4, out_m - (out0 + o));
@@ -252,7 +251,7 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[i] *= up[i];
     }
-    finish4(y, n, types, p.residual, row * p.ldr + out0 + o, p.out, row * p.ldo + out0 + o);
+    finish4(y, n, p.out_dt, p.residual, row * p.ldr + out0 + o, p.out, row * p.ldo + out0 + o);
   }
 }
 

@@ -240,7 +240,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
   const uint32_t two = held(0x22222222u);
   const uint8_t* mine = lds + min(i16, tokens - 1) * GB;
   f32x4* exchange = reinterpret_cast<f32x4*>(lds + f.exchange_at);
-  const OutputTypes types = output_types(a.out, a.ldo, a.residual, a.ldr, a.out_dt);
 
   for (int rb = b0; rb < b1; ++rb) {
     f32x4 acc[T] = {};
@@ -304,7 +303,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2) gemv_f6_kernel(F6Few f) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) y[c] *= up[c];
       }
-      finish4(y, left, types, a.residual, row * a.ldr + o, a.out, row * a.ldo + o);
+      finish4(y, left, a.out_dt, a.residual, row * a.ldr + o, a.out, row * a.ldo + o);
     }
   }
 }

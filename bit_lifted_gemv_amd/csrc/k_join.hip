@@ -16,7 +16,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ z, 
                                                    int m, const int* __restrict__ pos,
                                                    const float* __restrict__ weight, int T, int k,
                                                    const void* residual, int64_t ldr, void* out,
-                                                   int64_t ldo, int ldz, f6::OutputTypes types) {
+                                                   int64_t ldo, int ldz, int out_dt) {
   const int o = (blockIdx.x * 256 + threadIdx.x) * 4;
   if (o >= m) return;
   const int64_t step = static_cast<int64_t>(R) * ldz;
@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(256) join_kernel(const float* __restrict__ z, 
         y[3] += w[x] * v[x].w;
       }
     }
-    f6::finish4(y, min(4, m - o), types, residual, t * ldr + o, out, t * ldo + o);
+    f6::finish4(y, min(4, m - o), out_dt, residual, t * ldr + o, out, t * ldo + o);
   }
 }
 
@@ -59,7 +59,7 @@ hipError_t launch_join(const float* z, int slices, int64_t R, int64_t m, int64_t
   join_kernel<<<grid, 256, 0, st>>>(z, slices, static_cast<int>(R), static_cast<int>(m), pos, weight,
                                     static_cast<int>(T), k, residual, ldr, out, ldo,
                                     static_cast<int>(ldz),
-                                    f6::output_types(out, ldo, residual, ldr, dt));
+                                    dt);
   return hipGetLastError();
 }
 
