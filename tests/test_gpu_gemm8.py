@@ -157,6 +157,43 @@ def test_epilogue(m, K, B, dtype, kind, act, out):
         check(w, a, None, act, gated, None, out)
 
 
+# one size at least for every tile that the products are computed on, with one and several slices of the positions
+TILES = [(4096, 300, 4000), (4096, 300, 2048), (129, 200, 21760), (1000, 260, 2000), (130, 5000, 40), (2048, 700, 260), (31, 20000, 3)]
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("kind", [torch.uint8, F32])
+@pytest.mark.parametrize("dtype", [E4M3, E5M2])
+@pytest.mark.parametrize("m,K,B", TILES)
+def test_every_tile(m, K, B, dtype, kind, out):
+    g = torch.Generator().manual_seed(3)
+    w, a = weights(m, K, kind, 1), activations(B, K, dtype, 2)
+    bias, residual = torch.randn(m, generator=g).cuda(), torch.randn(B, m, generator=g).to(out).cuda()
+    check(w, a, bias, "gelu", False, residual, out)
+    if m % 2 == 0:
+        w = lq.Blocks8(w.values, w.scales / 64) if kind == F32 else w
+        check(w, a, bias, "relu", True, residual[:, :m // 2], out)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("B,K", [(1, 512), (3, 1000), (4, 2048), (1, 333), (20, 640), (200, 333)])
+def test_the_identity_gives_the_quantized_values(B, K, dtype):
+    """Weights of 1 on the diagonal: every output is one activation as it was quantized, bit for bit."""
+    eye = lq.quantize8_blocks(torch.eye(K).cuda())
+    g = torch.Generator().manual_seed(B + K)
+    a = torch.randn(B, K, generator=g) * torch.exp(3 * torch.randn(B, (K + 127) // 128, generator=g)).repeat_interleave(128, 1)[:, :K]
+    a[0, :128] *= 2.0**-14 if dtype == F16 else 2.0**-100
+    a = a.to(dtype).cuda()
+    want = rows64(lq.quantize8(a))[:, :K]
+    assert torch.equal(lq.gemm8(eye, a, out_dtype=F32).double(), want)
+    a[B - 1, 5] = float("inf")                                   # e4m3 has none: a NaN, and the block's scale is that of the others
+    q = lq.quantize8(a)
+    clean = torch.where(torch.isnan(q.values.float()), torch.zeros_like(q.values.float()), q.values.float()).to(E4M3)
+    rest = torch.arange(B, device="cuda") != B - 1
+    got = lq.gemm8(eye, a, out_dtype=F32)
+    assert torch.isnan(got[B - 1]).all() and torch.equal(got[rest].double(), rows64(lq.Rows8(clean, q.exps))[rest, :K])
+
+
 def routing(T, E, k, seed, skew=1.0, padded=0.0):
     g = torch.Generator().manual_seed(seed)
     logits = torch.randn(T, E, generator=g) + torch.randn(E, generator=g) * skew
@@ -190,7 +227,9 @@ def check_grouped(w, a, offsets, rows=None, bias=None, act="none", gated=False, 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("E,k,T,m,K,gated", [(4, 1, 1, 64, 128, False), (64, 8, 1, 96, 300, True), (8, 2, 24, 200, 1000, False),
                                              (64, 8, 40, 130, 257, True), (3, 2, 300, 384, 640, True), (130, 4, 500, 64, 200, False),
-                                             (8, 2, 2000, 256, 512, True), (2, 1, 5, 1000, 4096, False)])
+                                             (8, 2, 2000, 256, 512, True), (2, 1, 5, 1000, 4096, False),
+                                             (70, 2, 900, 130, 300, True), (2, 1, 4000, 8192, 200, False),
+                                             (16, 2, 3000, 640, 1100, True)])
 def test_experts(E, k, T, m, K, gated, dtype, kind):
     r = routing(T, E, k, T + E, padded=0.1)
     w = weights(m, K, kind, E + m, E=E)
@@ -207,15 +246,16 @@ def test_runs_that_are_empty_or_leave_rows():
         check_grouped(w, a, torch.tensor(ends, dtype=torch.int32, device="cuda"))
 
 
-def test_row_indices_out_of_range_are_rows_of_zeros():
+@pytest.mark.parametrize("repeats", [1, 3, 40])
+def test_row_indices_out_of_range_are_rows_of_zeros(repeats):
     w = weights(40, 200, F32, 1, E=2)
     a = activations(10, 200, E4M3, 2)
     a.values.view(torch.uint8)[0, 3] = 0x7F                     # a NaN in row 0, which nobody asks for
-    rows = torch.tensor([3, -1, 10, 5, 2**31 - 1, -2**31, 9, 1], dtype=torch.int32, device="cuda")
+    rows = torch.tensor([3, -1, 10, 5, 2**31 - 1, -2**31, 9, 1] * repeats, dtype=torch.int32, device="cuda")
     bias = torch.randn(2, 40, device="cuda")
     clean = lq.Rows8(a.values.clone(), a.exps)
     clean.values.view(torch.uint8)[0, 3] = 0
-    offsets = torch.tensor([0, 3, 8], dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([0, 3, 8 * repeats], dtype=torch.int32, device="cuda")
     want = check_grouped(w, clean, offsets, rows, bias)
     assert torch.equal(lq.gemm8_grouped(w, a, offsets, rows=rows, bias=bias, out_dtype=F32), want)
 
@@ -347,3 +387,35 @@ def test_captured_and_replayed(B):
         for _, out in graphs:
             for x, y in zip(out, eager):
                 assert torch.equal(x, y)
+
+
+def test_no_rows():
+    w = weights(40, 200, torch.uint8, 1, E=2)
+    offsets = torch.zeros(3, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    for a in (activations(5, 200, E4M3, 1), activations(5, 200, F16, 1)):
+        assert lq.gemm8_grouped(w, a, offsets, rows=none).shape == (0, 40)
+        out = torch.full((5, 40), 3.0, device="cuda")
+        assert (lq.gemm8_grouped(w, a, offsets, out=out) == 3.0).all()      # runs without rows
+    assert lq.gemm8_grouped(w, torch.empty(0, 200, dtype=F16, device="cuda"), offsets).shape == (0, 40)
+    with pytest.raises(lq.LQError):
+        lq.gemm8(lq.Blocks8(w.values[0], w.scales[0]), torch.empty(0, 200, dtype=F16, device="cuda"))
+
+
+def test_one_expert_takes_all_rows_and_indices_repeat():
+    w = weights(96, 300, torch.uint8, 1, E=5)
+    a = activations(3, 300, E4M3, 2)
+    rows = torch.tensor([2, 2, 0, 2, 1] * 60, dtype=torch.int32, device="cuda")
+    for ends in ([0, 0, 300, 300, 300, 300], [0, 300, 300, 300, 300, 300], [0, 0, 0, 0, 0, 300]):
+        check_grouped(w, a, torch.tensor(ends, dtype=torch.int32, device="cuda"), rows)
+
+
+def test_many_rows_of_few_tokens():
+    """More rows than a launch has threads for, from three tokens: tiles and offsets stay whole."""
+    R = 2**24 + 77
+    w = weights(2, 128, torch.uint8, 1, E=1)
+    a = activations(3, 128, E4M3, 2)
+    rows = (torch.arange(R, device="cuda") % 3).to(torch.int32)
+    out = lq.gemm8_grouped(w, a, torch.tensor([0, R], dtype=torch.int32, device="cuda"), rows=rows, out_dtype=F16)
+    want = lq.gemm8(lq.Blocks8(w.values[0], w.scales[0]), a, out_dtype=F16)
+    assert torch.equal(out, want[rows.long()])

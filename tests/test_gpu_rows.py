@@ -61,6 +61,24 @@ def test_sort(T, E, k, n, dtype):
     assert torch.equal(bytes_(got), plain_sort(bytes_(x).view(T, -1), r.rows))
 
 
+def test_offsets_past_32_bits():
+    """Rows whose bytes lie past 2^32, and columns wider than a workgroup's pass."""
+    n, R = 2**21 + 3, 1100
+    x = torch.zeros(2, n, dtype=torch.uint8, device="cuda")
+    x[0], x[1] = 3, 5
+    rows = torch.zeros(R, dtype=torch.int32, device="cuda")
+    rows[-1] = 1
+    out = lq.sort_rows(x, rows, out=torch.empty(R, 2**22, dtype=torch.uint8, device="cuda")[:, :n])
+    assert (out[-1] == 5).all() and (out[-2] == 3).all() and (out[0] == 3).all()
+    z = torch.empty(R, 2**21, dtype=F16, device="cuda")
+    z[-1], z[0] = 2.0, 1.0
+    pos = torch.tensor([[R - 1, 0]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[0.5, 3.0]], device="cuda")
+    assert (lq.join_rows(z, pos, w) == 4.0).all()
+    dz, dw = lq.join_rows_grad(torch.ones(1, 2**21, dtype=F16, device="cuda"), z, pos, w)
+    assert (dz[-1] == 0.5).all() and (dz[0] == 3.0).all() and dw.tolist() == [[2.0**22, 2.0**21]]
+
+
 def test_sort_of_indices_out_of_range_and_repeated():
     x = values(5, 70, BF16, 1)
     rows = torch.tensor([4, -1, 5, 4, 2**31 - 1, -2**31, 0, 4], dtype=torch.int32)
