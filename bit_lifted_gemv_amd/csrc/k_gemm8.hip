@@ -94,6 +94,8 @@ struct Tile {
   static_assert(WK <= 2 && S >= 2 && TOK >= 64 && ROWS >= 64 && FT >= 4 && S * LOADS < 64);
   static_assert(TOK / 64 + ROWS / 64 <= GROUP);                 // one wave for each 64 exponents or scales
   static_assert(WK == 1 || GROUP * FT * FW * 1024 <= LDS);           // the groups' sums change hands there
+  // a word of exponents is loaded S WK blocks ahead, over one whose blocks are behind: not more than four
+  static_assert(S * WK <= 4);
 };
 
 template <int AK, bool FS, bool PREC, int WT, int WW, int WK, int FT, int FW>

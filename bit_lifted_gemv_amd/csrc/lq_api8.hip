@@ -66,7 +66,7 @@ Plan8 plan8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_t a_rows, i
   Plan8 p{};
   const int64_t runs = grouped ? (E < R ? E : R < 1 ? 1 : R) : 1;
   p.few = R <= kFewRowsPerRun * runs;
-    p.fp = lq::few_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped);
+  p.fp = lq::few_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped);
   p.mp = lq::many_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped, float_scales, precise);
   p.slices = p.few ? p.fp.slices : p.mp.slices;
   p.ldq = whole(K);
