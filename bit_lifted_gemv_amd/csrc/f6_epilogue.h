@@ -138,14 +138,19 @@ __device__ __forceinline__ Residual load_residual(int n, int dt,
   return r;
 }
 
-// Adds the residual to y and stores the first n of four outputs.
-__device__ __forceinline__ void store4(float (&y)[4], int n, int dt,
-                                       const Residual& r, bool add, void* out, int64_t at) {
+__device__ __forceinline__ void add_residual(float (&y)[4], int dt, const Residual& r) {
   if (dt == LQ_F32) {
-    if (add) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) y[c] += __uint_as_float(r.w[c]);
-    }
+    for (int c = 0; c < 4; ++c) y[c] += __uint_as_float(r.w[c]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] += value16(r.w[c / 2] >> (16 * (c % 2)), dt);
+  }
+}
+
+// The first n of four outputs.
+__device__ __forceinline__ void store4(const float (&y)[4], int n, int dt, void* out, int64_t at) {
+  if (dt == LQ_F32) {
     float* to = static_cast<float*>(out) + at;
     if (n == 4) {
       *reinterpret_cast<u32x4_any*>(to) = u32x4{__float_as_uint(y[0]), __float_as_uint(y[1]),
@@ -157,10 +162,6 @@ __device__ __forceinline__ void store4(float (&y)[4], int n, int dt,
     }
     return;
   }
-  if (add) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] += value16(r.w[c / 2] >> (16 * (c % 2)), dt);
-  }
   const u32x2 v = {round16x2(y[0], y[1], dt), round16x2(y[2], y[3], dt)};
   uint16_t* to = static_cast<uint16_t*>(out) + at;
   if (n == 4) {
@@ -170,6 +171,13 @@ __device__ __forceinline__ void store4(float (&y)[4], int n, int dt,
     for (int c = 0; c < 4; ++c)
       if (c < n) to[c] = static_cast<uint16_t>(v[c / 2] >> (16 * (c % 2)));
   }
+}
+
+// Adds the residual to y and stores the first n of four outputs.
+__device__ __forceinline__ void store4(float (&y)[4], int n, int dt,
+                                       const Residual& r, bool add, void* out, int64_t at) {
+  if (add) add_residual(y, dt, r);
+  store4(y, n, dt, out, at);
 }
 
 __device__ __forceinline__ void finish4(float (&y)[4], int n, int dt,

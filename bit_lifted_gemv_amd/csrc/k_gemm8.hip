@@ -89,7 +89,7 @@ struct Tile {
   static constexpr int MAX_LDS = 163840 / (PER_SIMD * 4 / NW);  // workgroups of a compute unit
   static constexpr int RING = (MAX_LDS / WK - BEHIND) / STAGE, S = RING > 4 ? 4 : RING;
   static constexpr int PART = S * STAGE + BEHIND, LDS = WK * PART;   // of a group, of all
-  static constexpr int PITCH = 16 * FW + 4, AT_ONCE = 2;   // of the sums on their way out
+  static constexpr int PITCH = 16 * FW + 4, AT_ONCE = 8 / FW;   // of the sums on their way out
   static_assert(NW * AT_ONCE * 16 * PITCH * 4 <= LDS);
   static_assert(WK <= 2 && S >= 2 && TOK >= 64 && ROWS >= 64 && FT >= 4 && S * LOADS < 64);
   static_assert(TOK / 64 + ROWS / 64 <= GROUP);                 // one wave for each 64 exponents or scales
@@ -348,17 +348,39 @@ gemm8_kernel(F8Product p) {
       }
   }
 
-  // ---- the end: two token tiles at a time through the wave's own part of LDS, [token][row],
-  // so that its loop over them is short (unrolled over the sums' registers it would be 100 KB of
-  // code, fetched once per tile: 15 us of each instead of 5) and its stores are whole runs
-  constexpr int PITCH = P::PITCH, AT_ONCE = P::AT_ONCE;
+  // ---- the end: AT_ONCE token tiles at a time through the wave's own part of LDS, [token][row],
+  // so that its stores are whole runs and its code short (unrolled over all the sums it would be
+  // 100 KB, fetched once per tile: 15 us of each).  Without a residual no load stands between
+  // the stores: a wait for one is a wait for the stores before it.
+  constexpr int PITCH = P::PITCH, AT_ONCE = P::AT_ONCE, MASKS = (LAST + 3) / 4, G = 4;
+  const int wave_token = wt * 16 * FT + (WK == 2 && wk ? 16 * LAST : 0);
+  uint64_t live[MASKS];                                  // of the wave's tokens: whether their index is one
+#pragma unroll
+  for (int i = 0; i < MASKS; ++i) {
+    const int token = wave_token + 64 * i + lane;
+    int r = 0;
+    if (p.rows && token < tokens) r = p.rows[row0 + token];
+    live[i] = __ballot(r >= 0 && r < p.a_rows);
+  }
+  // a lane keeps its four columns and goes through the tokens
+  const int shift = (FW == 4 ? 4 : 3) - (p.gated ? 1 : 0), apart = 64 >> shift, first = lane >> shift;
+  const int o_in = (lane & ((1 << shift) - 1)) * 4, o = out0 + ww * (p.gated ? 16 * FW / 2 : 16 * FW) + o_in;
+  const int n = min(4, out_m - o);
+  float bias[4] = {}, bias_up[4] = {};
+  if (p.bias && slice == 0) {
+    const float* from = p.bias + static_cast<int64_t>(expert) * p.m + o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < n) bias[i] = from[i];
+      if (i < n && p.gated) bias_up[i] = from[half + i];
+    }
+  }
+  // (they have arrived before the stores begin)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(bias[i]), "+v"(bias_up[i]));
   if constexpr (WK == 1) wait_and_barrier<0>();
   else __syncthreads();
   float* ex = reinterpret_cast<float*>(lds) + wave * AT_ONCE * 16 * PITCH;
-  const int rows_out = p.gated ? 16 * FW / 2 : 16 * FW, quads = rows_out / 4;
-  const int o_wave = out0 + ww * rows_out;
-  const float* bias = p.bias && slice == 0 ? p.bias + static_cast<int64_t>(expert) * p.m : nullptr;
-  const int wave_token = wt * 16 * FT + (WK == 2 && wk ? 16 * LAST : 0);
 #pragma unroll
   for (int f0 = 0; f0 < LAST; f0 += AT_ONCE) {
 #pragma unroll
@@ -366,38 +388,47 @@ gemm8_kernel(F8Product p) {
 #pragma unroll
       for (int j = 0; j < FW; ++j)
         *reinterpret_cast<f32x4*>(ex + (16 * t + c) * PITCH + 16 * j + 4 * g) = acc[f0 + t][j];
+    const uint64_t alive = live[f0 / 4] >> (16 * (f0 % 4));
 #pragma unroll 1
-    for (int x = lane; x < AT_ONCE * 16 * quads; x += 64) {
-      const int at_token = x / quads, o_in = x % quads * 4, o = o_wave + o_in, n = min(4, out_m - o);
-      const int token = wave_token + 16 * f0 + at_token;
-      if (token >= tokens || n <= 0) continue;
-      const int64_t row = row0 + token, out_row = row + static_cast<int64_t>(slice) * p.R;
-      const Residual res = load_residual(n, p.out_dt, p.residual, row * p.ldr + o);
-      bool live = true;
-      if (p.rows) {
-        const int r = p.rows[row];
-        live = r >= 0 && r < p.a_rows;
+    for (int at0 = first; at0 < AT_ONCE * 16; at0 += G * apart) {
+      const int token0 = wave_token + 16 * f0 + at0;
+      auto inside = [&](int i) { return token0 + i * apart < tokens ? n : 0; };
+      Residual res[G];
+      if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+          res[i] = load_residual(inside(i), p.out_dt, p.residual,
+                                 static_cast<int64_t>(row0 + token0 + i * apart) * p.ldr + o);
       }
-      const float* from = ex + at_token * PITCH + o_in;
-      auto finished = [&](const float* z4, int o_bias, float (&y)[4]) {
-        const f32x4 z = *reinterpret_cast<const f32x4*>(z4);
+      auto finished = [&](int column, const float (&b)[4], float (&y)[4 * G]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = live ? z[i] : 0.f;
-        if (bias) {
+        for (int i = 0; i < G; ++i) {
+          const f32x4 z = *reinterpret_cast<const f32x4*>(ex + (at0 + i * apart) * PITCH + column);
+          const bool is = alive >> (at0 + i * apart) & 1;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < n) y[i] += bias[o_bias + i];
+          for (int j = 0; j < 4; ++j) y[4 * i + j] = (is ? z[j] : 0.f) + b[j];
         }
       };
-      float y[4], up[4];
-      finished(from, o, y);
+      float y[4 * G];
+      finished(o_in, bias, y);
       activate(y, p.act);
       if (p.gated) {
-        finished(from + 16 * FW / 2, half + o, up);
+        float up[4 * G];
+        finished(o_in + 16 * FW / 2, bias_up, up);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] *= up[i];
+        for (int i = 0; i < 4 * G; ++i) y[i] *= up[i];
       }
-      store4(y, n, p.out_dt, res, p.residual != nullptr, p.out, out_row * p.ldo + o);
+      float y4[G][4];
+#pragma unroll
+      for (int i = 0; i < 4 * G; ++i) y4[i / 4][i % 4] = y[i];
+      if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < G; ++i) add_residual(y4[i], p.out_dt, res[i]);
+      }
+      const int64_t to = (row0 + token0 + static_cast<int64_t>(slice) * p.R) * p.ldo + o;
+#pragma unroll
+      for (int i = 0; i < G; ++i)
+        if (inside(i) > 0) store4(y4[i], n, p.out_dt, p.out, to + i * apart * p.ldo);
     }
   }
 }
