@@ -492,16 +492,16 @@ F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
   };
   // Tiles of tokens x rows, measured on each side.  Where exponents alone are applied by
   // the matrix instruction: 256 x 256 in eight waves where every unit has one (4096 x 4096 ->
-  // 2 x 14336: 428 us; 128 x 256 533, 128 x 128 521; 2048 x 8192 -> 8192: 117; 140; 149), of
-  // runs only of long ones (16384 rows of 64 experts, 2048 -> 2 x 1408: 200; 128 x 256
-  // 192); then 128 x 256.  Float32 scales or results: 128 x 128 in four waves, two
-  // workgroups on a unit (4096 x 4096 -> 2 x 14336 with float32 scales 552, 128 x 256 588;
-  // to float32 803, 869).  Where there is about one such tile per unit or less, eight waves
-  // share it, 64 x 32 each (512 x 8192 -> 8192: 46; four waves 63); for float32 results four
-  // waves for every other block of positions, so that each operand is converted half as
-  // often (71; 64 x 32 each 80; four waves 80).
+  // 2 x 14336: 407 us; 128 x 256 480, 128 x 128 472; 2048 x 8192 -> 8192: 133; 159; 158), of
+  // runs only of long ones (64 experts, 2048 -> 2 x 1408, 512 rows each: 271, 128 x 256 312;
+  // 256 rows each: 188, 173); then 128 x 256 (the same: 128 x 128 184).  Float32 scales or
+  // results: 128 x 128 in four waves, two workgroups on a unit (4096 x 4096 -> 2 x 14336 with
+  // float32 scales 552, 128 x 256 588; to float32 803, 869).  Where there is about one such
+  // tile per unit or less, eight waves share it, 64 x 32 each (512 x 8192 -> 8192: 40; four
+  // waves 63); for float32 results four waves for every other block of positions, so that each
+  // operand is converted half as often (71; 64 x 32 each 80; four waves 80).
   const bool quick = !float_scales && !precise;
-  if (quick && count(256, 256) >= cus && R >= 1024 * (grouped ? runs : 0)) p.shape = kSquare;
+  if (quick && count(256, 256) >= cus && R >= 512 * (grouped ? runs : 0)) p.shape = kSquare;
   else if (quick && count(128, 256) * 5 >= cus * 4) p.shape = kTall;
   else if (count(128, 128) * 4 > cus * 5) p.shape = kPair;
   else p.shape = kOne;
