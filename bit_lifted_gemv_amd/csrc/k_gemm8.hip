@@ -3,12 +3,18 @@
 // the epilogue of lq_gemm8 and the ragged expert runs of lq_gemm8_grouped.
 //
 // Tile.  WT x WW waves, each 16 FT tokens x 16 FW rows of weights in tiles of 16 x 16:
-// v_mfma_scale_f32_16x16x128_f8f6f4 takes a whole block of 128 positions, so a
-// float32 scale of the block costs four multiply-adds per product (a lane's sums
-// are of one row of weights).  Operands come to LDS by loads that write it
-// directly, in stages of 128 positions (a ring of S); 16-byte piece c of row r
-// lies at piece c ^ (r / 2 % 8), so that 16 lanes reading one piece of 16 rows
-// touch every bank once.
+// v_mfma_scale_f32_16x16x128_f8f6f4 takes a whole block of 128 positions, rows of weights
+// as operand A, so that a lane's four sums are four rows of one token: one 8- or
+// 16-byte piece of the output.  The exponents of both sides are the instruction's
+// scales; a float32 scale costs four multiply-adds per product.  The instruction adds
+// eight products at a time and cuts them off 13 bits below the largest one's power of
+// two, which 16-bit results do not show; for float32 results (PREC) the operands become
+// bfloat16 (exact) and v_mfma_f32_16x16x32_bf16 keeps 24 bits, at half the rate or less.
+//
+// Operands come to LDS by loads that write it directly, in stages of 128 positions (a
+// ring of S); 16-byte piece c of row r lies at piece c ^ (r / 2 % 8), so that 16 lanes
+// reading one piece of 16 rows touch every bank once.  Rows of 128 bytes are what such
+// loads move best: rows of 64 bytes took twice as long per byte.
 //
 // A wave holds a stage's rows and a ring of four token tiles; each is refilled from
 // LDS as soon as its last product has been issued.  Where the refills pass to the
@@ -17,6 +23,11 @@
 //
 // The waits are counted by hand (the compiler would drain the loads before every
 // read of LDS): every wave issues the same number of loads per stage.
+//
+// Bound by the matrix instructions: 256 x 256 tiles of 4096 x 4096 -> 2 x 14336 take
+// 407 us (2.4 PF); per 1024 positions 90 us (2.7 PF, what a large library product of
+// the same types reaches on the same card), the rest is the tiles' beginnings (28 us, the
+// first loads) and ends (some 55 us, half of them the output's 117 MB).
 #include "f6_epilogue.h"
 #include "f6_product.h"
 #include "f8.h"
@@ -467,8 +478,9 @@ hipError_t by_shape(const F8Product& p, int shape, hipStream_t st) {
     if (shape == kTall) return launch<AK, FS, PREC, 2, 4, 1, 4, 4>(p, st);
   }
   if (shape == kPair) return launch<AK, FS, PREC, 2, 2, 1, 4, 4>(p, st);
-  // float32 results convert each operand in every wave that reads it: larger pieces of the tile
-  if constexpr (PREC) return launch<AK, FS, PREC, 2, 2, 2, 4, 4>(p, st);
+  // larger pieces of the tile where a wave works on each operand it reads (float32 results
+  // convert it, float32 scales multiply its sums)
+  if constexpr (PREC || FS) return launch<AK, FS, PREC, 2, 2, 2, 4, 4>(p, st);
   else return launch<AK, FS, PREC, 2, 4, 1, 4, 2>(p, st);
 }
 
@@ -496,10 +508,11 @@ F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
   // runs only of long ones (64 experts, 2048 -> 2 x 1408, 512 rows each: 271, 128 x 256 312;
   // 256 rows each: 188, 173); then 128 x 256 (the same: 128 x 128 184).  Float32 scales or
   // results: 128 x 128 in four waves, two workgroups on a unit (4096 x 4096 -> 2 x 14336 with
-  // float32 scales 552, 128 x 256 588; to float32 803, 869).  Where there is about one such
-  // tile per unit or less, eight waves share it, 64 x 32 each (512 x 8192 -> 8192: 40; four
-  // waves 63); for float32 results four waves for every other block of positions, so that each
-  // operand is converted half as often (71; 64 x 32 each 80; four waves 80).
+  // float32 scales 542, 128 x 256 561; to float32 811, 867).  Where there is about one such
+  // tile per unit or less, eight waves share it, 64 x 32 each (512 x 8192 -> 8192: 41; 64 x 64
+  // in four waves 46); for float32 scales or results 64 x 64, four waves for every other block
+  // of positions (the same with float32 scales 44, 64 x 32 each 48, four waves 55; to float32
+  // 64; 77; 77).
   const bool quick = !float_scales && !precise;
   if (quick && count(256, 256) >= cus && R >= 512 * (grouped ? runs : 0)) p.shape = kSquare;
   else if (quick && count(128, 256) * 5 >= cus * 4) p.shape = kTall;

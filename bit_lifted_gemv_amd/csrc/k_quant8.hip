@@ -70,39 +70,46 @@ __device__ __forceinline__ uint2 round8(const float (&v)[8], int byte) {
 
 // Rows: 16 lanes per block of 128 positions, so a wave takes 512 positions and
 // writes their four exponents as one word (rows of exponents are whole words).
-// UNITS pieces per wave, their loads on the way together.
-constexpr int kUnits = 2;
-
-template <int DT, int T>
+// U such pieces per wave, their loads on the way together.
+template <int DT, int T, int U>
 __global__ void __launch_bounds__(256) quant8_rows_kernel(const void* __restrict__ x, int64_t units,
                                                           int64_t K, int64_t ld, int per_row,
                                                           uint8_t* __restrict__ q, int64_t ldq,
                                                           uint8_t* __restrict__ exps, int64_t lde) {
   constexpr int ESZ = DT == LQ_F32 ? 4 : 2;
   const int lane = threadIdx.x & 63;
-  const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6)) * kUnits;
-  Eight<DT> raw[kUnits];
-  int64_t row[kUnits];
-  int at[kUnits];
+  const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6)) * U;
+  Eight<DT> raw[U];
+  int64_t row[U];
+  int at[U];
 #pragma unroll
-  for (int c = 0; c < kUnits; ++c) {
+  for (int c = 0; c < U; ++c) {
     const int64_t u = min(u0 + c, units - 1);
     row[c] = u / per_row;
     at[c] = static_cast<int>(u - row[c] * per_row);
     raw[c] = load8<DT>(static_cast<const uint8_t*>(x) + row[c] * ld * ESZ, at[c] * int64_t{512} + lane * 8, K);
   }
 #pragma unroll
-  for (int c = 0; c < kUnits; ++c) {
+  for (int c = 0; c < U; ++c) {
     if (u0 + c >= units) return;
-    float v[8];
-    values(raw[c], v);
-    float m = largest8(v);
+    int byte;
+    uint2 bits;
+    if constexpr (DT != LQ_F32 && T == LQ_E4M3) {          // the same in a third of the instructions
+      const auto& w = raw[c].w;
+      byte = block16<DT, 4, 1, 8>(w);
+      const float scale = power_of_two(byte);
+      bits = make_uint2(round16<DT>(w[0], w[1], scale), round16<DT>(w[2], w[3], scale));
+    } else {
+      float v[8];
+      values(raw[c], v);
+      float m = largest8(v);
 #pragma unroll
-    for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-    const int byte = block_exponent<T>(m);
+      for (int d = 1; d < 16; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
+      byte = block_exponent<T>(m);
+      bits = round8<T>(v, byte);
+    }
     const int64_t k = at[c] * int64_t{512} + lane * 8;
-    if (k < (K + 127) / 128 * 128)
-      *reinterpret_cast<uint2*>(q + row[c] * ldq + k) = round8<T>(v, byte);
+    if (k < (K + 127) / 128 * 128) *reinterpret_cast<uint2*>(q + row[c] * ldq + k) = bits;
     uint32_t word = 0;
 #pragma unroll
     for (int b = 0; b < 4; ++b)
@@ -152,16 +159,16 @@ __global__ void __launch_bounds__(256) quant8_blocks_kernel(const void* __restri
   }
 }
 
-template <int DT, int T>
+template <int DT, int T, int U>
 hipError_t rows(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, int64_t ldq,
                 uint8_t* exps, int64_t lde, hipStream_t st) {
   const int per_row = static_cast<int>((K + 511) / 512);
   constexpr int64_t most = int64_t{1} << 22;                  // workgroups of a launch
-  const int64_t rows_per = most * 4 * kUnits / per_row;
+  const int64_t rows_per = most * 4 * U / per_row;
   for (int64_t r = 0; r < n; r += rows_per) {
     const int64_t some = n - r < rows_per ? n - r : rows_per;
-    const int64_t groups = (some * per_row + 4 * kUnits - 1) / (4 * kUnits);
-    quant8_rows_kernel<DT, T><<<static_cast<uint32_t>(groups), 256, 0, st>>>(
+    const int64_t groups = (some * per_row + 4 * U - 1) / (4 * U);
+    quant8_rows_kernel<DT, T, U><<<static_cast<uint32_t>(groups), 256, 0, st>>>(
         static_cast<const uint8_t*>(x) + r * ld * (DT == LQ_F32 ? 4 : 2), some * per_row, K, ld,
         per_row, q + r * ldq, ldq, exps + r * lde, lde);
     const hipError_t e = hipGetLastError();
@@ -170,11 +177,25 @@ hipError_t rows(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, int
   return hipSuccess;
 }
 
+// One piece a wave where there are few (16 rows of 4096 and their product 32.5 us, two
+// pieces 33.2; 4096 rows of 4096 bfloat16 to e5m2 11.3, four 12.1), four of 16-bit values
+// where they fill the card many times (4096 rows of 14336 to e4m3: 29 us, 6.0 TB/s; one 35,
+// two 33, eight 33; to e5m2 32; one 35.6); of float32 one (48 us; two 49, four 51).
+template <int DT, int T>
+hipError_t by_size(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, int64_t ldq,
+                   uint8_t* exps, int64_t lde, hipStream_t st) {
+  if constexpr (DT != LQ_F32) {
+    if (n * ((K + 511) / 512) > int64_t{128} * num_cus())
+      return rows<DT, T, 4>(x, n, K, ld, q, ldq, exps, lde, st);
+  }
+  return rows<DT, T, 1>(x, n, K, ld, q, ldq, exps, lde, st);
+}
+
 template <int DT>
 hipError_t by_type(const void* x, int64_t n, int64_t K, int64_t ld, uint8_t* q, lq_dtype type,
                    int64_t ldq, uint8_t* exps, int64_t lde, hipStream_t st) {
-  return type == LQ_E4M3 ? rows<DT, LQ_E4M3>(x, n, K, ld, q, ldq, exps, lde, st)
-                         : rows<DT, LQ_E5M2>(x, n, K, ld, q, ldq, exps, lde, st);
+  return type == LQ_E4M3 ? by_size<DT, LQ_E4M3>(x, n, K, ld, q, ldq, exps, lde, st)
+                         : by_size<DT, LQ_E5M2>(x, n, K, ld, q, ldq, exps, lde, st);
 }
 
 template <int DT>

@@ -918,7 +918,8 @@ def gemm8(w: Blocks8, a, bias: Optional[torch.Tensor] = None, act: str = "none",
     """act(a @ w^T + bias) + residual for any number of tokens (lq_gemm8).  w:
     8-bit weights [m][K]; a: Rows8, or float16 or bfloat16 [B][K], which the
     call quantizes (to the same result).  Epilogue as gemm_ep; out_dtype: a's,
-    bfloat16 for Rows8.  The gradient of the activations is
+    bfloat16 for Rows8; float32 keeps 24 bits of every sum, at half the speed or
+    less (lq_gemm8).  The gradient of the activations is
     gemm8(w.transposed(), quantize8(dz, torch.float8_e5m2))."""
     m, width = w.values.shape
     values = a.values if isinstance(a, Rows8) else a
@@ -1047,7 +1048,8 @@ def join_rows_grad(dy: torch.Tensor, z: torch.Tensor, pos: torch.Tensor, weight:
     """The gradients of join_rows with weights, from dy [T][n] (lq_join_rows_grad):
     (dz [R][n] of z's type, dweight float32 [T][k]).  With rows (route's) the
     rows of dz that no token has are zeros; without, every row must be named
-    in pos, for the others are not written.  The residual's gradient is dy."""
+    in pos, for the others are not written.  Positions of two pairs must differ,
+    as route's do.  The residual's gradient is dy."""
     R, n = z.shape
     T, k = pos.shape
     dev = z.device

@@ -555,7 +555,8 @@ lq_status lq_gemm_join(const uint32_t* w_packed, int64_t E, int64_t m, int64_t K
  *       positions from K to the whole 128 are written as zeros.
  * exps: uint8 [rows][lde], lde >= ceil(K / 128), a multiple of 4, 4-byte aligned;
  *       the bytes behind the last block up to a whole word are written too.
- * Requires 1 <= K <= 2^22, 0 <= rows < 2^31 (0 is a no-op).
+ * Requires 1 <= K <= 2^22, 0 <= rows < 2^31 (0 is a no-op); q and exps must not
+ * overlap x.
  */
 lq_status lq_quant8(const void* x, lq_dtype dtype, int64_t rows, int64_t K, int64_t ld, void* q,
                     lq_dtype q_dtype, int64_t ldq, uint8_t* exps, int64_t lde, void* stream);
@@ -591,9 +592,15 @@ lq_status lq_quant8_blocks(const void* w, lq_dtype dtype, int64_t E, int64_t m, 
  * bias, act, gated, residual, out, out_dtype: as lq_gemm_ep.
  * workspace: >= lq_gemm8_workspace_size bytes (it may be 0), 256-byte aligned,
  *          caller-owned, no initialisation needed.
- * Requires 1 <= K <= 2^22, B >= 1, B rows of 8-bit activations below 4 GiB.
+ * Requires 1 <= K <= 2^22, B >= 1, B rows of 8-bit activations below 4 GiB (also as
+ * quantized from 16 bits), lde <= lda, at most 2^29 scales; out must not be a.
  * Exact products, float32 sums in a fixed order (deterministic); epilogue in
- * float32.  A NaN in a token gives NaN in its outputs.
+ * float32.  For out_dtype LQ_F16 and LQ_BF16 the 8-bit matrix instructions add
+ * eight products at a time and drop what lies below 2^-13 of the largest one's
+ * power of two (some 2^-17 of a typical z); for LQ_F32 16-bit instructions keep 24
+ * bits, at half the rate or less.  A value times its block's power of two lies
+ * within float32's normal range, of either operand: smaller ones may count as
+ * zeros, larger ones as infinities.  A NaN in a token gives NaN in its outputs.
  * The gradient of the activations is the same product with the transposed
  * weights and scales (128 x 128 blocks transpose onto blocks).
  */

@@ -161,3 +161,17 @@ def test_captured_and_on_another_stream():
         torch.cuda.synchronize()
         assert torch.equal(captured.values.view(torch.uint8), again.values.view(torch.uint8))
         assert torch.equal(captured.exps, again.exps)
+
+
+@pytest.mark.parametrize("to", [torch.float8_e4m3fn, torch.float8_e5m2])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_every_16_bit_value_as_from_float32(dtype, to):
+    """All 65536 of them, in order (blocks of one binade) and mixed (blocks of the widest range), in few rows and many."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    mixed = bits[torch.randperm(65536, generator=torch.Generator().manual_seed(1))]
+    x = torch.stack([bits, mixed]).view(dtype).reshape(1024, 128).cuda()
+    for a in (x, x.reshape(32, 4096).repeat(200, 1)):
+        got, want = lq.quantize8(a, to), lq.quantize8(a.float(), to)
+        nan = torch.isnan(want.values.float())
+        assert torch.equal(got.exps, want.exps) and torch.equal(torch.isnan(got.values.float()), nan)
+        assert torch.equal(got.values.view(torch.uint8)[~nan], want.values.view(torch.uint8)[~nan])
