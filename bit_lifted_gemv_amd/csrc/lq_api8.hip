@@ -56,16 +56,22 @@ lq_status check_sizes8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_
   return LQ_OK;
 }
 
-// Up to 16 rows of one matrix, or of a run on average, go to the few-row kernel: 16 x 4096
-// -> 4096 12 us there and 15 on tiles, -> 2 x 14336 32 and 33, 24 rows 44 and 33;
-// 64 experts (2048 -> 2 x 1408), 1024 rows 96 and 107, 2048 rows 150 and 114.
-constexpr int64_t kFewRowsPerRun = 16;
+// The rows of one matrix, or of a run on average, up to which the few-row kernel is the
+// faster one, us there and on tiles.  To float32: 16 (16 x 8192 -> 8192: 25 and 27; 64
+// experts, 2048 -> 2816, 16 each: 100 and 112, 24: 135 and 112).  To 16 bits: 11 of a run (8
+// each 77 and 85, 12 each 91 and 85; 8 experts, 4096 -> 28672: 181 and 192, 199 and 191), 16 of one
+// matrix (16 x 4096 -> 4096: 10.7 and 14, -> 57344: 55 and 54; 24 -> 4096: 15.4 and 13.9), 8 from 8192 positions
+// on, where the activations that each block of rows reads again weigh most (16 x 14336 ->
+// 4096: 21.3 and 17.6, 16 x 16384 -> 8192: 37 and 28; 6: 31 and 29).
+int64_t few_rows(int64_t K, bool grouped, bool precise) {
+  return precise ? 16 : grouped ? 11 : blocks(K) >= 64 ? 8 : 16;
+}
 
 Plan8 plan8(int64_t E, int64_t m, int64_t K, lq_dtype a_dtype, int64_t a_rows, int64_t R, bool gated,
             bool grouped, bool float_scales, bool precise) {
   Plan8 p{};
   const int64_t runs = grouped ? (E < R ? E : R < 1 ? 1 : R) : 1;
-  p.few = R <= kFewRowsPerRun * runs;
+  p.few = R <= few_rows(K, grouped, precise) * runs;
   p.fp = lq::few_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped);
   p.mp = lq::many_f8_plan(E, m, K, R < 1 ? 1 : R, gated, grouped, float_scales, precise);
   p.slices = p.few ? p.fp.slices : p.mp.slices;
