@@ -148,7 +148,8 @@ __device__ __forceinline__ void add_residual(float (&y)[4], int dt, const Residu
   }
 }
 
-// The first n of four outputs.
+// The first n of four outputs; STREAM: whole 16-bit ones past the caches.
+template <bool STREAM = false>
 __device__ __forceinline__ void store4(const float (&y)[4], int n, int dt, void* out, int64_t at) {
   if (dt == LQ_F32) {
     float* to = static_cast<float*>(out) + at;
@@ -165,7 +166,8 @@ __device__ __forceinline__ void store4(const float (&y)[4], int n, int dt, void*
   const u32x2 v = {round16x2(y[0], y[1], dt), round16x2(y[2], y[3], dt)};
   uint16_t* to = static_cast<uint16_t*>(out) + at;
   if (n == 4) {
-    *reinterpret_cast<u32x2_any*>(to) = v;
+    if (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any*>(to));
+    else *reinterpret_cast<u32x2_any*>(to) = v;
   } else {
 #pragma unroll
     for (int c = 0; c < 4; ++c)

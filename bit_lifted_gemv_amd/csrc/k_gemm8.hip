@@ -25,7 +25,7 @@
 // read of LDS): every wave issues the same number of loads per stage.
 //
 // Bound by the matrix instructions: 256 x 256 tiles of 4096 x 4096 -> 2 x 14336 take
-// 407 us (2.4 PF); per 1024 positions 90 us (2.7 PF, what a large library product of
+// 400 us (2.4 PF); per 1024 positions 90 us (2.7 PF, what a large library product of
 // the same types reaches on the same card), the rest is the tiles' beginnings (28 us, the
 // first loads) and ends (some 55 us, half of them the output's 117 MB).
 #include "f6_epilogue.h"
@@ -362,7 +362,9 @@ gemm8_kernel(F8Product p) {
   // ---- the end: AT_ONCE token tiles at a time through the wave's own part of LDS, [token][row],
   // so that its stores are whole runs and its code short (unrolled over all the sums it would be
   // 100 KB, fetched once per tile: 15 us of each).  Without a residual no load stands between
-  // the stores: a wait for one is a wait for the stores before it.
+  // the stores: a wait for one is a wait for the stores before it.  The large tiles' outputs are
+  // more than the caches hold and pass them by (4096 x 4096 -> 28672: 446 to 410 us).
+  constexpr bool STREAM = ROWS > 128;
   constexpr int PITCH = P::PITCH, AT_ONCE = P::AT_ONCE, MASKS = (LAST + 3) / 4, G = 4;
   const int wave_token = wt * 16 * FT + (WK == 2 && wk ? 16 * LAST : 0);
   uint64_t live[MASKS];                                  // of the wave's tokens: whether their index is one
@@ -415,9 +417,18 @@ gemm8_kernel(F8Product p) {
 #pragma unroll
         for (int i = 0; i < G; ++i) {
           const f32x4 z = *reinterpret_cast<const f32x4*>(ex + (at0 + i * apart) * PITCH + column);
-          const bool is = alive >> (at0 + i * apart) & 1;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[4 * i + j] = (is ? z[j] : 0.f) + b[j];
+          for (int j = 0; j < 4; ++j) y[4 * i + j] = z[j];
+        }
+        if (p.rows) {
+#pragma unroll
+          for (int i = 0; i < G; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) y[4 * i + j] = alive >> (at0 + i * apart) & 1 ? y[4 * i + j] : 0.f;
+        }
+        if (p.bias) {
+#pragma unroll
+          for (int i = 0; i < 4 * G; ++i) y[i] += b[i % 4];
         }
       };
       float y[4 * G];
@@ -439,7 +450,7 @@ gemm8_kernel(F8Product p) {
       const int64_t to = (row0 + token0 + static_cast<int64_t>(slice) * p.R) * p.ldo + o;
 #pragma unroll
       for (int i = 0; i < G; ++i)
-        if (inside(i) > 0) store4(y4[i], n, p.out_dt, p.out, to + i * apart * p.ldo);
+        if (inside(i) > 0) store4<STREAM>(y4[i], n, p.out_dt, p.out, to + i * apart * p.ldo);
     }
   }
 }
