@@ -25,9 +25,9 @@
 // read of LDS): every wave issues the same number of loads per stage.
 //
 // Bound by the matrix instructions: 256 x 256 tiles of 4096 x 4096 -> 2 x 14336 take
-// 400 us (2.4 PF); per 1024 positions 90 us (2.7 PF, what a large library product of
-// the same types reaches on the same card), the rest is the tiles' beginnings (28 us, the
-// first loads) and ends (some 55 us, half of them the output's 117 MB).
+// 397 us (2.4 PF); per 1024 positions 85 us (2.8 PF, what a large library product of
+// the same types reaches on the same card), the rest is the tiles' beginnings (25 us, the
+// first loads) and ends (some 50 us, half of them the output's 117 MB).
 #include "f6_epilogue.h"
 #include "f6_product.h"
 #include "f8.h"
@@ -513,21 +513,29 @@ F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
     const int64_t tiles = grouped ? R / tok + (runs + 1) / 2 : (R + tok - 1) / tok;
     return tiles * ((out_m + outs - 1) / outs);
   };
-  // Tiles of tokens x rows, measured on each side.  Where exponents alone are applied by
-  // the matrix instruction: 256 x 256 in eight waves where every unit has one (4096 x 4096 ->
-  // 2 x 14336: 407 us; 128 x 256 480, 128 x 128 472; 2048 x 8192 -> 8192: 133; 159; 158), of
-  // runs only of long ones (64 experts, 2048 -> 2 x 1408, 512 rows each: 271, 128 x 256 312;
-  // 256 rows each: 188, 173); then 128 x 256 (the same: 128 x 128 184).  Float32 scales or
-  // results: 128 x 128 in four waves, two workgroups on a unit (4096 x 4096 -> 2 x 14336 with
-  // float32 scales 542, 128 x 256 561; to float32 811, 867).  Where there is about one such
-  // tile per unit or less, eight waves share it, 64 x 32 each (512 x 8192 -> 8192: 41; 64 x 64
-  // in four waves 46); for float32 scales or results 64 x 64, four waves for every other block
-  // of positions (the same with float32 scales 44, 64 x 32 each 48, four waves 55; to float32
-  // 64; 77; 77).
+  // Tiles of tokens x rows, measured on each side.  Where exponents alone are applied by the
+  // matrix instruction: 256 x 256 and 128 x 256 in eight waves, one workgroup on a unit, or 128 x
+  // 128 in four, two of them (4096 x 4096 -> 2 x 14336: 397 us, 465, 456; 2048 x 8192 -> 8192:
+  // 131, 154, 147; of 2100 rows 199, 176, 156).  Of one matrix the fewest rounds of the units' tiles decide, priced by these
+  // rates, a last round of single workgroups 1.4 of 2.3 (700 x 4096 -> 14336: 128 x 256 66, 128 x
+  // 128 58).  Of runs, whose tiles are only estimated, 256 x 256 if they are long (64 experts,
+  // 2048 -> 2 x 1408, 512 rows each: 270, 128 x 256 306; 256 rows each: 186, 173, 128 x 128 190).
+  // Float32 scales or results: 128 x 128 in four waves, two workgroups on a unit (4096 x 4096 -> 2
+  // x 14336 with float32 scales 524, 128 x 256 561; to float32 811, 867).  Where no unit has more
+  // than one such tile (520 x 8192 -> 8192, 320 of them: 64, one at a time 82), eight waves share
+  // it, 64 x 32 each (512 x 8192 -> 8192: 41; 64 x 64 in four waves 46); for float32 scales or
+  // results 64 x 64, four waves for every other block of positions (the same with float32 scales
+  // 44, 64 x 32 each 48, four waves 55; to float32 64; 77; 77).
   const bool quick = !float_scales && !precise;
-  if (quick && count(256, 256) >= cus && R >= 512 * (grouped ? runs : 0)) p.shape = kSquare;
+  auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
+  const int64_t square = rounds(count(256, 256)) * 40, tall = rounds(count(128, 256)) * 23;
+  const int64_t pairs = count(128, 128), rest = pairs % (2 * cus);
+  const int64_t pair = pairs / (2 * cus) * 23 + (rest > cus ? 23 : rest ? 14 : 0);
+  if (quick && !grouped && count(128, 256) * 5 >= cus * 4)
+    p.shape = square <= tall && square <= pair ? kSquare : tall <= pair ? kTall : kPair;
+  else if (quick && grouped && count(256, 256) >= cus && R >= 512 * runs) p.shape = kSquare;
   else if (quick && count(128, 256) * 5 >= cus * 4) p.shape = kTall;
-  else if (count(128, 128) * 4 > cus * 5) p.shape = kPair;
+  else if (pairs > cus) p.shape = kPair;
   else p.shape = kOne;
   // Where tiles leave units without one, the positions are split, down to 1024 a
   // slice (777 x 5125 -> 1281: one 28, three 22; 64 x 14336 -> 4096: one 67, eight 22).
