@@ -514,18 +514,19 @@ F8ManyPlan many_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, 
     return tiles * ((out_m + outs - 1) / outs);
   };
   // Tiles of tokens x rows, measured on each side.  Where exponents alone are applied by the
-  // matrix instruction: 256 x 256 and 128 x 256 in eight waves, one workgroup on a unit, or 128 x
-  // 128 in four, two of them (4096 x 4096 -> 2 x 14336: 397 us, 465, 456; 2048 x 8192 -> 8192:
-  // 131, 154, 147; of 2100 rows 199, 176, 156).  Of one matrix the fewest rounds of the units' tiles decide, priced by these
-  // rates, a last round of single workgroups 1.4 of 2.3 (700 x 4096 -> 14336: 128 x 256 66, 128 x
-  // 128 58).  Of runs, whose tiles are only estimated, 256 x 256 if they are long (64 experts,
-  // 2048 -> 2 x 1408, 512 rows each: 270, 128 x 256 306; 256 rows each: 186, 173, 128 x 128 190).
-  // Float32 scales or results: 128 x 128 in four waves, two workgroups on a unit (4096 x 4096 -> 2
-  // x 14336 with float32 scales 524, 128 x 256 561; to float32 811, 867).  Where no unit has more
-  // than one such tile (520 x 8192 -> 8192, 320 of them: 64, one at a time 82), eight waves share
-  // it, 64 x 32 each (512 x 8192 -> 8192: 41; 64 x 64 in four waves 46); for float32 scales or
-  // results 64 x 64, four waves for every other block of positions (the same with float32 scales
-  // 44, 64 x 32 each 48, four waves 55; to float32 64; 77; 77).
+  // matrix instruction: 256 x 256 and 128 x 256 in eight waves, one workgroup on a unit, or 128
+  // x 128 in four, two of them (4096 x 4096 -> 2 x 14336: 397 us, 465, 456; 2048 x 8192 -> 8192:
+  // 131, 154, 147; of 2100 rows 199, 176, 156).  Of one matrix the fewest rounds of the units'
+  // tiles decide, priced by these rates, a last round of single workgroups 1.4 of 2.3 (700 x
+  // 4096 -> 14336: 128 x 256 66, 128 x 128 58).  Of runs, whose tiles are only estimated, 256 x
+  // 256 if they are long (64 experts, 2048 -> 2 x 1408, 512 rows each: 270, 128 x 256 306; 256
+  // rows each: 186, 173, 128 x 128 190). Float32 scales or results: 128 x 128 in four waves, two
+  // workgroups on a unit (4096 x 4096 -> 2 x 14336 with float32 scales 524, 128 x 256 561; to
+  // float32 811, 867).  Where no unit has more than one such tile (520 x 8192 -> 8192, 320 of
+  // them: 64, one at a time 82), eight waves share it, 64 x 32 each (512 x 8192 -> 8192: 41; 64
+  // x 64 in four waves 46); for float32 scales or results 64 x 64, four waves for every other
+  // block of positions (the same with float32 scales 44, 64 x 32 each 48, four waves 55; to
+  // float32 64; 77; 77).
   const bool quick = !float_scales && !precise;
   auto rounds = [&](int64_t n) { return (n + cus - 1) / cus; };
   const int64_t square = rounds(count(256, 256)) * 40, tall = rounds(count(128, 256)) * 23;
