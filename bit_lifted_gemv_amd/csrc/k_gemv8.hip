@@ -4,11 +4,11 @@
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4 covers one block of 128 positions: operand A
 // 16 tokens, scaled by the power of two of its lane's token; operand B 16 rows of
-// weights, whose scale multiplies the block's sum (a lane's four sums are of one
-// row).  The instruction adds eight products at a time and cuts them off 13 bits
+// weights, scaled by theirs (a float32 scale multiplies the block's sum: a lane's four
+// sums are of one row).  The instruction adds eight products at a time and cuts them off 13 bits
 // below the largest one's power of two: some 2^-17 of a typical result, which
 // 16-bit results do not show.  For float32 results (PREC) the operands become
-// bfloat16 (exact, and the token's power of two goes in) and
+// bfloat16 (exact, and the powers of two go in) and
 // v_mfma_f32_16x16x32_bf16 keeps 24 bits.
 //
 // Bound by reading the weights: nothing of them passes through LDS.  A wave
@@ -180,15 +180,18 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
 #pragma unroll
     for (int f = 0; f < WF; ++f) {
       const i32x8 b = words(wv[u][f][0], wv[u][f][1]);
-      const float scale = p.float_scales ? __uint_as_float(sv[u][f]) : power_of_two(sv[u][f]);
+      // a power of two goes into the products (a block's sum without it may leave float32's range)
+      const float scale = p.float_scales ? __uint_as_float(sv[u][f]) : 1.f;
       f32x4 z = {};
       if constexpr (PREC) {
+        const float power = p.float_scales ? 1.f : power_of_two(sv[u][f]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              wide[i], widen8<LQ_E4M3>(b[2 * i], b[2 * i + 1], 1.f), z, 0, 0, 0);
+              wide[i], widen8<LQ_E4M3>(b[2 * i], b[2 * i + 1], power), z, 0, 0, 0);
       } else {
-        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, AT == LQ_E5M2 ? 1 : 0, 0, 0, e, 0, 127);
+        const int byte = p.float_scales ? 127 : static_cast<int>(sv[u][f]);
+        z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, AT == LQ_E5M2 ? 1 : 0, 0, 0, e, 0, byte);
       }
       acc[f] += z * scale;
     }
