@@ -596,9 +596,11 @@ lq_status lq_quant8_blocks(const void* w, lq_dtype dtype, int64_t E, int64_t m, 
  * quantized from 16 bits), lde <= lda, at most 2^29 scales; out must not be a.
  * Exact products, float32 sums in a fixed order (deterministic); epilogue in
  * float32.  For out_dtype LQ_F16 and LQ_BF16 the 8-bit matrix instructions add
- * eight products at a time and drop what lies below 2^-13 of the largest one's
- * power of two (some 2^-17 of a typical z); for LQ_F32 16-bit instructions keep 24
- * bits, at half the rate or less.  A value times its block's power of two lies
+ * the products of eight consecutive positions and cut each off, toward zero, 13 binary
+ * places below the largest sum of two factors' exponents: 2^-16 of a typical z (root of the
+ * mean square) where the factors are normally distributed, 2^-14.5 where one position
+ * in a hundred is 20 times the others.  A sum that nearly cancels keeps that error;
+ * for LQ_F32 16-bit instructions keep 24 bits, at half the rate or less.  A value times its block's power of two lies
  * within float32's normal range, of either operand: smaller ones may count as
  * zeros, larger ones as infinities.  A NaN in a token gives NaN in its outputs.
  * The gradient of the activations is the same product with the transposed
