@@ -268,14 +268,10 @@ hipError_t launch(const F8Product& in, const F8FewPlan& plan, hipStream_t st) {
   const int64_t blocks = tiles * p.row_blocks * p.slices;
   if (blocks > INT32_MAX) return hipErrorInvalidValue;
   const int threads = 64 * plan.waves;
+  // the sums, in the place of the held activations: at most 34 KB of eight waves, and 17 KB
   int64_t bytes = plan.waves * tok * (16 * WF + 4) * 4;
-  if (plan.held && plan.held_bytes > bytes) bytes = plan.held_bytes;
+  if ((AK == LQ_F16 || AK == LQ_BF16) && plan.held_bytes > bytes) bytes = plan.held_bytes;
   auto* k = gemv8_kernel<AK, PREC, WF>;
-  if (bytes > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-    if (e != hipSuccess) return e;
-  }
   // a launch has fewer than 2^32 threads
   const int64_t most = (int64_t{1} << 31) / threads;
   for (int64_t b = 0; b < blocks; b += most) {
@@ -328,9 +324,9 @@ F8FewPlan few_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bo
     p.slice_steps = static_cast<int>((steps + s - 1) / s);
     p.slices = static_cast<int>((steps + p.slice_steps - 1) / p.slice_steps);
   }
-  // of runs the host knows only that none is longer than R
+  // 16-bit activations; of runs the host knows only that none is longer than R
   p.held = R <= 4 && R * p.slice_steps <= 128;
-  p.held_bytes = R * (p.slice_steps * 132 + 32);
+  p.held_bytes = p.held ? R * (p.slice_steps * 132 + 32) : 0;
   return p;
 }
 
