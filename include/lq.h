@@ -58,7 +58,7 @@ typedef int32_t lq_dtype;
 /* Types of lq_quant8 and the 8-bit products alone (OCP 8-bit floating point). */
 #define LQ_E4M3 3  /* 4 exponent bits, 3 of fraction, largest 448, no infinity  */
 #define LQ_E5M2 4  /* 5 exponent bits, 2 of fraction, largest 57344             */
-#define LQ_E8M0 5  /* of scales: a byte b, the scale 2^(b - 127)                */
+#define LQ_E8M0 5  /* of scales: a byte b, the scale 2^(b - 127); 255 is a NaN  */
 
 /* Activations of the products with an epilogue (lq_gemm_ep, lq_gemm_grouped). */
 typedef int32_t lq_act;
@@ -600,9 +600,11 @@ lq_status lq_quant8_blocks(const void* w, lq_dtype dtype, int64_t E, int64_t m, 
  * places below the largest sum of two factors' exponents: 2^-16 of a typical z (root of the
  * mean square) where the factors are normally distributed, 2^-14.5 where one position
  * in a hundred is 20 times the others.  A sum that nearly cancels keeps that error;
- * for LQ_F32 16-bit instructions keep 24 bits, at half the rate or less.  A value times its block's power of two lies
- * within float32's normal range, of either operand: smaller ones may count as
- * zeros, larger ones as infinities.  A NaN in a token gives NaN in its outputs.
+ * for LQ_F32 16-bit instructions keep 24 bits, at half the rate or less.
+ * A value times its block's power of two lies within float32's normal range, of either
+ * operand, and so does a block's sum before its LQ_F32 scale: smaller ones may count
+ * as zeros, larger ones as infinities.  A NaN in a token or a byte 255 of its exponents
+ * gives NaN in its outputs, a byte 255 of the weights' scales in the outputs of its rows.
  * The gradient of the activations is the same product with the transposed
  * weights and scales (128 x 128 blocks transpose onto blocks).
  */

@@ -76,3 +76,52 @@ def test_exponents_from_end_to_end(m, K, B, dtype, out):
         w, a = operands(m, K, B, dtype, seed)
         want = exact(w, a)
         assert torch.equal(lq.gemm8(w, a, out_dtype=out), want.float().to(out))
+
+
+def one_value(m, K, B, at, w_value, a_value, w_byte, a_byte, w_scale=None):
+    """A single position of every row and token that is not zero, in a block of those scales."""
+    w, a = torch.zeros(m, K), torch.zeros(B, K)
+    w[:, at], a[:, at] = w_value, a_value
+    we, ae = torch.full((-(-m // 128), K // 128), 127), torch.full((B, K // 128), 127)
+    we[:, at // 128], ae[:, at // 128] = w_byte, a_byte
+    scales = held(we)
+    if w_scale is not None:
+        scales = torch.ones(we.shape, device="cuda")
+        scales[:, at // 128] = w_scale
+    return lq.Blocks8(w.to(E4M3).cuda(), scales), lq.Rows8(a.to(E4M3).cuda(), held(ae))
+
+
+@pytest.mark.parametrize("out", [F16, BF16, F32])
+@pytest.mark.parametrize("m,B", [(256, 1), (256, 3), (256, 300), (129, 21760), (4096, 2048), (4096, 4000)])
+def test_the_byte_255_is_a_nan(m, B, out):
+    """In the outputs that read the block, and in no others; also where the block's values are zeros."""
+    K = 384
+    for value in (1.0, 0.0):
+        w, a = one_value(m, K, B, 200, value, value, 127, 127)
+        clean = lq.gemm8(w, a, out_dtype=out)
+        w.scales[m // 128 - 1, 1] = 255
+        got = lq.gemm8(w, a, out_dtype=out)
+        lo = (m // 128 - 1) * 128
+        hit = (torch.arange(m, device="cuda") >= lo) & (torch.arange(m, device="cuda") < lo + 128)
+        assert torch.isnan(got[:, hit]).all() and torch.equal(got[:, ~hit], clean[:, ~hit])
+        w.scales[m // 128 - 1, 1] = 127
+        a.exps[B - 1, 1] = 255
+        got = lq.gemm8(w, a, out_dtype=out)
+        assert torch.isnan(got[B - 1]).all() and torch.equal(got[:B - 1], clean[:B - 1])
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("B", [1, 3, 300, 4000])
+def test_float32_scales_of_any_size(B, out):
+    """Both signs, near the ends of float32, infinities and NaN.  The block's sum before its scale is a float32 number:
+    exact here, so one rounding for the scale and one for the output."""
+    for scale, value, byte in ((2.0**-120, 3.0, 245), (2.0**120, 3.0, 6), (-3e38, 1.5, 10), (1.2e-38, 448.0, 200), (0.0, 5.0, 127),
+                               (1.7e38, 0.001953125, 127), (-1e-30, 448.0, 230)):
+        w, a = one_value(256, 384, B, 130, value, 1.0, 127, byte, scale)
+        want = torch.tensor(scale).double().item() * value * 2.0**(byte - 127)
+        got = lq.gemm8(w, a, out_dtype=out).double()
+        assert ((got - want).abs() <= (2.0**-24 + torch.finfo(out).eps / 2 * 1.001) * abs(want)).all()
+    w, a = one_value(256, 384, B, 130, 2.0, 1.0, 127, 127, float("inf"))
+    assert (lq.gemm8(w, a, out_dtype=out) == float("inf")).all()
+    w, a = one_value(256, 384, B, 130, 2.0, 1.0, 127, 127, float("nan"))
+    assert torch.isnan(lq.gemm8(w, a, out_dtype=out)).all()
