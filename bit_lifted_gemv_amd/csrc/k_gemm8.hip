@@ -363,8 +363,11 @@ gemm8_kernel(F8Product p) {
   // ---- the end: AT_ONCE token tiles at a time through the wave's own part of LDS, [token][row],
   // so that its stores are whole runs and its code short (unrolled over all the sums it would be
   // 100 KB, fetched once per tile: 15 us of each).  Without a residual no load stands between
-  // the stores: a wait for one is a wait for the stores before it.  The large tiles' outputs are
-  // more than the caches hold and pass them by (4096 x 4096 -> 28672: 446 to 410 us).
+  // the stores: a wait for one is a wait for the stores before it.  Tiles of 256 rows store past
+  // the caches, which their operands need: outputs from 12 MB, the smallest that take these tiles
+  // (1664 x 4096 -> 4096, 14 MB: 37.2 us, plain stores 38.4; 512 tokens to 8 of 64 experts 84 and
+  // 90; 4096 x 4096 -> 28672, 235 MB: 434 and 443), also where lq_quant8 reads the output next
+  // (both calls: 40.7 and 41.4; 93 and 96; 495 and 502; nothing at 117 MB, 447 and 446).
   constexpr bool STREAM = ROWS > 128;
   constexpr int PITCH = P::PITCH, AT_ONCE = P::AT_ONCE, MASKS = (LAST + 3) / 4, G = 4;
   const int wave_token = wt * 16 * FT + (WK == 2 && wk ? 16 * LAST : 0);

@@ -20,8 +20,9 @@ typedef i32x4 i32x4_any __attribute__((aligned(1)));
 
 // ------------------------------------------------------------------ sort
 // A wave per row, 16 bytes per lane, kAhead of them on their way, the rest of a
-// row byte by byte.  Stores past the caches: the rows are read next by another
-// kernel, on any XCD (32768 rows of 4 KB 37 us, 4.1 TB/s; with plain stores 45).
+// row byte by byte.  Stores past the caches, which leaves those to the tokens' rows, each
+// read k times: 32768 rows of 4 KB 37.0 us, plain stores 38.9; 65536 75 and 79, and with lq_quant8
+// reading them next 146 and 166; 8192 rows 9.7 and 10.1 (22.2 and 21.3), fewer no difference.
 constexpr int kAhead = 4;
 
 __global__ void __launch_bounds__(256) sort_rows_kernel(const uint8_t* __restrict__ x, int T,
