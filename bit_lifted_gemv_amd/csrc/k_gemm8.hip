@@ -45,6 +45,8 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // 64 lanes x 16 (or 4) bytes from resource r at voff + soff to LDS at `lds` (bytes).
+// m0 is the compiler's own and never allocated (it warns of it among the clobbers): each load sets it,
+// and no other instruction of the kernel reads it.
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t voff, const i32x4& r, uint32_t soff) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"

@@ -52,6 +52,8 @@ __device__ __forceinline__ f32x16 mfma(const i32x8& a, const i32x8& b, const f32
 }
 
 // 64 lanes x 16 bytes from resource r at voff + soff to LDS at `lds` (bytes).
+// m0 is the compiler's own and never allocated (it warns of it among the clobbers): each load sets it,
+// and no other instruction of the kernel reads it.
 __device__ __forceinline__ void load_to_lds(uint32_t lds, uint32_t voff, const i32x4& r,
                                             uint32_t soff) {
   asm volatile(
