@@ -31,6 +31,13 @@ lq_status check_quant(const void* x, lq_dtype dtype, int64_t K, int64_t ld) {
   return LQ_OK;
 }
 
+// Outputs over the values that other workgroups still read.
+lq_status check_quant_out(const void* x, const void* q, const void* exps) {
+  if (!x || !q || !exps) return fail(LQ_ERR_NULL, "null pointer");
+  if (q == x || exps == x) return fail(LQ_ERR_UNSUPPORTED, "q or exps overlaps the input");
+  return LQ_OK;
+}
+
 // ---- the products
 struct Plan8 {
   bool few;                    // on the few-row kernel
@@ -232,7 +239,8 @@ lq_status lq_quant8(const void* x, lq_dtype dtype, int64_t rows, int64_t K, int6
   if (st == LQ_OK) st = check_rows8("outputs", q, K, ldq, exps, lde);
   if (st != LQ_OK) return st;
   if (rows == 0) return ok();
-  if (!x || !q || !exps) return fail(LQ_ERR_NULL, "null pointer");
+  st = check_quant_out(x, q, exps);
+  if (st != LQ_OK) return st;
   return hip_status(lq::launch_quant8(x, dtype, rows, K, ld, static_cast<uint8_t*>(q), q_dtype, ldq,
                                       exps, lde, as_stream(stream)),
                     "lq_quant8 launch");
@@ -246,8 +254,8 @@ lq_status lq_quant8_blocks(const void* w, lq_dtype dtype, int64_t E, int64_t m, 
     return fail(LQ_ERR_SHAPE, "E=%lld (1..1024) m=%lld (1..2^22)", (long long)E, (long long)m);
   lq_status st = check_quant(w, dtype, K, ld);
   if (st == LQ_OK) st = check_rows8("outputs", q, K, ldq, exps, lde);
+  if (st == LQ_OK) st = check_quant_out(w, q, exps);
   if (st != LQ_OK) return st;
-  if (!w || !q || !exps) return fail(LQ_ERR_NULL, "null pointer");
   return hip_status(lq::launch_quant8_blocks(w, dtype, E, m, K, ld, static_cast<uint8_t*>(q), ldq,
                                              exps, lde, as_stream(stream)),
                     "lq_quant8_blocks launch");
