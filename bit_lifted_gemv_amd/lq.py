@@ -995,7 +995,7 @@ def sort_rows(x, rows: torch.Tensor, out=None, stream=None):
         exps = held.exps
         if exps is None:
             exps = _exponents((rows.shape[0], x.exps.shape[1]), x.exps.device)
-        return Rows8(sort_rows(x.values, rows, held.values), sort_rows(x.exps, rows, exps))
+        return Rows8(sort_rows(x.values, rows, held.values, stream), sort_rows(x.exps, rows, exps, stream))
     T, n = x.shape
     R, dev = rows.shape[0], x.device
     _on_gpu(x)
