@@ -42,10 +42,15 @@ __device__ __forceinline__ void wait_lds_and_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
 }
 
-template <int AK, bool PREC, int WF>
+// FS: float32 scales, where activations are held (one bfloat16 token x 4096 -> 8192 11.4 us, 12.4 where the
+// kernel asks p.float_scales; four x 4096 -> 1024 10.6 and 11.4; one x 8192 -> 8192 22.2 and 21.6).  Others ask:
+// the branch keeps a block's loads behind the products before them (one e4m3 token x 8192 -> 8192 19.9 us, 20.9
+// without it; x 28672 47.5 and 49.2; x 4096 -> 28672 25.6 and 25.8).
+template <int AK, bool FS, bool PREC, int WF>
 __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
   constexpr bool HELD = AK == LQ_F16 || AK == LQ_BF16;   // 16-bit activations
   constexpr int AT = HELD ? LQ_E4M3 : AK;                // of the operand
+  const bool float_scales = HELD ? FS : p.float_scales;
   constexpr int TOK = kFewTokens, ROWS = 16 * WF, PITCH = ROWS + 4;
   constexpr int U = WF == 1 ? (HELD ? 8 : 4) : WF == 2 || HELD ? 4 : 2;   // blocks of positions on their way
   extern __shared__ __align__(16) float lds[];
@@ -76,7 +81,7 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
     }
     wrow[f] = p.w + expert * p.w_matrix + row * p.ldw + 16 * g;
     srow[f] = static_cast<const uint8_t*>(p.scales) +
-              (expert * p.scales_matrix + row / 128 * p.lds) * (p.float_scales ? 4 : 1);
+              (expert * p.scales_matrix + row / 128 * p.lds) * (float_scales ? 4 : 1);
   }
   auto source_row = [&](int token) {
     int r = row0 + min(token, tokens - 1);
@@ -108,7 +113,7 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
       const uint4* from = reinterpret_cast<const uint4*>(wrow[f] + at * 128);
       wv[u][f][0] = from[0];
       wv[u][f][1] = from[4];
-      sv[u][f] = p.float_scales ? reinterpret_cast<const uint32_t*>(srow[f])[at] : srow[f][at];
+      sv[u][f] = float_scales ? reinterpret_cast<const uint32_t*>(srow[f])[at] : srow[f][at];
     }
     if constexpr (!HELD) {
       const uint4* from = reinterpret_cast<const uint4*>(arow + at * 128);
@@ -181,16 +186,16 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
     for (int f = 0; f < WF; ++f) {
       const i32x8 b = words(wv[u][f][0], wv[u][f][1]);
       // a power of two goes into the products (a block's sum without it may leave float32's range)
-      const float scale = p.float_scales ? __uint_as_float(sv[u][f]) : 1.f;
+      const float scale = float_scales ? __uint_as_float(sv[u][f]) : 1.f;
       f32x4 z = {};
       if constexpr (PREC) {
-        const float power = p.float_scales ? 1.f : power_of_two(sv[u][f]);
+        const float power = float_scales ? 1.f : power_of_two(sv[u][f]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               wide[i], widen8<LQ_E4M3>(b[2 * i], b[2 * i + 1], power), z, 0, 0, 0);
       } else {
-        const int byte = p.float_scales ? 127 : static_cast<int>(sv[u][f]);
+        const int byte = float_scales ? 127 : static_cast<int>(sv[u][f]);
         z = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, AT == LQ_E5M2 ? 1 : 0, 0, 0, e, 0, byte);
       }
       acc[f] += z * scale;
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(512) gemv8_kernel(F8Product p) {
   }
 }
 
-template <int AK, bool PREC, int WF>
+template <int AK, bool FS, bool PREC, int WF>
 hipError_t launch(const F8Product& in, const F8FewPlan& plan, hipStream_t st) {
   F8Product p = in;
   const int64_t tok = kFewTokens, outs = p.gated ? 8 * WF : 16 * WF, out_m = p.gated ? p.m / 2 : p.m;
@@ -271,7 +276,7 @@ hipError_t launch(const F8Product& in, const F8FewPlan& plan, hipStream_t st) {
   // the sums, in the place of the held activations: at most 34 KB of eight waves, and 17 KB
   int64_t bytes = plan.waves * tok * (16 * WF + 4) * 4;
   if ((AK == LQ_F16 || AK == LQ_BF16) && plan.held_bytes > bytes) bytes = plan.held_bytes;
-  auto* k = gemv8_kernel<AK, PREC, WF>;
+  auto* k = gemv8_kernel<AK, FS, PREC, WF>;
   // a launch has fewer than 2^32 threads
   const int64_t most = (int64_t{1} << 31) / threads;
   for (int64_t b = 0; b < blocks; b += most) {
@@ -283,16 +288,19 @@ hipError_t launch(const F8Product& in, const F8FewPlan& plan, hipStream_t st) {
   return hipSuccess;
 }
 
-template <int AK, bool PREC>
+template <int AK, bool FS, bool PREC>
 hipError_t by_shape(const F8Product& p, const F8FewPlan& plan, hipStream_t st) {
-  return plan.wf == 1   ? launch<AK, PREC, 1>(p, plan, st)
-         : plan.wf == 2 ? launch<AK, PREC, 2>(p, plan, st)
-                        : launch<AK, PREC, 4>(p, plan, st);
+  return plan.wf == 1   ? launch<AK, FS, PREC, 1>(p, plan, st)
+         : plan.wf == 2 ? launch<AK, FS, PREC, 2>(p, plan, st)
+                        : launch<AK, FS, PREC, 4>(p, plan, st);
 }
 
 template <int AK>
-hipError_t by_precision(const F8Product& p, const F8FewPlan& plan, bool precise, hipStream_t st) {
-  return precise ? by_shape<AK, true>(p, plan, st) : by_shape<AK, false>(p, plan, st);
+hipError_t by_scales(const F8Product& p, const F8FewPlan& plan, bool precise, hipStream_t st) {
+  if constexpr (AK == LQ_F16 || AK == LQ_BF16) {
+    if (p.float_scales) return precise ? by_shape<AK, true, true>(p, plan, st) : by_shape<AK, true, false>(p, plan, st);
+  }
+  return precise ? by_shape<AK, false, true>(p, plan, st) : by_shape<AK, false, false>(p, plan, st);
 }
 
 }  // namespace
@@ -333,10 +341,10 @@ F8FewPlan few_f8_plan(int64_t E, int64_t m, int64_t K, int64_t R, bool gated, bo
 hipError_t launch_gemv8(const F8Product& p, int a_type, const F8FewPlan& plan, bool precise,
                         hipStream_t st) {
   switch (a_type) {
-    case LQ_E4M3: return by_precision<LQ_E4M3>(p, plan, precise, st);
-    case LQ_E5M2: return by_precision<LQ_E5M2>(p, plan, precise, st);
-    case LQ_F16: return by_precision<LQ_F16>(p, plan, precise, st);
-    default: return by_precision<LQ_BF16>(p, plan, precise, st);
+    case LQ_E4M3: return by_scales<LQ_E4M3>(p, plan, precise, st);
+    case LQ_E5M2: return by_scales<LQ_E5M2>(p, plan, precise, st);
+    case LQ_F16: return by_scales<LQ_F16>(p, plan, precise, st);
+    default: return by_scales<LQ_BF16>(p, plan, precise, st);
   }
 }
 
