@@ -9,7 +9,9 @@
 // 13 places below the largest sum of two factors' exponents: 2^-16 of a typical result,
 // 2^-14.5 with outlying positions, where the 16-bit results round by up to 2^-11 or 2^-8.
 // For float32 results (PREC) the operands become bfloat16 (exact, and the powers of two
-// go in) and v_mfma_f32_16x16x32_bf16 keeps 24 bits.
+// go in) and v_mfma_f32_16x16x32_bf16 keeps 24 bits; for 16-bit results too that would cost
+// 0 to 4 % (x 4096 -> 2 x 14336: one token 25.5 and 26.5 us, 16 tokens 28.1 and 28.8; 4096 x
+// 4096 11.2 and 11.2) for an error that their rounding hides.
 //
 // Bound by reading the weights: nothing of them passes through LDS.  A wave
 // takes WF x 16 rows and up to 16 tokens, each lane loads two 16-byte pieces of
@@ -20,8 +22,8 @@
 //
 // HELD: 16-bit activations of few tokens are quantized on the way to LDS (lq_quant8's
 // result bit for bit), behind the first loads of weights, which saves the launch that
-// does it (about 4.7 us): 4096 x 4096, one token, 9.5 us (8-bit ones straight from memory
-// 8.8), four tokens 12.9 (9.2); 28672 positions of one token would cost 51 (42).
+// does it (about 4.7 us): 4096 x 4096, one token, 9.3 us (8-bit ones straight from memory
+// 7.5), four tokens 12.8 (8.2); 28672 positions of one token would cost 51 (42).
 #include "f6_epilogue.h"
 #include "f6_product.h"
 #include "f8.h"

@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(256) quant8_rows_kernel(const void* __restrict
 }
 
 // Blocks: a workgroup per 128 x 128 block, eight rows of 16 lanes at a time per
-// two waves.
+// two waves.  Bound by memory: 28672 x 4096 float32 103 us (5.7 TB/s), bfloat16 67 (5.25), 64
+// experts of 2816 x 2048 bfloat16 206 (5.4).
 template <int DT>
 __global__ void __launch_bounds__(256) quant8_blocks_kernel(const void* __restrict__ w, int m,
                                                             int64_t K, int64_t ld,
